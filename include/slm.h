@@ -247,7 +247,9 @@ SLM_API int slm_set_backward_mode(int mode);
 #define SLM_TRACE_BWD_FUSED 5    /* the persistent fused backward (dZ, dH, dW together)  */
 #define SLM_TRACE_LOGITS_ROW 6   /* row kernels over kept logits (slm_loss_fwd_bwd)      */
 #define SLM_TRACE_ROW 7          /* combines, reductions, counts, alignment              */
-#define SLM_TRACE_CLASSES 8
+#define SLM_TRACE_NORM 8         /* block norms, forward and backward                    */
+#define SLM_TRACE_ORTH 9         /* the orthogonalised update                            */
+#define SLM_TRACE_CLASSES 10
 SLM_API int slm_trace_enable(int on);
 SLM_API int slm_trace_read(double* ms, int64_t* launches, int n_classes);
 
@@ -344,6 +346,67 @@ SLM_API int slm_align_labels(const int32_t* tokens, const uint8_t* loss_mask,
 SLM_API size_t slm_flatness_workspace_bytes(int64_t N, int64_t d, int64_t V);
 SLM_API int slm_target_flatness(const void* Hp, const void* W, int64_t N, int64_t d, int64_t V,
                                 float* flat, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Either side of the loss in a training step: the norms of the block that makes the hidden
+ * states, and the orthogonalised update made of a weight's gradient.  The pages define no
+ * counterpart; the formulas are given here.
+ * ------------------------------------------------------------------------------------- */
+typedef enum slm_dtype { SLM_BF16 = 0, SLM_F16 = 1, SLM_F32 = 2 } slm_dtype;
+
+/* Norm after a block, its gate, the scaled residual add, and the norm before the next block
+ * (or before the LM head), in one pass over the rows.  Per row n of d channels, with
+ * norm(t) = t / sqrt(mean(t^2) + eps):
+ *     v = norm(y) (w_post + weight_offset)                 (v = y when w_post is NULL)
+ *     r = residual_scale x + block_scale gate v            (no gate factor when gate is NULL)
+ *     h = norm(r) (w_pre + weight_offset)                  (not made when w_pre is NULL)
+ *   dtype     slm_dtype of x, y, residual and hidden.
+ *   x, y      [N, d] with ldx / ldy elements from row to row (>= d; rows must not overlap);
+ *             y may be NULL: then r = residual_scale x, and w_post and gate must be NULL.
+ *   w_post, w_pre  [d], of type w_dtype: dtype itself or SLM_F32.  Either may be NULL, not
+ *             both of y and w_pre.
+ *   gate      [gate_rows, d] contiguous, of type gate_dtype (dtype or SLM_F32), or NULL (then
+ *             gate_rows is ignored): row n uses gate row n / (N / gate_rows), so 1 is a gate
+ *             per channel, the batch size a gate per sequence, N a gate per token.  gate_rows
+ *             must divide N.
+ *   residual  [N, d] contiguous, r rounded to dtype; may be NULL, and may be x itself (ldx = d),
+ *             which is then updated in place; no other overlap of outputs and inputs.
+ *   hidden    [N, d] contiguous, h (made from r before r's rounding); required with w_pre.
+ *   rstd_post, rstd_pre  float [N], the norms' factors 1 / sqrt(mean + eps), which the backward
+ *             takes; may be NULL.
+ * All arithmetic is fp32, rounded once per output.  Every alignment and width is accepted;
+ * rows that start on 16-byte boundaries and widths of whole 16-byte pieces run fastest.
+ * Returns SLM_ERR_KIND for an unknown type, SLM_ERR_SHAPE for bad sizes, strides, gate_rows, a
+ * scale that is not finite or eps <= 0, SLM_ERR_NULL for a missing or unusable pointer and
+ * SLM_ERR_ALIGN for a pointer that is not aligned to its element type. */
+SLM_API int slm_block_norm_fwd(int dtype, const void* x, int64_t ldx, const void* y, int64_t ldy,
+                               const void* w_post, const void* w_pre, int w_dtype,
+                               const void* gate, int gate_dtype, int64_t gate_rows, int64_t N,
+                               int64_t d, float residual_scale, float block_scale, float eps,
+                               float weight_offset, void* residual, void* hidden,
+                               float* rstd_post, float* rstd_pre, void* stream);
+
+/* Backward of slm_block_norm_fwd for the same inputs.
+ *   d_residual, d_hidden  gradients of r and h, of type dtype, with row strides ld_dr / ld_dh.
+ *             d_residual may be NULL (zero); d_hidden is required exactly when w_pre is given.
+ *   rstd_post, rstd_pre  as the forward wrote them (required with w_post / w_pre).
+ *   dx, dy    [N, d] contiguous, of type dtype; dy required with y.  Neither may overlap an input.
+ *   dgate     [gate_rows, d] of type gate_dtype, summed over the rows that share a gate row;
+ *             required with gate.
+ *   dw_post, dw_pre  float [d], overwritten; required with the weights (zero when N = 0).
+ *   workspace at least slm_block_norm_workspace_bytes(N, d, gate_rows) bytes (gate_rows = 0
+ *             without a gate), 256-byte aligned.
+ * The sums over rows are taken in a fixed order: the same inputs give the same bits. */
+SLM_API size_t slm_block_norm_workspace_bytes(int64_t N, int64_t d, int64_t gate_rows);
+SLM_API int slm_block_norm_bwd(int dtype, const void* x, int64_t ldx, const void* y, int64_t ldy,
+                               const void* w_post, const void* w_pre, int w_dtype,
+                               const void* gate, int gate_dtype, int64_t gate_rows,
+                               const void* d_residual, int64_t ld_dr, const void* d_hidden,
+                               int64_t ld_dh, const float* rstd_post, const float* rstd_pre,
+                               int64_t N, int64_t d, float residual_scale, float block_scale,
+                               float weight_offset, void* dx, void* dy, void* dgate,
+                               float* dw_post, float* dw_pre, void* workspace, size_t ws_bytes,
+                               void* stream);
 
 /* Test hook for the device-side failure path (not for production use).  fault_mode 1 makes
  * every following launch withhold one internal pipeline release, so that a bounded wait in

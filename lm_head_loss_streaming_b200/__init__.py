@@ -18,6 +18,9 @@ def __getattr__(name):
                 "lm_head_loss_bwd"):
         from . import loss as _loss
         return getattr(_loss, name)
+    if name in ("block_norm", "block_norm_fwd", "block_norm_bwd"):
+        from . import norms as _norms
+        return getattr(_norms, name)
     if name == "lib":
         from . import _lib
         return _lib

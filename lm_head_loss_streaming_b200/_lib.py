@@ -23,6 +23,8 @@ ALPHA_KINDS = (SLM_TV, SLM_NLA, SLM_LK_HYBRID)
 SLM_NUM_KINDS = 8
 SLM_COMBO_STATS = 9
 
+SLM_BF16, SLM_F16, SLM_F32 = 0, 1, 2
+
 SLM_OK = 0
 STATUS_NAMES = {
     0: "SLM_OK", 1: "SLM_ERR_NULL", 2: "SLM_ERR_SHAPE", 3: "SLM_ERR_ALIGN",
@@ -34,6 +36,7 @@ STATUS_NAMES = {
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
+_F32 = ctypes.c_float
 _INT = ctypes.c_int
 _SZ = ctypes.c_size_t
 SIGNATURES = {
@@ -67,13 +70,19 @@ SIGNATURES = {
     "slm_count_valid": (_INT, [_INT, _P, _I32, _I64, _I64, _P, _P]),
     "slm_set_backward_mode": (_INT, [_INT]),
     "slm_debug_exp2": (_INT, [_P, _P, _P, _I64, _P]),
+    "slm_block_norm_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "slm_block_norm_fwd": (_INT, [_INT, _P, _I64, _P, _I64, _P, _P, _INT, _P, _INT, _I64, _I64,
+                                  _I64, _F32, _F32, _F32, _F32, _P, _P, _P, _P, _P]),
+    "slm_block_norm_bwd": (_INT, [_INT, _P, _I64, _P, _I64, _P, _P, _INT, _P, _INT, _I64, _P,
+                                  _I64, _P, _I64, _P, _P, _I64, _I64, _F32, _F32, _F32, _P, _P,
+                                  _P, _P, _P, _P, _SZ, _P]),
     "slm_trace_enable": (_INT, [_INT]),
     "slm_trace_read": (_INT, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_I64), _INT]),
 }
 
 # Kernel classes of slm_trace_read, in order.
 TRACE_CLASSES = ("fwd_gemm", "pass2_gemm", "dz_gemm", "dh_gemm", "dw_gemm", "bwd_fused",
-                 "logits_row", "row")
+                 "logits_row", "row", "norm", "orth")
 
 
 class SLMError(RuntimeError):
@@ -239,6 +248,20 @@ def slm_flatness_workspace_bytes(N, d, V):
 def slm_target_flatness(Hp, W, N, d, V, flat, workspace, ws_bytes, stream):
     return load().slm_target_flatness(Hp, W, int(N), int(d), int(V), flat, workspace,
                                       int(ws_bytes), stream)
+
+
+def slm_block_norm_workspace_bytes(N, d, gate_rows=0):
+    return load().slm_block_norm_workspace_bytes(int(N), int(d), int(gate_rows))
+
+
+def slm_block_norm_fwd(*args):
+    """Arguments as declared in ``include/slm.h``, in order."""
+    return load().slm_block_norm_fwd(*args)
+
+
+def slm_block_norm_bwd(*args):
+    """Arguments as declared in ``include/slm.h``, in order."""
+    return load().slm_block_norm_bwd(*args)
 
 
 def slm_count_valid(kind, labels, ignore_index, N, V, n_valid, stream):

@@ -42,7 +42,9 @@ enum TraceClass : int {
   kTrBwdFused = 5,   // the persistent fused backward (dZ, dH and dW in one launch)
   kTrLogitsRow = 6,  // row kernels over kept logits (fused single call)
   kTrRow = 7,        // combines, reductions, counts, alignment
-  kTraceClasses = 8
+  kTrNorm = 8,       // block norms
+  kTrOrth = 9,       // the orthogonalised update
+  kTraceClasses = 10
 };
 constexpr int kMaxReserveSms = 128;  // slm_loss_bwd_overlap's reserve_sms, at most
 constexpr long long kTimeoutCycles = 4000000000LL;  // ~2 s at the B200's boost clock
@@ -397,6 +399,50 @@ FusedLayout fused_layout(int kind, int64_t N, int64_t V, int64_t chunk_tokens) {
   off = align_up(off + C * L.ldz * 2, kAlign);
   L.total = off;
   return L;
+}
+
+// Block norms.
+bool valid_dtype(int t) { return t >= SLM_BF16 && t <= SLM_F32; }
+size_t elem_bytes(int t) { return t == SLM_F32 ? 4 : 2; }
+bool finite(float v) { return v == v && v <= 3.4e38f && v >= -3.4e38f; }
+
+struct NormLayout {
+  size_t c1_off, post_off, pre_off, gate_off, total;
+};
+
+NormLayout norm_layout(int64_t N, int64_t d, int64_t gate_rows) {
+  NormLayout L{};
+  const NormPlan q = norm_plan(std::max<int64_t>(N, 1), gate_rows > 0 ? N / gate_rows : 1,
+                               gate_rows > 0);
+  const size_t part = align_up(static_cast<size_t>(q.blocks) * d * sizeof(float), kAlign);
+  L.c1_off = 0;
+  L.post_off = align_up(static_cast<size_t>(N) * sizeof(float), kAlign);
+  L.pre_off = L.post_off + part;
+  L.gate_off = L.pre_off + part;
+  L.total = L.gate_off + (q.shared_gate && q.slices > 1 ? part : 0) + kAlign;
+  return L;
+}
+
+int norm_checks(int dtype, const void* x, int64_t ldx, const void* y, int64_t ldy,
+                const void* w_post, const void* w_pre, int w_dtype, const void* gate,
+                int gate_dtype, int64_t gate_rows, int64_t N, int64_t d, float residual_scale,
+                float block_scale, float weight_offset) {
+  if (!valid_dtype(dtype)) return SLM_ERR_KIND;
+  if ((w_post || w_pre) && w_dtype != dtype && w_dtype != SLM_F32) return SLM_ERR_KIND;
+  if (gate && gate_dtype != dtype && gate_dtype != SLM_F32) return SLM_ERR_KIND;
+  if (N < 0 || d <= 0 || N >= (int64_t(1) << 31) || d >= (int64_t(1) << 31)) return SLM_ERR_SHAPE;
+  if (!finite(residual_scale) || !finite(block_scale) || !finite(weight_offset))
+    return SLM_ERR_SHAPE;
+  if (N > 0) {
+    if (!x || (!y && (w_post || gate || !w_pre))) return SLM_ERR_NULL;
+    if (ldx < d || (y && ldy < d)) return SLM_ERR_SHAPE;
+    if (gate && (gate_rows <= 0 || gate_rows > N || N % gate_rows != 0)) return SLM_ERR_SHAPE;
+  }
+  const size_t e = elem_bytes(dtype);
+  if (misaligned(x, e) || misaligned(y, e) || misaligned(w_post, elem_bytes(w_dtype)) ||
+      misaligned(w_pre, elem_bytes(w_dtype)) || misaligned(gate, elem_bytes(gate_dtype)))
+    return SLM_ERR_ALIGN;
+  return SLM_OK;
 }
 
 #define SLM_TRY_CUDA(expr)                  \
@@ -968,6 +1014,85 @@ int slm_combo_bwd(const float* weights, const void* Hq, const void* Hp, const vo
                               SLM_SYNC_KB_B, SLM_SYNC_SLACK_B);
     SLM_LAUNCH(kTrDwGemm, launch_dw(tDz_mn, tH_mn, gw, pw, ctl, s));
   }
+  return SLM_OK;
+}
+
+size_t slm_block_norm_workspace_bytes(int64_t N, int64_t d, int64_t gate_rows) {
+  if (N < 0 || d <= 0 || gate_rows < 0 || N >= (int64_t(1) << 31) || d >= (int64_t(1) << 31))
+    return 0;
+  if (gate_rows > 0 && (gate_rows > N || N % gate_rows != 0)) return 0;
+  return norm_layout(N, d, gate_rows).total;
+}
+
+int slm_block_norm_fwd(int dtype, const void* x, int64_t ldx, const void* y, int64_t ldy,
+                       const void* w_post, const void* w_pre, int w_dtype, const void* gate,
+                       int gate_dtype, int64_t gate_rows, int64_t N, int64_t d,
+                       float residual_scale, float block_scale, float eps, float weight_offset,
+                       void* residual, void* hidden, float* rstd_post, float* rstd_pre,
+                       void* stream) {
+  int st = norm_checks(dtype, x, ldx, y, ldy, w_post, w_pre, w_dtype, gate, gate_dtype, gate_rows,
+                       N, d, residual_scale, block_scale, weight_offset);
+  if (st != SLM_OK) return st;
+  if (!finite(eps) || eps <= 0.f) return SLM_ERR_SHAPE;
+  if (N == 0) return SLM_OK;
+  if ((w_pre && !hidden) || (!w_pre && !residual)) return SLM_ERR_NULL;
+  const size_t e = elem_bytes(dtype);
+  if (misaligned(residual, e) || misaligned(hidden, e) || misaligned(rstd_post, 4) ||
+      misaligned(rstd_pre, 4))
+    return SLM_ERR_ALIGN;
+  if (residual == x && ldx != d) return SLM_ERR_SHAPE;
+  if ((st = check_device()) != SLM_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const NormFwd p{x, y, w_post, w_pre, gate, ldx, ldy, N, d, gate ? N / gate_rows : 1,
+                  w_dtype == SLM_F32, gate_dtype == SLM_F32, residual_scale, block_scale, eps,
+                  weight_offset, residual, w_pre ? hidden : nullptr, rstd_post, rstd_pre};
+  SLM_LAUNCH(kTrNorm, launch_norm_fwd(dtype, p, s));
+  return SLM_OK;
+}
+
+int slm_block_norm_bwd(int dtype, const void* x, int64_t ldx, const void* y, int64_t ldy,
+                       const void* w_post, const void* w_pre, int w_dtype, const void* gate,
+                       int gate_dtype, int64_t gate_rows, const void* d_residual, int64_t ld_dr,
+                       const void* d_hidden, int64_t ld_dh, const float* rstd_post,
+                       const float* rstd_pre, int64_t N, int64_t d, float residual_scale,
+                       float block_scale, float weight_offset, void* dx, void* dy, void* dgate,
+                       float* dw_post, float* dw_pre, void* workspace, size_t ws_bytes,
+                       void* stream) {
+  int st = norm_checks(dtype, x, ldx, y, ldy, w_post, w_pre, w_dtype, gate, gate_dtype, gate_rows,
+                       N, d, residual_scale, block_scale, weight_offset);
+  if (st != SLM_OK) return st;
+  if ((w_post && !dw_post) || (w_pre && !dw_pre)) return SLM_ERR_NULL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (N == 0) {
+    if ((st = check_device()) != SLM_OK) return st;
+    if (w_post) SLM_TRY_CUDA(cudaMemsetAsync(dw_post, 0, d * sizeof(float), s));
+    if (w_pre) SLM_TRY_CUDA(cudaMemsetAsync(dw_pre, 0, d * sizeof(float), s));
+    return SLM_OK;
+  }
+  if (!dx || (y && !dy) || (gate && !dgate) || (w_pre && !d_hidden) || (!w_pre && d_hidden) ||
+      (!d_hidden && !d_residual) || (w_post && !rstd_post) || (w_pre && !rstd_pre) || !workspace)
+    return SLM_ERR_NULL;
+  if ((d_residual && ld_dr < d) || (d_hidden && ld_dh < d)) return SLM_ERR_SHAPE;
+  const size_t e = elem_bytes(dtype);
+  if (misaligned(d_residual, e) || misaligned(d_hidden, e) || misaligned(dx, e) ||
+      misaligned(dy, e) || misaligned(dgate, elem_bytes(gate ? gate_dtype : SLM_BF16)) ||
+      misaligned(rstd_post, 4) || misaligned(rstd_pre, 4) || misaligned(dw_post, 4) ||
+      misaligned(dw_pre, 4))
+    return SLM_ERR_ALIGN;
+  const NormLayout L = norm_layout(N, d, gate ? gate_rows : 0);
+  if (misaligned(workspace, kAlign) || ws_bytes < L.total) return SLM_ERR_WORKSPACE;
+  if ((st = check_device()) != SLM_OK) return st;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const int64_t per = gate ? N / gate_rows : 1;
+  const NormBwd p{x, y, w_post, w_pre, gate, d_residual, d_hidden, ldx, ldy, ld_dr, ld_dh, N, d,
+                  per, w_dtype == SLM_F32, gate_dtype == SLM_F32, residual_scale, block_scale,
+                  weight_offset, rstd_post, rstd_pre, dx, dy, dgate, dw_post, dw_pre,
+                  norm_plan(N, per, gate != nullptr),
+                  reinterpret_cast<float*>(ws + L.c1_off),
+                  reinterpret_cast<float*>(ws + L.post_off),
+                  reinterpret_cast<float*>(ws + L.pre_off),
+                  reinterpret_cast<float*>(ws + L.gate_off)};
+  SLM_LAUNCH(kTrNorm, launch_norm_bwd(dtype, p, s));
   return SLM_OK;
 }
 

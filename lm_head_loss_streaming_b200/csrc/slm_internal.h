@@ -236,6 +236,69 @@ cudaError_t launch_finalize(const double* blk_sum, const long long* blk_cnt, int
                             cudaStream_t s);
 cudaError_t launch_zero_f32(float* p, int64_t n, cudaStream_t s);
 
+// ---- Block norm (slm_norm.cu): element types 0 = bf16, 1 = fp16, 2 = fp32. ----
+// How the rows of a backward are divided: blocks own either one of `slices` slices of one
+// group (rows that share a gate row; everything is one group without a shared gate), or, when
+// there are at least as many groups as blocks, several whole groups.
+constexpr int kNormBlocks = 296;
+struct NormPlan {
+  int64_t rows;    // rows per group
+  int64_t groups;
+  int slices;      // slices per group
+  int blocks;
+  bool shared_gate;
+};
+struct NormRows {
+  int64_t g0, g1, rows;
+  int64_t lo, hi;  // rows of each group that the block owns
+  __host__ __device__ int64_t begin(int64_t g) const { return g * rows + lo; }
+  __host__ __device__ int64_t end(int64_t g) const { return g * rows + hi; }
+};
+__host__ __device__ inline NormRows norm_rows(const NormPlan& q, int b) {
+  NormRows r;
+  r.rows = q.rows;
+  if (q.slices > 1) {
+    const int s = b % q.slices;
+    r.g0 = b / q.slices;
+    r.g1 = r.g0 + 1;
+    r.lo = q.rows * s / q.slices;
+    r.hi = q.rows * (s + 1) / q.slices;
+  } else {
+    r.g0 = q.groups * b / q.blocks;
+    r.g1 = q.groups * (b + 1) / q.blocks;
+    r.lo = 0;
+    r.hi = q.rows;
+  }
+  return r;
+}
+// Plan for N >= 1 rows; rows_per_gate = 1 is a gate of its own for each row (not shared).
+NormPlan norm_plan(int64_t N, int64_t rows_per_gate, bool has_gate);
+
+struct NormFwd {
+  const void *x, *y, *w_post, *w_pre, *gate;
+  int64_t ldx, ldy;
+  int64_t N, d, rows_per_gate;
+  bool w_f32, gate_f32;
+  float residual_scale, block_scale, eps, weight_offset;
+  void *residual, *hidden;      // contiguous rows
+  float *rstd_post, *rstd_pre;  // [N]; may be NULL
+};
+struct NormBwd {
+  const void *x, *y, *w_post, *w_pre, *gate, *d_residual, *d_hidden;
+  int64_t ldx, ldy, ld_dr, ld_dh;
+  int64_t N, d, rows_per_gate;
+  bool w_f32, gate_f32;
+  float residual_scale, block_scale, weight_offset;
+  const float *rstd_post, *rstd_pre;
+  void *dx, *dy, *dgate;
+  float *dw_post, *dw_pre;
+  NormPlan plan;
+  float* c1;                               // [N]
+  float *part_post, *part_pre, *part_gate;  // [plan.blocks][d] each
+};
+cudaError_t launch_norm_fwd(int dtype, const NormFwd& p, cudaStream_t s);
+cudaError_t launch_norm_bwd(int dtype, const NormBwd& p, cudaStream_t s);
+
 constexpr int kCombineThreads = 256;
 
 }  // namespace slm

@@ -1,0 +1,251 @@
+"""Norms before and after a draft block, fused with its gate and its residual scale.
+
+``block_norm`` makes, in one pass over the rows, the residual stream after a block and the
+normalised hidden states that the next block or ``streaming_lm_head_loss`` reads; its
+backward takes the gradient that the loss returns for them.  Through ``slm_block_norm_fwd``
+and ``slm_block_norm_bwd``.
+"""
+
+from __future__ import annotations
+
+from dataclasses import dataclass
+
+import torch
+
+from . import _lib
+from .loss import _ptr, _stream
+
+_DTYPE = {torch.bfloat16: _lib.SLM_BF16, torch.float16: _lib.SLM_F16,
+          torch.float32: _lib.SLM_F32}
+
+
+@dataclass
+class BlockNormResult:
+    residual: torch.Tensor            # [N, d], the inputs' type; x itself without y
+    hidden: torch.Tensor | None       # [N, d]; None without w_pre
+    rstd_post: torch.Tensor | None    # float32 [N]; None without w_post
+    rstd_pre: torch.Tensor | None     # float32 [N]; None without w_pre
+    residual_scale: float
+    block_scale: float
+    weight_offset: float
+
+
+@dataclass
+class BlockNormGrads:
+    dx: torch.Tensor                  # [N, d], the inputs' type
+    dy: torch.Tensor | None           # [N, d]
+    dgate: torch.Tensor | None        # the gate's shape and type
+    dw_pre: torch.Tensor | None       # float32 [d]
+    dw_post: torch.Tensor | None      # float32 [d]
+
+
+def _check_rows(name, t, shape, dtype, dev):
+    """Rows of ``shape`` on the current device, elements of a row adjacent, rows apart."""
+    if (not t.is_cuda or t.dtype != dtype or t.dim() != 2 or tuple(t.shape) != shape
+            or t.device.index != dev):
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {shape} on the current CUDA "
+                         f"device")
+    if t.stride(1) != 1 and shape[1] > 1 or (shape[0] > 1 and t.stride(0) < shape[1]):
+        raise ValueError(f"{name} must have adjacent channels and rows that do not overlap; its "
+                         f"strides are {t.stride()}")
+
+
+def _ld(t, d):
+    return d if t is None or t.shape[0] <= 1 else t.stride(0)
+
+
+def _check_block(x, y, w_pre, w_post, gate):
+    """Raises ValueError unless the inputs are what the kernels are told; returns
+    (N, d, dtype id, weight dtype id, gate dtype id, gate rows)."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.dtype not in _DTYPE:
+        raise ValueError("x must be a 2-D bf16, fp16 or fp32 CUDA tensor")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    dev = torch.cuda.current_device()
+    N, d = x.shape
+    if d < 1:
+        raise ValueError("x has rows of no channels")
+    _check_rows("x", x, (N, d), x.dtype, dev)
+    if y is None:
+        if w_post is not None or gate is not None:
+            raise ValueError("w_post and gate apply to y, which is missing")
+        if w_pre is None:
+            raise ValueError("nothing to do: neither y nor w_pre is given")
+    else:
+        _check_rows("y", y, (N, d), x.dtype, dev)
+    w = w_post if w_post is not None else w_pre
+    for name, t in (("w_post", w_post), ("w_pre", w_pre)):
+        if t is not None and (not t.is_cuda or t.device.index != dev or tuple(t.shape) != (d,)
+                              or not t.is_contiguous() or t.dtype != w.dtype
+                              or t.dtype not in (x.dtype, torch.float32)):
+            raise ValueError(f"{name} must be a contiguous tensor of shape ({d},) on the current "
+                             f"CUDA device, of {x.dtype} or float32 like the other weight")
+    rows = 0
+    if gate is not None:
+        if (not gate.is_cuda or gate.device.index != dev or gate.dim() not in (1, 2)
+                or gate.shape[-1] != d or not gate.is_contiguous()
+                or gate.dtype not in (x.dtype, torch.float32)):
+            raise ValueError(f"gate must be a contiguous tensor of shape ({d},) or (rows, {d}) on "
+                             f"the current CUDA device, of {x.dtype} or float32")
+        rows = 1 if gate.dim() == 1 else gate.shape[0]
+        if N > 0 and (rows == 0 or N % rows != 0):
+            raise ValueError(f"gate has {rows} rows; they must divide the {N} rows of x")
+    return (N, d, _DTYPE[x.dtype], _lib.SLM_F32 if w is None else _DTYPE[w.dtype],
+            _lib.SLM_F32 if gate is None else _DTYPE[gate.dtype], rows)
+
+
+def _overlap(a, b):
+    """Whether two tensors' address ranges meet."""
+    if a is None or b is None or a.numel() == 0 or b.numel() == 0:
+        return False
+
+    def span(t):
+        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+        return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+
+    (a0, a1), (b0, b1) = span(a), span(b)
+    return a0 < b1 and b0 < a1
+
+
+def _check_outputs(outs, ins, may_be=None):
+    """Caller-provided outputs overlap neither an input nor each other (``may_be``: the pair
+    (output, input) that may be the same tensor)."""
+    for i, (name, t) in enumerate(outs):
+        for other, u in list(ins) + outs[:i]:
+            if _overlap(t, u) and not (may_be == (name, other) and t.data_ptr() == u.data_ptr()
+                                       and u.is_contiguous()):
+                raise ValueError(f"{name} overlaps {other}")
+
+
+def block_norm_fwd(x, y=None, w_pre=None, w_post=None, gate=None, residual_scale=1.0,
+                   block_scale=1.0, eps=1e-6, weight_offset=0.0, residual=None, hidden=None
+                   ) -> BlockNormResult:
+    """Residual stream and normalised hidden states after a block, through
+    ``slm_block_norm_fwd``::
+
+        v        = norm(y) * (w_post + weight_offset)      (v = y without w_post)
+        residual = residual_scale * x + block_scale * gate * v
+        hidden   = norm(residual) * (w_pre + weight_offset)
+        norm(t)  = t / sqrt(mean(t^2) + eps)
+
+    ``x`` (the stream) and ``y`` (the block's output) are [N, d] bf16, fp16 or fp32 CUDA
+    tensors with adjacent channels; rows may be strided.  ``w_pre`` and ``w_post`` are [d],
+    ``gate`` [d] or [G, d] with G dividing N (each gate row covers N / G rows in a row: a gate
+    per channel, per sequence or per token), of the inputs' type or float32.  Without ``y``
+    only ``hidden`` is made, of ``x`` (residual_scale must be 1); without ``w_pre`` only the
+    residual.  ``residual`` and ``hidden`` may be preallocated contiguous outputs;
+    ``residual`` may be ``x`` itself, which is then updated in place (a backward needs the old
+    ``x``)."""
+    N, d, dt, wt, gt, rows = _check_block(x, y, w_pre, w_post, gate)
+    if y is None and residual_scale != 1.0:
+        raise ValueError("residual_scale needs y: without a block the stream is x itself")
+    if y is None and residual is not None:
+        raise ValueError("residual is an output of the block's add: there is none without y")
+    if w_pre is None and hidden is not None:
+        raise ValueError("hidden is made by the norm before the next block: there is no w_pre")
+    if not eps > 0:
+        raise ValueError("eps must be positive")
+    given = [(n, t) for n, t in (("residual", residual), ("hidden", hidden)) if t is not None]
+    if given:
+        for name, t in given:
+            _check_rows(name, t, (N, d), x.dtype, x.device.index)
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        _check_outputs(given, [("x", x), ("y", y), ("w_pre", w_pre), ("w_post", w_post),
+                               ("gate", gate)], ("residual", "x"))
+    if y is not None and residual is None:
+        residual = torch.empty(N, d, dtype=x.dtype, device=x.device)
+    if w_pre is not None and hidden is None:
+        hidden = torch.empty(N, d, dtype=x.dtype, device=x.device)
+    post = None if w_post is None else torch.empty(N, dtype=torch.float32, device=x.device)
+    pre = None if w_pre is None else torch.empty(N, dtype=torch.float32, device=x.device)
+    st = _lib.slm_block_norm_fwd(dt, _ptr(x), _ld(x, d), _ptr(y), _ld(y, d), _ptr(w_post),
+                                 _ptr(w_pre), wt, _ptr(gate), gt, rows, N, d, residual_scale,
+                                 block_scale, eps, weight_offset,
+                                 _ptr(residual) if y is not None else None, _ptr(hidden),
+                                 _ptr(post), _ptr(pre), _stream())
+    _lib.check(st, "slm_block_norm_fwd")
+    return BlockNormResult(x if y is None else residual, hidden, post, pre,
+                           float(residual_scale), float(block_scale), float(weight_offset))
+
+
+def block_norm_bwd(fwd: BlockNormResult, x, y=None, w_pre=None, w_post=None, gate=None,
+                   d_residual=None, d_hidden=None, workspace=None) -> BlockNormGrads:
+    """Gradients of ``block_norm_fwd`` for the same inputs, through ``slm_block_norm_bwd``.
+
+    ``d_residual`` and ``d_hidden`` are the gradients of its two outputs (``d_residual`` may
+    be None: zero).  ``dx`` and ``dy`` have the inputs' type, ``dgate`` the gate's shape and
+    type (summed over the rows that share a gate row), the weights' gradients are float32.
+    The sums run in a fixed order.  ``workspace`` may hold a uint8 tensor of
+    ``slm_block_norm_workspace_bytes``."""
+    N, d, dt, wt, gt, rows = _check_block(x, y, w_pre, w_post, gate)
+    dev = x.device
+    if (w_pre is None) != (d_hidden is None) or (d_hidden is None and d_residual is None):
+        raise ValueError("d_hidden is the gradient of hidden, made with w_pre: give both or "
+                         "neither, and at least one gradient")
+    for name, t in (("d_residual", d_residual), ("d_hidden", d_hidden)):
+        if t is not None:
+            _check_rows(name, t, (N, d), x.dtype, dev.index)
+    for name, t, w in (("rstd_post", fwd.rstd_post, w_post), ("rstd_pre", fwd.rstd_pre, w_pre)):
+        if (t is None) != (w is None) or (t is not None and (t.shape != (N,) or t.device != dev)):
+            raise ValueError("fwd does not come from a forward over these inputs")
+    need = _lib.slm_block_norm_workspace_bytes(N, d, rows if N > 0 else 0)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif (workspace.dtype != torch.uint8 or workspace.device != dev
+          or not workspace.is_contiguous() or workspace.numel() < need):
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of {need} bytes on {dev}")
+    g = BlockNormGrads(
+        torch.empty(N, d, dtype=x.dtype, device=dev),
+        None if y is None else torch.empty(N, d, dtype=x.dtype, device=dev),
+        None if gate is None else (torch.empty_like(gate) if N > 0 else torch.zeros_like(gate)),
+        None if w_pre is None else torch.empty(d, dtype=torch.float32, device=dev),
+        None if w_post is None else torch.empty(d, dtype=torch.float32, device=dev))
+    st = _lib.slm_block_norm_bwd(dt, _ptr(x), _ld(x, d), _ptr(y), _ld(y, d), _ptr(w_post),
+                                 _ptr(w_pre), wt, _ptr(gate), gt, rows, _ptr(d_residual),
+                                 _ld(d_residual, d), _ptr(d_hidden), _ld(d_hidden, d),
+                                 _ptr(fwd.rstd_post), _ptr(fwd.rstd_pre), N, d,
+                                 fwd.residual_scale, fwd.block_scale, fwd.weight_offset,
+                                 _ptr(g.dx), _ptr(g.dy), _ptr(g.dgate), _ptr(g.dw_post),
+                                 _ptr(g.dw_pre), _ptr(workspace), workspace.numel(), _stream())
+    _lib.check(st, "slm_block_norm_bwd")
+    return g
+
+
+class BlockNorm(torch.autograd.Function):
+    """(residual, hidden) of ``block_norm_fwd`` with its gradients."""
+
+    @staticmethod
+    def forward(ctx, x, y, w_pre, w_post, gate, residual_scale, block_scale, eps, weight_offset):
+        fwd = block_norm_fwd(x, y, w_pre, w_post, gate, residual_scale, block_scale, eps,
+                             weight_offset)
+        ctx.save_for_backward(x, y, w_pre, w_post, gate, fwd.rstd_post, fwd.rstd_pre)
+        ctx.scales = (fwd.residual_scale, fwd.block_scale, fwd.weight_offset)
+        ctx.set_materialize_grads(False)
+        return None if y is None else fwd.residual, fwd.hidden
+
+    @staticmethod
+    def backward(ctx, d_residual, d_hidden):
+        x, y, w_pre, w_post, gate, rstd_post, rstd_pre = ctx.saved_tensors
+        if d_residual is None and d_hidden is None:
+            return (None,) * 9
+        if w_pre is not None and d_hidden is None:   # hidden was not used
+            d_hidden = torch.zeros_like(x, memory_format=torch.contiguous_format)
+        d_residual, d_hidden = (
+            None if t is None else t if t.stride(-1) == 1 and t.stride(0) >= t.shape[1]
+            else t.contiguous() for t in (d_residual, d_hidden))
+        fwd = BlockNormResult(None, None, rstd_post, rstd_pre, *ctx.scales)
+        g = block_norm_bwd(fwd, x, y, w_pre, w_post, gate, d_residual, d_hidden)
+        return (g.dx, g.dy, None if w_pre is None else g.dw_pre.to(w_pre.dtype),
+                None if w_post is None else g.dw_post.to(w_post.dtype), g.dgate,
+                None, None, None, None)
+
+
+def block_norm(x, y=None, w_pre=None, w_post=None, gate=None, residual_scale=1.0,
+               block_scale=1.0, eps=1e-6, weight_offset=0.0):
+    """(residual, hidden) as ``block_norm_fwd`` makes them, differentiable with respect to
+    every tensor argument.  Without ``y`` the residual is ``x``; without ``w_pre`` hidden is
+    None."""
+    residual, hidden = BlockNorm.apply(x, y, w_pre, w_post, gate, residual_scale, block_scale,
+                                       eps, weight_offset)
+    return (x if y is None else residual), hidden
