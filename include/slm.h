@@ -408,6 +408,44 @@ SLM_API int slm_block_norm_bwd(int dtype, const void* x, int64_t ldx, const void
                                float* dw_post, float* dw_pre, void* workspace, size_t ws_bytes,
                                void* stream);
 
+/* Orthogonalised update of a stack of matrices by Newton-Schulz products, with the momentum's
+ * update in front (the direction that the Muon optimiser steps along).  For each [m, n] matrix
+ * g of the stack:
+ *     momentum <- beta momentum + (1 - beta) g           (when momentum is given)
+ *     u = beta momentum + (1 - beta) g  (nesterov != 0),  momentum (nesterov == 0),
+ *         or g (without momentum)
+ *     X = u / (||u||_F + eps)
+ *     for each step (a, b, c) of the coefficients:
+ *         A = X X^T,  X <- a X + (b A + c A^2) X          (A = X^T X on the right when m > n)
+ *     out = X rounded to bf16
+ * which moves every singular value s of X to a s + b s^3 + c s^5.
+ *   dtype     slm_dtype of grad.
+ *   grad      [batch, m, n]: ld elements from row to row (>= n), batch_stride from matrix to
+ *             matrix (>= (m - 1) ld + n when batch > 1).  Not written.
+ *   momentum  float [batch, m, n] contiguous, updated in place, or NULL.
+ *   beta      a double, so that 1 - beta is not the complement of a rounded beta.
+ *   coefficients  HOST float [steps][3].  Every value must be finite, and the iteration must
+ *             stay within the kernels' fp16 scaling for every X with singular values in [0, 1]:
+ *             all iterates' singular values at most 1.9 and |b s^2 + c s^4| at most 15, else
+ *             SLM_ERR_KIND.  (3.4445, -4.7750, 2.0315), five times, stays below 1.21 and 2.81.
+ *   steps     1 to 64.
+ *   out       bf16 [batch, m, n] contiguous; overlaps neither grad nor momentum.
+ *   workspace at least slm_orthogonalize_workspace_bytes(batch, m, n) bytes, 256-byte aligned;
+ *             its first word is the status word that slm_device_status reads.
+ * The products' operands are fp16 with fp32 accumulators; X is kept to 22 bits and the
+ * diagonals of A and B in fp32, so that the result is within about 2e-3 (Frobenius, relative)
+ * of the exact iteration on grad, the bf16 rounding of out (1.7e-3) included.  A matrix of
+ * zeros gives zeros; one with a NaN or an infinity gives NaN throughout, and no other matrix of
+ * the stack is touched by it.  Matrices with ||u||_F far below eps lose relative precision
+ * (their X is below 2^-28).  batch, m or n = 0: nothing is done.
+ * Returns SLM_ERR_SHAPE for bad sizes (m, n >= 2^31; batch > 65535; more than 2^31 - 1 tiles),
+ * strides, steps, beta outside [0, 1] or eps <= 0; the rest as everywhere. */
+SLM_API size_t slm_orthogonalize_workspace_bytes(int64_t batch, int64_t m, int64_t n);
+SLM_API int slm_orthogonalize(int dtype, const void* grad, int64_t ld, int64_t batch_stride,
+                              int64_t batch, int64_t m, int64_t n, float* momentum, double beta,
+                              int nesterov, const float* coefficients, int steps, float eps,
+                              void* out, void* workspace, size_t ws_bytes, void* stream);
+
 /* Test hook for the device-side failure path (not for production use).  fault_mode 1 makes
  * every following launch withhold one internal pipeline release, so that a bounded wait in
  * the kernel runs out: the kernel then records SLM_ERR_TIMEOUT in the workspace status word,

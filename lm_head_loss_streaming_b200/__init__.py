@@ -21,6 +21,9 @@ def __getattr__(name):
     if name in ("block_norm", "block_norm_fwd", "block_norm_bwd"):
         from . import norms as _norms
         return getattr(_norms, name)
+    if name in ("orthogonalize", "orthogonalize_workspace_bytes"):
+        from . import orth as _orth
+        return getattr(_orth, name)
     if name == "lib":
         from . import _lib
         return _lib

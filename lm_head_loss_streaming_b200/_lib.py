@@ -37,6 +37,7 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _F32 = ctypes.c_float
+_F64 = ctypes.c_double
 _INT = ctypes.c_int
 _SZ = ctypes.c_size_t
 SIGNATURES = {
@@ -76,6 +77,9 @@ SIGNATURES = {
     "slm_block_norm_bwd": (_INT, [_INT, _P, _I64, _P, _I64, _P, _P, _INT, _P, _INT, _I64, _P,
                                   _I64, _P, _I64, _P, _P, _I64, _I64, _F32, _F32, _F32, _P, _P,
                                   _P, _P, _P, _P, _SZ, _P]),
+    "slm_orthogonalize_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "slm_orthogonalize": (_INT, [_INT, _P, _I64, _I64, _I64, _I64, _I64, _P, _F64, _INT,
+                                 ctypes.POINTER(_F32), _INT, _F32, _P, _P, _SZ, _P]),
     "slm_trace_enable": (_INT, [_INT]),
     "slm_trace_read": (_INT, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_I64), _INT]),
 }
@@ -262,6 +266,19 @@ def slm_block_norm_fwd(*args):
 def slm_block_norm_bwd(*args):
     """Arguments as declared in ``include/slm.h``, in order."""
     return load().slm_block_norm_bwd(*args)
+
+
+def slm_orthogonalize_workspace_bytes(batch, m, n):
+    return load().slm_orthogonalize_workspace_bytes(int(batch), int(m), int(n))
+
+
+def slm_orthogonalize(dtype, grad, ld, batch_stride, batch, m, n, momentum, beta, nesterov,
+                      coefficients, eps, out, workspace, ws_bytes, stream):
+    """coefficients: one (a, b, c) per step."""
+    co = (_F32 * (3 * len(coefficients)))(*(v for step in coefficients for v in step))
+    return load().slm_orthogonalize(dtype, grad, ld, batch_stride, batch, m, n, momentum, beta,
+                                    1 if nesterov else 0, co, len(coefficients), eps, out,
+                                    workspace, ws_bytes, stream)
 
 
 def slm_count_valid(kind, labels, ignore_index, N, V, n_valid, stream):

@@ -20,6 +20,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <mutex>
 #include <utility>
 #include <vector>
@@ -443,6 +444,111 @@ int norm_checks(int dtype, const void* x, int64_t ldx, const void* y, int64_t ld
       misaligned(w_pre, elem_bytes(w_dtype)) || misaligned(gate, elem_bytes(gate_dtype)))
     return SLM_ERR_ALIGN;
   return SLM_OK;
+}
+
+// Orthogonalised update.
+constexpr int kMaxOrthSteps = 64;
+
+struct OrthLayout {
+  size_t status_off, sums_off, diag_off[2], a_off[2], hi_off[2], lo_off, total;
+  int64_t k, ldx, ldk;
+};
+
+OrthLayout orth_layout(int64_t batch, int64_t m, int64_t n) {
+  OrthLayout L{};
+  L.k = std::min(m, n);
+  L.ldx = static_cast<int64_t>(align_up(static_cast<size_t>(n), 8));
+  L.ldk = static_cast<int64_t>(align_up(static_cast<size_t>(L.k), 8));
+  const size_t b = static_cast<size_t>(batch);
+  size_t off = kAlign;
+  L.sums_off = off;
+  off = align_up(off + b * kOrthSums * sizeof(double), kAlign);
+  for (int i = 0; i < 2; ++i) {
+    L.diag_off[i] = off;
+    off = align_up(off + b * L.k * sizeof(float), kAlign);
+  }
+  for (int i = 0; i < 2; ++i) {
+    L.a_off[i] = off;
+    off = align_up(off + b * L.k * L.ldk * 2, kAlign);
+  }
+  for (int i = 0; i < 2; ++i) {
+    L.hi_off[i] = off;
+    off = align_up(off + b * m * L.ldx * 2, kAlign);
+  }
+  L.lo_off = off;
+  L.total = align_up(off + b * m * L.ldx * 2, kAlign);
+  return L;
+}
+
+bool orth_sizes_ok(int64_t batch, int64_t m, int64_t n) {
+  const int64_t big = int64_t(1) << 31;
+  if (batch < 0 || m < 0 || n < 0 || batch > 65535 || m >= big || n >= big) return false;
+  return ceil_div(m, 256) * ceil_div(n, 128) * batch < big;
+}
+
+// Whether the iteration keeps every X with singular values in [0, 1] within the kernels' fp16
+// scaling (see slm_orth.cu); the polynomials are sampled, with 1% to spare between samples.
+bool orth_coefficients_ok(const float* co, int steps) {
+  double most = 1.0;
+  for (int i = 0; i < steps; ++i) {
+    const double a = co[3 * i], b = co[3 * i + 1], c = co[3 * i + 2];
+    if (!finite(co[3 * i]) || !finite(co[3 * i + 1]) || !finite(co[3 * i + 2])) return false;
+    double next = 0.0, bmax = 0.0;
+    constexpr int kSamples = 1024;
+    for (int q = 0; q <= kSamples; ++q) {
+      const double s = most * q / kSamples, l = s * s;
+      const double pb = b * l + c * l * l;
+      bmax = std::max(bmax, std::abs(pb));
+      next = std::max(next, std::abs(s * (a + pb)));
+    }
+    most = 1.01 * next;
+    if (!(most <= 1.9) || !(bmax <= 15.0)) return false;
+  }
+  return true;
+}
+
+// 3-D fp16 tensor map over a stack of row-major [outer, inner] matrices with `ld` elements per
+// row, outer * ld per matrix; box {box_inner, box_outer, 1}, 128-byte swizzle.
+bool make_map_stack(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t ld,
+                    int64_t stack, int box_inner, int box_outer) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer),
+                        static_cast<cuuint64_t>(stack)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2,
+                           static_cast<cuuint64_t>(outer) * static_cast<cuuint64_t>(ld) * 2};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_outer), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tile grid of one product and its tile width: the width (256 or 128 columns) whose rounds of
+// tiles over the pairs take less time; a tile's time is taken as proportional to its width.
+int orth_tiles(OrthGemm* g, int64_t rows, int64_t cols, int64_t k, int64_t batch, bool sym) {
+  const int64_t pairs = std::max(1, sm_count() / 2);
+  int best = 256;
+  int64_t best_cost = 0;
+  for (int bn : {256, 128}) {
+    const int64_t nm = ceil_div(rows, kPairM), nn = ceil_div(cols, bn);
+    const int64_t w = kPairM / bn;
+    const int64_t per = sym ? w * (nm - 1) * nm / 2 + nn : nm * nn;
+    const int64_t cost = ceil_div(per * batch, pairs) * bn;
+    if (best_cost == 0 || cost < best_cost) {
+      best_cost = cost;
+      best = bn;
+      g->num_m = static_cast<int>(nm);
+      g->num_n = static_cast<int>(nn);
+      g->units_per = static_cast<int>(per);
+      g->num_units = static_cast<int>(per * batch);
+    }
+  }
+  g->k_blocks = static_cast<int>(ceil_div(k, kBK));
+  g->group_m = std::min(kGroupPairs, g->num_m);
+  g->rows = rows;
+  g->cols = cols;
+  return best;
 }
 
 #define SLM_TRY_CUDA(expr)                  \
@@ -1093,6 +1199,102 @@ int slm_block_norm_bwd(int dtype, const void* x, int64_t ldx, const void* y, int
                   reinterpret_cast<float*>(ws + L.pre_off),
                   reinterpret_cast<float*>(ws + L.gate_off)};
   SLM_LAUNCH(kTrNorm, launch_norm_bwd(dtype, p, s));
+  return SLM_OK;
+}
+
+size_t slm_orthogonalize_workspace_bytes(int64_t batch, int64_t m, int64_t n) {
+  if (!orth_sizes_ok(batch, m, n)) return 0;
+  return orth_layout(batch, m, n).total;
+}
+
+int slm_orthogonalize(int dtype, const void* grad, int64_t ld, int64_t batch_stride,
+                      int64_t batch, int64_t m, int64_t n, float* momentum, double beta,
+                      int nesterov, const float* coefficients, int steps, float eps, void* out,
+                      void* workspace, size_t ws_bytes, void* stream) {
+  if (!valid_dtype(dtype)) return SLM_ERR_KIND;
+  if (!orth_sizes_ok(batch, m, n) || steps < 1 || steps > kMaxOrthSteps || !finite(eps) ||
+      eps <= 0.f || !(beta >= 0.0 && beta <= 1.0))
+    return SLM_ERR_SHAPE;
+  if (!coefficients) return SLM_ERR_NULL;
+  if (!orth_coefficients_ok(coefficients, steps)) return SLM_ERR_KIND;
+  if (batch == 0 || m == 0 || n == 0) return SLM_OK;
+  if (!grad || !out || !workspace) return SLM_ERR_NULL;
+  if (ld < n || (batch > 1 && batch_stride < (m - 1) * ld + n)) return SLM_ERR_SHAPE;
+  if (misaligned(grad, elem_bytes(dtype)) || misaligned(momentum, 4) || misaligned(out, 2))
+    return SLM_ERR_ALIGN;
+  const OrthLayout L = orth_layout(batch, m, n);
+  if (misaligned(workspace, kAlign) || ws_bytes < L.total) return SLM_ERR_WORKSPACE;
+  int st = check_device();
+  if (st != SLM_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  int* status = reinterpret_cast<int*>(ws + L.status_off);
+  __half* hi[2] = {reinterpret_cast<__half*>(ws + L.hi_off[0]),
+                   reinterpret_cast<__half*>(ws + L.hi_off[1])};
+  __half* lo = reinterpret_cast<__half*>(ws + L.lo_off);
+  __half* mat[2] = {reinterpret_cast<__half*>(ws + L.a_off[0]),
+                    reinterpret_cast<__half*>(ws + L.a_off[1])};
+  float* diag[2] = {reinterpret_cast<float*>(ws + L.diag_off[0]),
+                    reinterpret_cast<float*>(ws + L.diag_off[1])};
+  const bool tall = m > n;
+  const int64_t k = L.k, l = std::max(m, n);
+
+  OrthGemm gram{}, square{}, update{};
+  const int bn_gram = orth_tiles(&gram, k, k, l, batch, true);
+  const int bn_square = orth_tiles(&square, k, k, k, batch, true);
+  const int bn_update = orth_tiles(&update, m, n, k, batch, false);
+  gram.ld = square.ld = L.ldk;
+  gram.a_out = mat[0];
+  gram.diag_out = diag[0];
+  square.a_in = mat[0];
+  square.a_out = mat[1];
+  square.diag_in = diag[0];
+  square.diag_out = diag[1];
+  update.ld = L.ldx;
+  update.diag_in = diag[1];
+  update.diag_n = k;
+  update.lo = lo;
+  update.out = static_cast<__nv_bfloat16*>(out);
+  update.tall = tall ? 1 : 0;
+  update.out_vec = n % 8 == 0 && !misaligned(out, 16);
+
+  // Operand maps.  A K-major operand has boxes of 64 (K) x 128 rows, its B form the columns
+  // that one CTA holds; an MN-major operand (X seen from its long side's other end) 64 x 64.
+  CUtensorMap xa[2], xb[2], ra, rb, ba, bb;
+  for (int i = 0; i < 2; ++i) {
+    // The A and B operands of X X^T; of X^T X both are MN-major.
+    if (!make_map_stack(&xa[i], hi[i], n, m, L.ldx, batch, 64, tall ? 64 : kBM)) return SLM_ERR_CUDA;
+    if (!make_map_stack(&xb[i], hi[i], n, m, L.ldx, batch, 64, tall ? 64 : bn_gram / 2))
+      return SLM_ERR_CUDA;
+  }
+  if (!make_map_stack(&ra, mat[0], k, k, L.ldk, batch, 64, kBM) ||
+      !make_map_stack(&rb, mat[0], k, k, L.ldk, batch, 64, bn_square / 2) ||
+      !make_map_stack(&ba, mat[1], k, k, L.ldk, batch, 64, kBM) ||
+      !make_map_stack(&bb, mat[1], k, k, L.ldk, batch, 64, bn_update / 2))
+    return SLM_ERR_CUDA;
+  CUtensorMap xu[2];  // X in the update: X B has it as K-major A, B X as MN-major B
+  for (int i = 0; i < 2; ++i)
+    if (!make_map_stack(&xu[i], hi[i], n, m, L.ldx, batch, 64, tall ? kBM : 64)) return SLM_ERR_CUDA;
+
+  SLM_TRY_CUDA(cudaMemsetAsync(status, 0, sizeof(int), s));
+  const DevCtl ctl = make_ctl(status);
+  const OrthPrep prep{grad, m, n, ld, batch_stride, L.ldx, momentum, static_cast<float>(beta),
+                      static_cast<float>(1.0 - beta), eps, nesterov,
+                      reinterpret_cast<double*>(ws + L.sums_off), hi[0], lo};
+  SLM_LAUNCH(kTrOrth, launch_orth_prep(dtype, prep, batch, s));
+  for (int i = 0; i < steps; ++i) {
+    const int cur = i & 1;
+    const bool last = i == steps - 1;
+    SLM_LAUNCH(kTrOrth, launch_orth_gemm(0, bn_gram, tall, false, xa[cur], xb[cur], gram, ctl, s));
+    square.b = coefficients[3 * i + 1];
+    square.c = coefficients[3 * i + 2];
+    SLM_LAUNCH(kTrOrth, launch_orth_gemm(1, bn_square, tall, false, ra, rb, square, ctl, s));
+    update.a = coefficients[3 * i];
+    update.hi_in = hi[cur];
+    update.hi_out = hi[cur ^ 1];
+    SLM_LAUNCH(kTrOrth, launch_orth_gemm(2, bn_update, tall, last, tall ? xu[cur] : ba,
+                                         tall ? bb : xu[cur], update, ctl, s));
+  }
   return SLM_OK;
 }
 

@@ -4,6 +4,7 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -298,6 +299,38 @@ struct NormBwd {
 };
 cudaError_t launch_norm_fwd(int dtype, const NormFwd& p, cudaStream_t s);
 cudaError_t launch_norm_bwd(int dtype, const NormBwd& p, cudaStream_t s);
+
+// ---- Orthogonalised update (slm_orth.cu); types as above. ----
+constexpr int kOrthSums = 592;  // partial sums of squares per matrix, at most
+struct OrthPrep {
+  const void* grad;
+  int64_t m, n, ldg, grad_batch, ldx;  // grad_batch: elements from matrix to matrix
+  float* momentum;                     // contiguous, or NULL
+  float beta, rest, eps;  // rest = 1 - beta
+  int nesterov;
+  double* sums;  // [batch][kOrthSums]
+  __half *hi, *lo;
+};
+// One product over the stack: rows x cols outputs per matrix, tiles of 256 x bn.
+struct OrthGemm {
+  int num_m, num_n, units_per, num_units, k_blocks, group_m;
+  int64_t rows, cols, ld;  // of the output (fp16 matrices: ld elements per row)
+  const __half* a_in;      // kSquare: R
+  __half* a_out;           // kGram: R; kSquare: R_B
+  const float* diag_in;    // kSquare: D; kUpdate: D_B
+  float* diag_out;         // kGram: D; kSquare: D_B
+  const __half* hi_in;
+  __half *hi_out, *lo;
+  __nv_bfloat16* out;
+  int64_t diag_n;  // kUpdate: entries of D_B per matrix
+  float a, b, c;
+  int tall, out_vec;
+};
+// op: 0 R and D of X X^T (X^T X when tall), 1 R_B and D_B, 2 the update of X (`last`: to out).
+cudaError_t launch_orth_prep(int dtype, const OrthPrep& p, int64_t batch, cudaStream_t s);
+cudaError_t launch_orth_gemm(int op, int bn, bool tall, bool last, const CUtensorMap& a,
+                             const CUtensorMap& b, const OrthGemm& g, const DevCtl& c,
+                             cudaStream_t s);
 
 constexpr int kCombineThreads = 256;
 

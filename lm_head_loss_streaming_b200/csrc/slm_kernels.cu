@@ -44,6 +44,7 @@
 #include <utility>
 
 #include "slm_internal.h"
+#include "slm_wait.cuh"
 #include "sm100.cuh"
 
 namespace slm {
@@ -52,28 +53,6 @@ using namespace sm100;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kTmemCols = 512;
-
-// Bounded wait executed by all 32 lanes of a warp; the result is warp-uniform.
-// honor_abort = false is used for the final waits on a CTA's own in-flight work.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                          const DevCtl& ctl, bool honor_abort = true) {
-  const uint32_t a = smem_u32(bar);
-  bool done = mbar_try_wait(a, parity);
-  if (!done) {
-    const long long t0 = clock64();
-    while (true) {
-      done = mbar_try_wait(a, parity);
-      if (done) break;
-      if (honor_abort && *abort) break;
-      if (clock64() - t0 > ctl.timeout_cycles) {
-        *abort = 1;
-        atomicOr(ctl.status, kFlagTimeout);
-        break;
-      }
-    }
-  }
-  return __all_sync(0xffffffffu, done);
-}
 
 // Work unit u -> (pair M tile mt, vocabulary run j).  Units are handed to the pairs round
 // robin, so the pairs that start together share B tiles only while their units have the
