@@ -395,7 +395,8 @@ SLM_API int slm_block_norm_fwd(int dtype, const void* x, int64_t ldx, const void
  *             required with gate.
  *   dw_post, dw_pre  float [d], overwritten; required with the weights (zero when N = 0).
  *   workspace at least slm_block_norm_workspace_bytes(N, d, gate_rows) bytes (gate_rows = 0
- *             without a gate), 256-byte aligned.
+ *             without a gate), 256-byte aligned; its first word is the status word that
+ *             slm_device_status reads.
  * The sums over rows are taken in a fixed order: the same inputs give the same bits. */
 SLM_API size_t slm_block_norm_workspace_bytes(int64_t N, int64_t d, int64_t gate_rows);
 SLM_API int slm_block_norm_bwd(int dtype, const void* x, int64_t ldx, const void* y, int64_t ldy,

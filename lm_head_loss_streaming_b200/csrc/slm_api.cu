@@ -408,7 +408,7 @@ size_t elem_bytes(int t) { return t == SLM_F32 ? 4 : 2; }
 bool finite(float v) { return v == v && v <= 3.4e38f && v >= -3.4e38f; }
 
 struct NormLayout {
-  size_t c1_off, post_off, pre_off, gate_off, total;
+  size_t status_off, c1_off, post_off, pre_off, gate_off, total;
 };
 
 NormLayout norm_layout(int64_t N, int64_t d, int64_t gate_rows) {
@@ -416,8 +416,9 @@ NormLayout norm_layout(int64_t N, int64_t d, int64_t gate_rows) {
   const NormPlan q = norm_plan(std::max<int64_t>(N, 1), gate_rows > 0 ? N / gate_rows : 1,
                                gate_rows > 0);
   const size_t part = align_up(static_cast<size_t>(q.blocks) * d * sizeof(float), kAlign);
-  L.c1_off = 0;
-  L.post_off = align_up(static_cast<size_t>(N) * sizeof(float), kAlign);
+  L.status_off = 0;
+  L.c1_off = kAlign;
+  L.post_off = align_up(L.c1_off + static_cast<size_t>(N) * sizeof(float), kAlign);
   L.pre_off = L.post_off + part;
   L.gate_off = L.pre_off + part;
   L.total = L.gate_off + (q.shared_gate && q.slices > 1 ? part : 0) + kAlign;
@@ -1198,7 +1199,9 @@ int slm_block_norm_bwd(int dtype, const void* x, int64_t ldx, const void* y, int
                   reinterpret_cast<float*>(ws + L.post_off),
                   reinterpret_cast<float*>(ws + L.pre_off),
                   reinterpret_cast<float*>(ws + L.gate_off)};
-  SLM_LAUNCH(kTrNorm, launch_norm_bwd(dtype, p, s));
+  int* status = reinterpret_cast<int*>(ws + L.status_off);
+  SLM_TRY_CUDA(cudaMemsetAsync(status, 0, sizeof(int), s));
+  SLM_LAUNCH(kTrNorm, launch_norm_bwd(dtype, p, make_ctl(status), s));
   return SLM_OK;
 }
 

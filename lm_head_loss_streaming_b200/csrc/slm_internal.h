@@ -273,7 +273,9 @@ __host__ __device__ inline NormRows norm_rows(const NormPlan& q, int b) {
   return r;
 }
 // Plan for N >= 1 rows; rows_per_gate = 1 is a gate of its own for each row (not shared).
-NormPlan norm_plan(int64_t N, int64_t rows_per_gate, bool has_gate);
+// (`max_blocks` row workers at most, which take `batch` rows at a time).
+NormPlan norm_plan(int64_t N, int64_t rows_per_gate, bool has_gate, int max_blocks = kNormBlocks,
+                   int batch = 1);
 
 struct NormFwd {
   const void *x, *y, *w_post, *w_pre, *gate;
@@ -298,7 +300,7 @@ struct NormBwd {
   float *part_post, *part_pre, *part_gate;  // [plan.blocks][d] each
 };
 cudaError_t launch_norm_fwd(int dtype, const NormFwd& p, cudaStream_t s);
-cudaError_t launch_norm_bwd(int dtype, const NormBwd& p, cudaStream_t s);
+cudaError_t launch_norm_bwd(int dtype, const NormBwd& p, const DevCtl& c, cudaStream_t s);
 
 // ---- Orthogonalised update (slm_orth.cu); types as above. ----
 constexpr int kOrthSums = 592;  // partial sums of squares per matrix, at most
