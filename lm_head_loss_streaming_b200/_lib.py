@@ -260,12 +260,12 @@ def slm_block_norm_workspace_bytes(N, d, gate_rows=0):
 
 def slm_block_norm_fwd(*args):
     """Arguments as declared in ``include/slm.h``, in order."""
-    return load().slm_block_norm_fwd(*args)
+    return (_lib or load()).slm_block_norm_fwd(*args)
 
 
 def slm_block_norm_bwd(*args):
     """Arguments as declared in ``include/slm.h``, in order."""
-    return load().slm_block_norm_bwd(*args)
+    return (_lib or load()).slm_block_norm_bwd(*args)
 
 
 def slm_orthogonalize_workspace_bytes(batch, m, n):

@@ -1152,7 +1152,8 @@ int slm_block_norm_fwd(int dtype, const void* x, int64_t ldx, const void* y, int
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const NormFwd p{x, y, w_post, w_pre, gate, ldx, ldy, N, d, gate ? N / gate_rows : 1,
                   w_dtype == SLM_F32, gate_dtype == SLM_F32, residual_scale, block_scale, eps,
-                  weight_offset, residual, w_pre ? hidden : nullptr, rstd_post, rstd_pre};
+                  weight_offset, residual, w_pre ? hidden : nullptr, w_post ? rstd_post : nullptr,
+                  w_pre ? rstd_pre : nullptr};
   SLM_LAUNCH(kTrNorm, launch_norm_fwd(dtype, p, s));
   return SLM_OK;
 }

@@ -44,7 +44,6 @@
 #include <utility>
 
 #include "slm_internal.h"
-#include "f32x2.cuh"
 #include "slm_wait.cuh"
 #include "sm100.cuh"
 
@@ -568,11 +567,49 @@ __device__ __forceinline__ float max32(const float (&v)[32]) {
   return fmaxf(m0, m1);
 }
 
-// SLM_PACKED_EPI = 0 selects scalar epilogue arithmetic instead of the packed fp32 pairs (same
-// results, except where a packed pair of partial sums replaces one running sum).
+// Packed fp32 pairs (sm_100 fma / add / sub / mul .f32x2): two independent fp32 operations,
+// each rounded to nearest as its scalar form, in one instruction.  SLM_PACKED_EPI = 0 selects
+// the scalar forms (same results, except where a packed pair of partial sums replaces one
+// running sum).
 #ifndef SLM_PACKED_EPI
 #define SLM_PACKED_EPI 1
 #endif
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "sub.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 __device__ __forceinline__ float2 exp2_2(float2 a) { return make_float2(exp2f(a.x), exp2f(a.y)); }
 // log2 of a pair of sums of probabilities; a sum of 0 (both terms underflowed or masked)
 // gives -126 instead of -inf, so that the terms it multiplies stay 0.

@@ -21,7 +21,6 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "f32x2.cuh"
 #include "slm_internal.h"
 #include "slm_wait.cuh"
 #include "sm100.cuh"
@@ -199,7 +198,7 @@ __global__ void __launch_bounds__(kAnyThreads) norm_bwd_rows_any(const NormBwd p
       static_cast<T*>(p.dx)[n * p.d + c] = from_f<T>(p.residual_scale * g);
       if (p.y) {
         const float a = p.block_scale * e.gate * e.wq;
-        static_cast<T*>(p.dy)[n * p.d + c] = from_f<T>(iy * (a * g - e.yh * c2));
+        static_cast<T*>(p.dy)[n * p.d + c] = from_f<T>(p.w_post ? iy * (a * g - e.yh * c2) : a * g);
       }
       if (p.gate && p.rows_per_gate == 1) {
         const float dg = p.block_scale * e.yh * e.wq * g;
@@ -349,7 +348,11 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
                : "l"(p));
   return v;
 }
+// Packed fp32 pairs: two operations, each rounded as its scalar form, in one instruction.
 __device__ __forceinline__ float2 pair(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 
 // Sum over the TPR threads of a row (a warp, or the whole block), in every one of them.
 template <int TPR>
@@ -459,43 +462,46 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_fwd_vec(const Norm
 
 // ----------------------------------------------------------------------------------------
 // Backward for rows of whole, aligned 16-byte pieces, in one pass: every row worker (a block,
-// or a cluster of CL blocks that share a row's columns) walks its rows with the row data
-// coming in through a ring of bulk copies, and keeps the column sums in registers.
-//   warp 8      copies the rows' segments into the ring (cp.async.bulk, counted on an mbarrier)
-//   warps 0-7   TPR threads per row, NV pieces each; a batch of 256 / TPR rows at a time
-// Sweep 1 over a row forms the three sums, sweep 2 the outputs, both from shared memory.
+// or a cluster of blocks that share a row's columns) walks its rows, a batch of 256 / TPR at
+// a time.
+//   warp 8      copies the batches' row segments into a ring (cp.async.bulk, counted on
+//               mbarriers)
+//   warps 0-7   TPR threads per row, NV pieces of each array per thread; parameters and column
+//               sums stay in registers, as every thread keeps its columns
+// Sweep 1 over a batch forms the rows' three sums, sweep 2 the outputs, both from the ring.
+// Sweep 1 runs one batch ahead, so that the sums are exchanged behind sweep 2 of the batch
+// before: at most one block barrier per batch, and a cluster's exchange is off the critical path.
 // Only two parameters per column are needed in the loop: a = bs gate wq (bs wq with a gate per
 // token) and wp.  The group's sum S = sum yh g serves two gradients, which are taken when the
 // group ends:  dgate = bs wq S,  dw_post += bs gate S.
 //   GATE   0 none or shared by the rows of a group; 1 per token, of the rows' type; 2 per
 //          token, fp32 beside 16-bit rows
 // ----------------------------------------------------------------------------------------
-constexpr int kRingThreads = 256;  // computing threads; one more warp copies
+constexpr int kRingThreads = 256;  // computing threads
+constexpr int kRingWarps = kRingThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kMaxStages = 6;
+constexpr int kPartStride = kMaxCluster * kRingWarps + 8;  // the three sums in banks apart
 
 struct RingCtl {
-  uint64_t full[4], empty[4], sums;
+  uint64_t full[kMaxStages], empty[kMaxStages], sums[2];
   int abort;
-  float part[2][kMaxCluster * 8][3];
+  float part[4][3 * kPartStride];
 };
 
 template <class T, int TPR, int NV, int GATE>
 struct RingCfg {
-  static constexpr int kRows = kRingThreads / TPR;      // rows per batch
-  static constexpr int kCap = TPR * NV;                 // pieces per row segment, at most
-  static constexpr int kSeg = kCap * 16;                // bytes of one array's row segment
+  static constexpr int kRows = kRingThreads / TPR;  // rows per batch
+  static constexpr int kSeg = TPR * NV * 16;        // bytes of one array's row segment, at most
   static constexpr int kGateSeg = GATE == 0 ? 0 : GATE == 1 ? kSeg : 2 * kSeg;
   static constexpr int kStage = kRows * (4 * kSeg + kGateSeg);
-  static constexpr int kParams = 2 * kCap * Piece<T>::kElems * 4;  // a, wp
+  static constexpr int kCtl = (static_cast<int>(sizeof(RingCtl)) + 127) / 128 * 128;
   static constexpr int kScratch = kRows > 1 ? kRingThreads * NV * Piece<T>::kElems * 4 : 0;
-  static constexpr int kFixed = (static_cast<int>(sizeof(RingCtl)) + 127) / 128 * 128 + kParams + kScratch;
-  // Two blocks per SM where two stages fit in half of it, so that one block's reductions
-  // overlap the other's arithmetic.
-  static constexpr int kHalf = 115712 - 128, kWhole = 232448 - 128;
-  static constexpr int kFit2 = (kHalf - kFixed) / kStage, kFit1 = (kWhole - kFixed) / kStage;
-  static constexpr int kStages = kFit2 >= 2 ? (kFit2 > 4 ? 4 : kFit2) : (kFit1 > 4 ? 4 : kFit1);
-  static constexpr size_t kSmem = 128 + kFixed + static_cast<size_t>(kStages) * kStage;
-  static_assert(kStages >= 2, "ring");
+  static constexpr int kFit = (232448 - 128 - kCtl - kScratch - kSeg) / kStage;
+  static constexpr int kStages = kFit > kMaxStages ? kMaxStages : kFit;
+  static constexpr size_t kSmem =
+      128 + kCtl + kScratch + kSeg + static_cast<size_t>(kStages) * kStage;
+  static_assert(kStages >= 4, "two batches in use, two under way");
 };
 
 // wait_warp for a barrier that other blocks of the cluster arrive on after storing to this
@@ -518,24 +524,34 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, vol
   return __all_sync(0xffffffffu, done);
 }
 
-__device__ __forceinline__ void consumers_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kRingThreads) : "memory");
+// Three sums over the warp with six shuffles instead of fifteen: the first two steps also deal
+// the sums out, so that lanes 8 k .. 8 k + 7 end with sum k (k = 0, 1, 2).
+__device__ __forceinline__ float warp_sum3(float v0, float v1, float v2, int lane) {
+  const bool b4 = lane & 16, b3 = lane & 8;
+  float k0 = b4 ? v2 : v0, k1 = b4 ? 0.f : v1;
+  k0 += __shfl_xor_sync(0xffffffffu, b4 ? v0 : v2, 16);
+  k1 += __shfl_xor_sync(0xffffffffu, b4 ? v1 : 0.f, 16);
+  float k = b3 ? k1 : k0;
+  k += __shfl_xor_sync(0xffffffffu, b3 ? k0 : k1, 8);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
+  return k;
 }
 
 template <class T, int TPR, int NV, int GATE, bool CL>
-__global__ void __launch_bounds__(kRingThreads + 32, 2)
+__global__ void __launch_bounds__(kRingThreads + 32, 1)
     norm_bwd_ring(const NormBwd p, const DevCtl ctl, const int seg) {
   using P = Piece<T>;
   using C = RingCfg<T, TPR, NV, GATE>;
-  constexpr int K = P::kPairs, kRows = C::kRows, kCap = C::kCap, S = C::kStages;
+  constexpr int K = P::kPairs, kRows = C::kRows, S = C::kStages;
+  static_assert(!CL || TPR == kRingThreads, "a cluster shares one row");
   extern __shared__ uint8_t ring_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ring_raw) + 127) &
                                              ~static_cast<uintptr_t>(127));
   RingCtl* rc = reinterpret_cast<RingCtl*>(base);
-  float4* a4 = reinterpret_cast<float4*>(base + (sizeof(RingCtl) + 127) / 128 * 128);
-  float4* wp4 = a4 + kCap * (K / 2);      // half h of piece i at [h * kCap + i]
-  float4* scratch = wp4 + kCap * (K / 2);
-  uint8_t* ring = reinterpret_cast<uint8_t*>(scratch) + C::kScratch;
+  float4* scratch = reinterpret_cast<float4*>(base + C::kCtl);
+  uint8_t* zeros = base + C::kCtl + C::kScratch;  // stands in for the arrays that are absent
+  uint8_t* ring = zeros + C::kSeg;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cs = CL ? static_cast<int>(cluster_size()) : 1;
   const int rank = CL ? static_cast<int>(cluster_ctarank()) : 0;
@@ -547,12 +563,14 @@ __global__ void __launch_bounds__(kRingThreads + 32, 2)
   const bool has_y = p.y != nullptr, has_dr = p.d_residual != nullptr, pre = p.w_pre != nullptr;
   volatile int* abort = &rc->abort;
 
+  for (int i = threadIdx.x; i < C::kSeg / 16; i += kRingThreads + 32)
+    reinterpret_cast<uint4*>(zeros)[i] = make_uint4(0, 0, 0, 0);
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&rc->full[s], 1);
-      mbar_init(&rc->empty[s], kRingThreads / 32);
+      mbar_init(&rc->empty[s], kRingWarps);
     }
-    mbar_init(&rc->sums, cs * (kRingThreads / 32));
+    for (int s = 0; s < 2; ++s) mbar_init(&rc->sums[s], cs * kRingWarps);
     rc->abort = 0;
     fence_barrier_init();
   }
@@ -561,11 +579,10 @@ __global__ void __launch_bounds__(kRingThreads + 32, 2)
   else
     __syncthreads();
 
-  if (warp == kRingThreads / 32) {
+  if (warp == kRingWarps) {
     // ------------------------------ copies ------------------------------
     const uint32_t bytes = static_cast<uint32_t>(mine) * 16;
     const uint32_t gbytes = GATE == 2 ? 2 * bytes : bytes;
-    const int narr = 5;
     const uint32_t row_bytes = bytes * (has_y + has_dr + 2 * pre) + (GATE ? gbytes : 0);
     uint32_t it = 0;
     bool ok = true;
@@ -581,37 +598,23 @@ __global__ void __launch_bounds__(kRingThreads + 32, 2)
         if (lane == 0) mbar_arrive_expect_tx(&rc->full[s], row_bytes * valid);
         __syncwarp();
         uint8_t* st = ring + s * C::kStage;
-        for (int q = lane; q < valid * narr; q += 32) {
-          const int arr = q % narr, rw = q / narr;
-          const int64_t row = n + rw;
-          const uint8_t* src = nullptr;
-          int64_t ld = 0;
-          if (arr == 0) {
-            src = pre ? static_cast<const uint8_t*>(p.x) : nullptr;
-            ld = p.ldx;
-          } else if (arr == 1) {
-            src = static_cast<const uint8_t*>(p.y);
-            ld = p.ldy;
-          } else if (arr == 2) {
-            src = static_cast<const uint8_t*>(p.d_residual);
-            ld = p.ld_dr;
-          } else if (arr == 3) {
-            src = pre ? static_cast<const uint8_t*>(p.d_hidden) : nullptr;
-            ld = p.ld_dh;
-          } else if (GATE) {
-            src = static_cast<const uint8_t*>(p.gate);
-            ld = p.d;
-          }
+        for (int q = lane; q < valid * 5; q += 32) {
+          const int arr = q % 5, rw = q / 5;
+          const void* src = arr == 0 ? (pre ? p.x : nullptr) : arr == 1 ? p.y
+                            : arr == 2 ? p.d_residual : arr == 3 ? (pre ? p.d_hidden : nullptr)
+                            : GATE ? p.gate : nullptr;
+          const int64_t ld = arr == 0 ? p.ldx : arr == 1 ? p.ldy : arr == 2 ? p.ld_dr
+                             : arr == 3 ? p.ld_dh : p.d;
           if (!src) continue;
+          const int64_t at = (n + rw) * ld * static_cast<int64_t>(sizeof(T)) +
+                             static_cast<int64_t>(piece0) * 16;
           if (arr < 4)
-            bulk_load(st + arr * kRows * C::kSeg + rw * C::kSeg,
-                      src + row * ld * sizeof(T) + static_cast<int64_t>(piece0) * 16, bytes,
-                      &rc->full[s]);
+            bulk_load(st + (arr * kRows + rw) * C::kSeg, static_cast<const uint8_t*>(src) + at,
+                      bytes, &rc->full[s]);
           else
             bulk_load(st + 4 * kRows * C::kSeg + rw * C::kGateSeg,
-                      src + (row * ld * sizeof(T) + static_cast<int64_t>(piece0) * 16) *
-                                (GATE == 2 ? 2 : 1),
-                      gbytes, &rc->full[s]);
+                      static_cast<const uint8_t*>(src) + at * (GATE == 2 ? 2 : 1), gbytes,
+                      &rc->full[s]);
         }
         __syncwarp();
       }
@@ -624,49 +627,37 @@ __global__ void __launch_bounds__(kRingThreads + 32, 2)
     }
   } else {
     // ------------------------------ arithmetic ------------------------------
-    const int rw = threadIdx.x / TPR, t = threadIdx.x % TPR;
+    const int rw = threadIdx.x / TPR, t = threadIdx.x % TPR;  // row of the batch, first piece
     const float2 zero = pair(0.f);
     const float2 off = pair(p.weight_offset), bs = pair(p.block_scale), rs = pair(p.residual_scale);
     const float inv_d = 1.f / static_cast<float>(p.d);
-    float2 acc_s[NV][K], acc_p[NV][K];
+    bool col[NV];
+    float2 acc_s[NV][K], acc_p[NV][K], a[NV][K], wp[NV][K];
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+    for (int v = 0; v < NV; ++v) {
+      col[v] = t + v * TPR < mine;
 #pragma unroll
-      for (int k = 0; k < K; ++k) acc_s[v][k] = acc_p[v][k] = zero;
-
-    auto put = [&](float4* dst, int i, const float2(&v)[K]) {
+      for (int k = 0; k < K; ++k) acc_s[v][k] = acc_p[v][k] = a[v][k] = wp[v][k] = zero;
+      if (pre && col[v]) {
+        P::param(p.w_pre, p.w_f32, piece0 + t + v * TPR, wp[v]);
 #pragma unroll
-      for (int h = 0; h < K / 2; ++h)
-        dst[h * kCap + i] = make_float4(v[2 * h].x, v[2 * h].y, v[2 * h + 1].x, v[2 * h + 1].y);
-    };
-    auto get = [&](const float4* src, int i, float2(&v)[K]) {
-#pragma unroll
-      for (int h = 0; h < K / 2; ++h) {
-        const float4 f = src[h * kCap + i];
-        v[2 * h] = make_float2(f.x, f.y);
-        v[2 * h + 1] = make_float2(f.z, f.w);
+        for (int k = 0; k < K; ++k) wp[v][k] = add2(wp[v][k], off);
       }
+    }
+    // wq, and bs times the group's gate, of piece t + v TPR.
+    auto load_wq = [&](int v, float2(&w)[K]) {
+      if (p.w_post) P::param(p.w_post, p.w_f32, piece0 + t + v * TPR, w);
+#pragma unroll
+      for (int k = 0; k < K; ++k) w[k] = p.w_post ? add2(w[k], off) : pair(1.f);
     };
-    // wq of piece i, and bs times the group's gate.
-    auto load_wq = [&](int i, float2(&w)[K]) {
-      if (p.w_post) {
-        P::param(p.w_post, p.w_f32, piece0 + i, w);
+    auto load_gs = [&](int64_t g, int v, float2(&w)[K]) {
+      const bool shared = GATE == 0 && p.gate;
+      if (shared) P::param(p.gate, p.gate_f32, g * nvec + piece0 + t + v * TPR, w);
 #pragma unroll
-        for (int k = 0; k < K; ++k) w[k] = add2(w[k], off);
-      } else {
-#pragma unroll
-        for (int k = 0; k < K; ++k) w[k] = pair(1.f);
-      }
+      for (int k = 0; k < K; ++k) w[k] = shared ? mul2(w[k], bs) : bs;
     };
-    auto load_gs = [&](int64_t g, int i, float2(&w)[K]) {
-      if (GATE == 0 && p.gate) {
-        P::param(p.gate, p.gate_f32, g * nvec + piece0 + i, w);
-#pragma unroll
-        for (int k = 0; k < K; ++k) w[k] = mul2(w[k], bs);
-      } else {
-#pragma unroll
-        for (int k = 0; k < K; ++k) w[k] = bs;
-      }
+    auto consumers_sync = [] {
+      asm volatile("bar.sync 1, %0;" ::"n"(kRingThreads) : "memory");
     };
     // The column sums of the batch's row lanes, added in a fixed order into lane 0's.
     auto join = [&](float2(&acc)[NV][K]) {
@@ -675,8 +666,8 @@ __global__ void __launch_bounds__(kRingThreads + 32, 2)
       for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int h = 0; h < K / 2; ++h)
-          scratch[(v * (K / 2) + h) * kRingThreads + threadIdx.x] =
-              make_float4(acc[v][2 * h].x, acc[v][2 * h].y, acc[v][2 * h + 1].x, acc[v][2 * h + 1].y);
+          scratch[(v * (K / 2) + h) * kRingThreads + threadIdx.x] = make_float4(
+              acc[v][2 * h].x, acc[v][2 * h].y, acc[v][2 * h + 1].x, acc[v][2 * h + 1].y);
       consumers_sync();
       if (rw == 0)
         for (int o = 1; o < kRows; ++o)
@@ -690,12 +681,11 @@ __global__ void __launch_bounds__(kRingThreads + 32, 2)
             }
       consumers_sync();
     };
-    // Pieces of an fp32 output row.
-    auto store_f32 = [&](float* dst, int i, const float2(&v)[K], bool add) {
-      float4* o = reinterpret_cast<float4*>(dst) + static_cast<int64_t>(piece0 + i) * (K / 2);
+    auto store_f32 = [&](float* dst, int v, const float2(&w)[K], bool add) {
+      float4* o = reinterpret_cast<float4*>(dst) + static_cast<int64_t>(piece0 + t + v * TPR) * (K / 2);
 #pragma unroll
       for (int h = 0; h < K / 2; ++h) {
-        float4 f = make_float4(v[2 * h].x, v[2 * h].y, v[2 * h + 1].x, v[2 * h + 1].y);
+        float4 f = make_float4(w[2 * h].x, w[2 * h].y, w[2 * h + 1].x, w[2 * h + 1].y);
         if (add) {
           const float4 q = o[h];
           f = make_float4(f.x + q.x, f.y + q.y, f.z + q.z, f.w + q.w);
@@ -703,243 +693,213 @@ __global__ void __launch_bounds__(kRingThreads + 32, 2)
         o[h] = f;
       }
     };
-    auto store_param_grad = [&](void* dst, bool f32, int64_t row, int i, const float2(&v)[K]) {
+    auto store_gate_grad = [&](bool f32, int64_t row, int v, const float2(&w)[K]) {
       if (f32)
-        store_f32(static_cast<float*>(dst) + row * p.d, i, v, false);
+        store_f32(static_cast<float*>(p.dgate) + row * p.d, v, w, false);
       else
-        reinterpret_cast<uint4*>(static_cast<T*>(dst) + row * p.d)[piece0 + i] = P::pack(v);
+        reinterpret_cast<uint4*>(static_cast<T*>(p.dgate) + row * p.d)[piece0 + t + v * TPR] = P::pack(w);
     };
-
-    // wp for the whole run; a per group.
-    if (rw == 0)
+    auto factors = [&](int64_t n, int64_t n1, float& iy, float& ir) {
+      iy = p.w_post && n < n1 ? __ldg(p.rstd_post + n) : 1.f;
+      ir = pre && n < n1 ? __ldg(p.rstd_pre + n) : 0.f;
+    };
+    // Where this thread's pieces of x, y, dr and dh lie in stage 0, and how far on in the next.
+    const uint8_t* arr[4];
+    int step[4];
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
+    for (int q = 0; q < 4; ++q) {
+      const bool there = q == 1 ? has_y : q == 2 ? has_dr : pre;
+      arr[q] = (there ? ring + (q * kRows + rw) * C::kSeg : zeros) + t * 16;
+      step[q] = there ? C::kStage : 0;
+    }
+    // This thread's piece v of a stage: y, dr, the gate, i_y a (gate), r and dh.
+    auto load = [&](int s, int v, float2 iy, float2(&y)[K], float2(&dr)[K], float2(&gate)[K],
+                    float2(&ay)[K], float2(&r)[K], float2(&dh)[K]) {
+      P::unpack(*reinterpret_cast<const uint4*>(arr[0] + s * step[0] + v * TPR * 16), r);
+      P::unpack(*reinterpret_cast<const uint4*>(arr[1] + s * step[1] + v * TPR * 16), y);
+      P::unpack(*reinterpret_cast<const uint4*>(arr[2] + s * step[2] + v * TPR * 16), dr);
+      P::unpack(*reinterpret_cast<const uint4*>(arr[3] + s * step[3] + v * TPR * 16), dh);
+      if (GATE) {
+        const uint8_t* sg = ring + s * C::kStage + 4 * kRows * C::kSeg + rw * C::kGateSeg;
         const int i = t + v * TPR;
-        if (i >= mine) break;
-        float2 w[K];
-        if (pre) {
-          P::param(p.w_pre, p.w_f32, piece0 + i, w);
-#pragma unroll
-          for (int k = 0; k < K; ++k) w[k] = add2(w[k], off);
+        if (GATE == 1) {
+          P::unpack(reinterpret_cast<const uint4*>(sg)[i], gate);
         } else {
 #pragma unroll
-          for (int k = 0; k < K; ++k) w[k] = zero;
+          for (int h = 0; h < K / 2; ++h) {
+            const float4 f = reinterpret_cast<const float4*>(sg)[i * (K / 2) + h];
+            gate[2 * h] = make_float2(f.x, f.y);
+            gate[2 * h + 1] = make_float2(f.z, f.w);
+          }
         }
-        put(wp4, i, w);
       }
-
-    uint32_t it = 0;
-    float iy = 1.f, ir = 0.f;
-    auto factors = [&](int64_t n, float& fy, float& fr) {
-      if (n < p.N) {
-        fy = p.w_post ? __ldg(p.rstd_post + n) : 1.f;
-        fr = pre ? __ldg(p.rstd_pre + n) : 0.f;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        ay[k] = mul2(GATE ? mul2(a[v][k], gate[k]) : a[v][k], iy);
+        r[k] = fma2(rs, r[k], mul2(ay[k], y[k]));
       }
     };
-    factors(rows.begin(rows.g0) + rw, iy, ir);
-    for (int64_t g = rows.g0; g < rows.g1; ++g) {
-      if (rw == 0)
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const int i = t + v * TPR;
-          if (i >= mine) break;
-          float2 w[K], q[K];
-          load_wq(i, w);
-          load_gs(g, i, q);
-#pragma unroll
-          for (int k = 0; k < K; ++k) w[k] = has_y ? mul2(w[k], q[k]) : zero;
-          put(a4, i, w);
-        }
-      if (kRows > 1) consumers_sync();
-      const int64_t n1 = rows.end(g);
-      for (int64_t nb = rows.begin(g); nb < n1; nb += kRows, ++it) {
-        const int s = it % S;
-        const int64_t n = nb + rw;
-        const bool live = n < n1;
-        float iy_next = 1.f, ir_next = 0.f;
-        factors((nb + kRows < n1 ? nb + kRows : rows.begin(g + 1)) + rw, iy_next, ir_next);
-        wait_warp(&rc->full[s], (it / S) & 1u, abort, ctl);
-        const uint8_t* st = ring + s * C::kStage + rw * C::kSeg;
-        const uint4* sx = reinterpret_cast<const uint4*>(st);
-        const uint4* sy = reinterpret_cast<const uint4*>(st + kRows * C::kSeg);
-        const uint4* sr = reinterpret_cast<const uint4*>(st + 2 * kRows * C::kSeg);
-        const uint4* sh = reinterpret_cast<const uint4*>(st + 3 * kRows * C::kSeg);
-        const uint8_t* sg = ring + s * C::kStage + 4 * kRows * C::kSeg + rw * C::kGateSeg;
+    // Sweep 1: sum u r, sum a yh (dr + i_r u), sum a yh r over the rows of the batch, handed on
+    // to the warps that share a row (the factor i_r of rh comes in afterwards).
+    auto sweep1 = [&](uint32_t it, int s, bool live, float iy, float ir) {
+      wait_warp(&rc->full[s], (it / S) & 1u, abort, ctl);
+      float2 s0 = zero, s1 = zero, s2 = zero;
+      if (live) {
         const float2 iy2 = pair(iy), ir2 = pair(ir);
-        // Everything both sweeps need of piece i.
-        auto load = [&](int i, float2(&a)[K], float2(&gate)[K], float2(&yh)[K], float2(&rh)[K],
-                        float2(&dh)[K], float2(&u)[K], float2(&tt)[K]) {
-          float2 x[K];
-          get(a4, i, a);
-          get(wp4, i, u);
-          if (pre)
-            P::unpack(sx[i], x);
-          if (GATE == 1) P::unpack(reinterpret_cast<const uint4*>(sg)[i], gate);
-          if (GATE == 2) {
 #pragma unroll
-            for (int h = 0; h < K / 2; ++h) {
-              const float4 f = reinterpret_cast<const float4*>(sg)[i * (K / 2) + h];
-              gate[2 * h] = make_float2(f.x, f.y);
-              gate[2 * h + 1] = make_float2(f.z, f.w);
-            }
-          }
-          if (has_y)
-            P::unpack(sy[i], yh);
-          else
-#pragma unroll
-            for (int k = 0; k < K; ++k) yh[k] = zero;
-          if (pre)
-            P::unpack(sh[i], dh);
-          else
-#pragma unroll
-            for (int k = 0; k < K; ++k) dh[k] = zero;
-          if (has_dr)
-            P::unpack(sr[i], tt);
-          else
-#pragma unroll
-            for (int k = 0; k < K; ++k) tt[k] = zero;
-#pragma unroll
-          for (int k = 0; k < K; ++k) {
-            yh[k] = mul2(yh[k], iy2);
-            const float2 ag = GATE ? mul2(a[k], gate[k]) : a[k];
-            rh[k] = pre ? mul2(ir2, fma2(rs, x[k], mul2(ag, yh[k]))) : zero;
-            u[k] = mul2(dh[k], u[k]);
-            tt[k] = fma2(ir2, u[k], tt[k]);
-          }
-        };
-        float2 s0 = zero, s1 = zero, s2 = zero;
-        if (live)
-#pragma unroll
-          for (int v = 0; v < NV; ++v) {
-            const int i = t + v * TPR;
-            if (i >= mine) break;
-            float2 a[K], gate[K], yh[K], rh[K], dh[K], u[K], tt[K];
-            load(i, a, gate, yh, rh, dh, u, tt);
+        for (int v = 0; v < NV; ++v)
+          if (col[v]) {
+            float2 y[K], dr[K], gate[K], ay[K], r[K], dh[K];
+            load(s, v, iy2, y, dr, gate, ay, r, dh);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-              const float2 ay = mul2(GATE ? mul2(a[k], gate[k]) : a[k], yh[k]);
-              s0 = fma2(u[k], rh[k], s0);
-              s1 = fma2(ay, tt[k], s1);
-              s2 = fma2(ay, rh[k], s2);
+              const float2 u = mul2(dh[k], wp[v][k]), ayy = mul2(ay[k], y[k]);
+              s0 = fma2(u, r[k], s0);
+              s1 = fma2(ayy, fma2(ir2, u, dr[k]), s1);
+              s2 = fma2(ayy, r[k], s2);
             }
           }
-        float v3[3] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y};
+      }
+      const float v = warp_sum3(s0.x + s0.y, s1.x + s1.y, s2.x + s2.y, lane);
+      if (TPR == 32) return v;
+      const int slot = (lane >> 3) * kPartStride + rank * kRingWarps + warp;
+      if (CL) {
+        // Lane c of each eight serves block c.  Four buffers: a block that sends batch it has
+        // received every warp's sums of batch it - 2, so that none of them still reads those
+        // of batch it - 4.
+        if (lane < 24 && (lane & 7) < cs)
+          st_shared_cluster_u32(mapa_shared(smem_u32(&rc->part[it & 3][slot]), lane & 7),
+                                __float_as_uint(v));
+        __syncwarp();
+        if (lane < cs) mbar_arrive_cluster(mapa_shared(smem_u32(&rc->sums[it & 1]), lane));
+        __syncwarp();
+      } else if (lane < 24 && (lane & 7) == 0) {
+        rc->part[it & 3][slot] = v;
+      }
+      return v;
+    };
+
+    uint32_t it = 0;
+    int s = 0;  // it % S
+    for (int64_t g = rows.g0; g < rows.g1; ++g) {
 #pragma unroll
-        for (int k = 0; k < 3; ++k)
+      for (int v = 0; v < NV; ++v)
+        if (col[v] && has_y) {
+          float2 w[K], q[K];
+          load_wq(v, w);
+          load_gs(g, v, q);
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) v3[k] += __shfl_xor_sync(0xffffffffu, v3[k], o);
-        if (CL) {
-          // Every warp hands its sums to each block of the cluster; lane c serves block c.
-          if (lane < cs) {
-            float* slot = rc->part[it & 1][rank * 8 + warp];
-            const uint32_t dst = mapa_shared(smem_u32(slot), lane);
-#pragma unroll
-            for (int k = 0; k < 3; ++k) st_shared_cluster_u32(dst + 4 * k, __float_as_uint(v3[k]));
-            mbar_arrive_cluster(mapa_shared(smem_u32(&rc->sums), lane));
-          }
-          __syncwarp();
-          wait_cluster(&rc->sums, it & 1u, abort, ctl);
-        } else if (TPR > 32) {
-          if (lane == 0)
-#pragma unroll
-            for (int k = 0; k < 3; ++k) rc->part[it & 1][warp][k] = v3[k];
-          consumers_sync();
+          for (int k = 0; k < K; ++k) a[v][k] = mul2(w[k], q[k]);
         }
-        if (CL || TPR > 32) {
-          const int w0 = CL ? 0 : rw * (TPR / 32), nw = CL ? cs * 8 : TPR / 32;
-          v3[0] = v3[1] = v3[2] = 0.f;
-          for (int w = 0; w < nw; ++w)
+      const int64_t n1 = rows.end(g);
+      int64_t n = rows.begin(g) + rw;
+      float iy, ir, iy1, ir1;
+      factors(n, n1, iy, ir);
+      factors(n + kRows, n1, iy1, ir1);
+      float mysum = sweep1(it, s, n < n1, iy, ir);
+      const int batches = static_cast<int>((n1 - rows.begin(g) + kRows - 1) / kRows);
+      for (int b = 0; b < batches; ++b, n += kRows, ++it) {
+        float iy2, ir2;
+        factors(n + 2 * kRows, n1, iy2, ir2);
+        if (!CL && TPR > 32) consumers_sync();  // the sums of this batch are there
+        float sum = mysum;
+        const int s_next = s + 1 == S ? 0 : s + 1;
+        if (b + 1 < batches) mysum = sweep1(it + 1, s_next, n + kRows < n1, iy1, ir1);
+        if (CL) wait_cluster(&rc->sums[it & 1], (it >> 1) & 1u, abort, ctl);
+        if (TPR > 32) {
+          const float* part = rc->part[it & 3] + (lane >> 3) * kPartStride;
+          const int w0 = CL ? 0 : rw * (TPR / 32), nw = CL ? cs * kRingWarps : TPR / 32;
+          sum = 0.f;
+          if (lane < 24)
+            for (int w = lane & 7; w < nw; w += 8) sum += part[w0 + w];
 #pragma unroll
-            for (int k = 0; k < 3; ++k) v3[k] += rc->part[it & 1][w0 + w][k];
+          for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         }
-        const float c1 = v3[0] * inv_d;
-        const float c2 = p.w_post ? (v3[1] - ir * c1 * v3[2]) * inv_d : 0.f;
-        const float2 kg = pair(-ir * c1), ky = pair(-iy * c2);
-        if (live)
+        const float c1 = __shfl_sync(0xffffffffu, sum, 0) * ir * inv_d;
+        const float s1 = __shfl_sync(0xffffffffu, sum, 8), s2 = __shfl_sync(0xffffffffu, sum, 16);
+        const float c2 = p.w_post ? (s1 - ir * ir * c1 * s2) * inv_d : 0.f;
+        if (n < n1) {
+          const float2 kg = pair(-ir * ir * c1), ky = pair(-iy * iy * c2), py = pair(iy), pr = pair(ir);
 #pragma unroll
-          for (int v = 0; v < NV; ++v) {
-            const int i = t + v * TPR;
-            if (i >= mine) break;
-            float2 a[K], gate[K], yh[K], rh[K], dh[K], u[K], g2[K], o[K];
-            load(i, a, gate, yh, rh, dh, u, g2);
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-              g2[k] = fma2(kg, rh[k], g2[k]);
-              o[k] = mul2(rs, g2[k]);
-              acc_p[v][k] = fma2(dh[k], rh[k], acc_p[v][k]);
-            }
-            const int64_t at = n * nvec + piece0 + i;
-            __stcs(static_cast<uint4*>(p.dx) + at, P::pack(o));
-            if (has_y) {
+          for (int v = 0; v < NV; ++v)
+            if (col[v]) {
+              float2 y[K], g2[K], gate[K], ay[K], r[K], dh[K], o[K];
+              load(s, v, py, y, g2, gate, ay, r, dh);
 #pragma unroll
               for (int k = 0; k < K; ++k) {
-                const float2 yg = mul2(yh[k], g2[k]);
-                const float2 ag = GATE ? mul2(a[k], gate[k]) : a[k];
-                acc_s[v][k] = GATE ? fma2(gate[k], yg, acc_s[v][k]) : add2(yg, acc_s[v][k]);
-                o[k] = fma2(ky, yh[k], mul2(mul2(iy2, ag), g2[k]));
-                if (GATE) g2[k] = mul2(a[k], yg);
+                dh[k] = mul2(dh[k], pr);
+                g2[k] = fma2(kg, r[k], fma2(dh[k], wp[v][k], g2[k]));
+                o[k] = mul2(rs, g2[k]);
+                acc_p[v][k] = fma2(dh[k], r[k], acc_p[v][k]);
               }
-              __stcs(static_cast<uint4*>(p.dy) + at, P::pack(o));
-              if (GATE) store_param_grad(p.dgate, GATE == 2 || std::is_same_v<T, float>, n, i, g2);
+              const int64_t at = n * nvec + piece0 + t + v * TPR;
+              __stcs(static_cast<uint4*>(p.dx) + at, P::pack(o));
+              if (has_y) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                  o[k] = mul2(ay[k], g2[k]);
+                  if (p.w_post) o[k] = fma2(ky, y[k], o[k]);
+                  const float2 yg = mul2(mul2(y[k], py), g2[k]);
+                  acc_s[v][k] = GATE ? fma2(gate[k], yg, acc_s[v][k]) : add2(yg, acc_s[v][k]);
+                  if (GATE) g2[k] = mul2(a[v][k], yg);
+                }
+                __stcs(static_cast<uint4*>(p.dy) + at, P::pack(o));
+                if (GATE) store_gate_grad(GATE == 2 || std::is_same_v<T, float>, n, v, g2);
+              }
             }
-          }
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&rc->empty[s]);
-        iy = iy_next;
-        ir = ir_next;
+        s = s_next;
+        iy = iy1;
+        ir = ir1;
+        iy1 = iy2;
+        ir1 = ir2;
       }
       if (GATE == 0 && (p.w_post || p.gate)) {
         // The group's end: its S into the gate's and the post weight's gradients.
         join(acc_s);
-        if (rw == 0)
 #pragma unroll
-          for (int v = 0; v < NV; ++v) {
-            const int i = t + v * TPR;
-            if (i >= mine) break;
+        for (int v = 0; v < NV; ++v) {
+          if (rw == 0 && col[v]) {
             float2 w[K], q[K];
-            load_wq(i, w);
-            load_gs(g, i, q);
+            load_wq(v, w);
+            load_gs(g, v, q);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
               q[k] = mul2(q[k], acc_s[v][k]);
               w[k] = mul2(mul2(w[k], bs), acc_s[v][k]);
             }
             if (p.w_post)
-              store_f32(p.part_post + static_cast<int64_t>(worker) * p.d, i, q, g > rows.g0);
+              store_f32(p.part_post + static_cast<int64_t>(worker) * p.d, v, q, g > rows.g0);
             if (p.gate) {
               if (p.plan.slices > 1)
-                store_f32(p.part_gate + static_cast<int64_t>(worker) * p.d, i, w, false);
+                store_f32(p.part_gate + static_cast<int64_t>(worker) * p.d, v, w, false);
               else
-                store_param_grad(p.dgate, p.gate_f32, g, i, w);
+                store_gate_grad(p.gate_f32, g, v, w);
             }
           }
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
           for (int k = 0; k < K; ++k) acc_s[v][k] = zero;
+        }
       }
     }
     if (GATE && p.w_post) {
       join(acc_s);
-      if (rw == 0)
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const int i = t + v * TPR;
-          if (i >= mine) break;
+      for (int v = 0; v < NV; ++v) {
 #pragma unroll
-          for (int k = 0; k < K; ++k) acc_s[v][k] = mul2(bs, acc_s[v][k]);
-          store_f32(p.part_post + static_cast<int64_t>(worker) * p.d, i, acc_s[v], false);
-        }
+        for (int k = 0; k < K; ++k) acc_s[v][k] = mul2(bs, acc_s[v][k]);
+        if (rw == 0 && col[v])
+          store_f32(p.part_post + static_cast<int64_t>(worker) * p.d, v, acc_s[v], false);
+      }
     }
     if (pre) {
       join(acc_p);
-      if (rw == 0)
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const int i = t + v * TPR;
-          if (i >= mine) break;
-          store_f32(p.part_pre + static_cast<int64_t>(worker) * p.d, i, acc_p[v], false);
-        }
+      for (int v = 0; v < NV; ++v)
+        if (rw == 0 && col[v])
+          store_f32(p.part_pre + static_cast<int64_t>(worker) * p.d, v, acc_p[v], false);
     }
   }
   // No block leaves while another of its cluster may still write its sums into it.
@@ -1035,9 +995,9 @@ template <class T, int GATE>
 cudaError_t bwd_vec(const NormBwd& p, const DevCtl& c, cudaStream_t s) {
   const int64_t nvec = p.d / Piece<T>::kElems;
   if (nvec <= 32) return bwd_ring<T, 32, 1, GATE, false>(p, c, 1, s);
-  if (nvec <= 64) return bwd_ring<T, 64, 1, GATE, false>(p, c, 1, s);
-  if (nvec <= 128) return bwd_ring<T, 128, 1, GATE, false>(p, c, 1, s);
-  if (nvec <= 256) return bwd_ring<T, 256, 1, GATE, false>(p, c, 1, s);
+  if (nvec <= 64) return bwd_ring<T, 32, 2, GATE, false>(p, c, 1, s);
+  if (nvec <= 128) return bwd_ring<T, 64, 2, GATE, false>(p, c, 1, s);
+  if (nvec <= 256) return bwd_ring<T, 128, 2, GATE, false>(p, c, 1, s);
   if (nvec <= 512) return bwd_ring<T, 256, 2, GATE, false>(p, c, 1, s);
   return bwd_ring<T, 256, 2, GATE, true>(p, c, nvec <= 1024 ? 2 : nvec <= 2048 ? 4 : 8, s);
 }
@@ -1045,7 +1005,7 @@ cudaError_t bwd_vec(const NormBwd& p, const DevCtl& c, cudaStream_t s) {
 template <class T>
 cudaError_t bwd_t(const NormBwd& p, const DevCtl& c, cudaStream_t s) {
   constexpr int E = Piece<T>::kElems;
-  const bool vec = p.d % E == 0 && p.d / E <= 512 * kMaxCluster && p.ldx % E == 0 &&
+  const bool vec = p.d % E == 0 && p.d / E <= 2 * kRingThreads * kMaxCluster && p.ldx % E == 0 &&
                    (!p.y || p.ldy % E == 0) && (!p.d_residual || p.ld_dr % E == 0) &&
                    (!p.d_hidden || p.ld_dh % E == 0) && aligned16(p.x) && aligned16(p.y) &&
                    aligned16(p.d_residual) && aligned16(p.d_hidden) && aligned16(p.w_post) &&

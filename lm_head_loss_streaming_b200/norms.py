@@ -13,7 +13,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from .loss import _ptr, _stream
+from .loss import _ptr
 
 _DTYPE = {torch.bfloat16: _lib.SLM_BF16, torch.float16: _lib.SLM_F16,
           torch.float32: _lib.SLM_F32}
@@ -23,8 +23,8 @@ _DTYPE = {torch.bfloat16: _lib.SLM_BF16, torch.float16: _lib.SLM_F16,
 class BlockNormResult:
     residual: torch.Tensor            # [N, d], the inputs' type; x itself without y
     hidden: torch.Tensor | None       # [N, d]; None without w_pre
-    rstd_post: torch.Tensor | None    # float32 [N]; None without w_post
-    rstd_pre: torch.Tensor | None     # float32 [N]; None without w_pre
+    stats: torch.Tensor               # float32 [2, N]: 1 / sqrt(mean + eps) of the norms of y and
+                                      # of the residual (each written if there is that norm)
     residual_scale: float
     block_scale: float
     weight_offset: float
@@ -39,59 +39,68 @@ class BlockNormGrads:
     dw_post: torch.Tensor | None      # float32 [d]
 
 
-def _check_rows(name, t, shape, dtype, dev):
-    """Rows of ``shape`` on the current device, elements of a row adjacent, rows apart."""
-    if (not t.is_cuda or t.dtype != dtype or t.dim() != 2 or tuple(t.shape) != shape
-            or t.device.index != dev):
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {shape} on the current CUDA "
+def _current(x):
+    """(current device, raw stream handle of its current stream), once x is seen to be on a GPU."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError("the inputs must be CUDA tensors")
+    dev = torch.cuda.current_device()
+    return dev, torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _check_rows(name, t, N, d, dtype, dev):
+    """Rows [N, d] on the current device, elements of a row adjacent, rows apart; returns the
+    distance between rows."""
+    if t.dtype is not dtype or t.shape != (N, d) or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {(N, d)} on the current CUDA "
                          f"device")
-    if t.stride(1) != 1 and shape[1] > 1 or (shape[0] > 1 and t.stride(0) < shape[1]):
+    ld, step = t.stride()
+    if N <= 1:
+        ld = d
+    if (step != 1 and d > 1) or ld < d:
         raise ValueError(f"{name} must have adjacent channels and rows that do not overlap; its "
                          f"strides are {t.stride()}")
+    return ld
 
 
-def _ld(t, d):
-    return d if t is None or t.shape[0] <= 1 else t.stride(0)
-
-
-def _check_block(x, y, w_pre, w_post, gate):
+def _check_block(x, y, w_pre, w_post, gate, dev):
     """Raises ValueError unless the inputs are what the kernels are told; returns
-    (N, d, dtype id, weight dtype id, gate dtype id, gate rows)."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.dtype not in _DTYPE:
+    (N, d, dtype id, row strides of x and y, weight dtype id, gate dtype id, gate rows)."""
+    if x.dim() != 2 or x.dtype not in _DTYPE:
         raise ValueError("x must be a 2-D bf16, fp16 or fp32 CUDA tensor")
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor")
-    dev = torch.cuda.current_device()
+    dtype = x.dtype
     N, d = x.shape
     if d < 1:
         raise ValueError("x has rows of no channels")
-    _check_rows("x", x, (N, d), x.dtype, dev)
-    if y is None:
-        if w_post is not None or gate is not None:
-            raise ValueError("w_post and gate apply to y, which is missing")
-        if w_pre is None:
-            raise ValueError("nothing to do: neither y nor w_pre is given")
-    else:
-        _check_rows("y", y, (N, d), x.dtype, dev)
-    w = w_post if w_post is not None else w_pre
-    for name, t in (("w_post", w_post), ("w_pre", w_pre)):
-        if t is not None and (not t.is_cuda or t.device.index != dev or tuple(t.shape) != (d,)
-                              or not t.is_contiguous() or t.dtype != w.dtype
-                              or t.dtype not in (x.dtype, torch.float32)):
-            raise ValueError(f"{name} must be a contiguous tensor of shape ({d},) on the current "
-                             f"CUDA device, of {x.dtype} or float32 like the other weight")
+    ldx = ldy = _check_rows("x", x, N, d, dtype, dev)
+    if y is not None:
+        ldy = _check_rows("y", y, N, d, dtype, dev)
+    elif w_post is not None or gate is not None:
+        raise ValueError("w_post and gate apply to y, which is missing")
+    elif w_pre is None:
+        raise ValueError("nothing to do: neither y nor w_pre is given")
+    wt = gt = dt = _DTYPE[dtype]
     rows = 0
+    if w_post is not None or w_pre is not None:
+        w_dtype = (w_post if w_post is not None else w_pre).dtype
+        for name, t in (("w_post", w_post), ("w_pre", w_pre)):
+            if t is not None and (t.get_device() != dev or t.shape != (d,) or t.dtype is not w_dtype
+                                  or not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous tensor of shape ({d},) on the "
+                                 f"current CUDA device, of the same type as the other weight")
+        if w_dtype is not dtype and w_dtype is not torch.float32:
+            raise ValueError(f"the weights must be {dtype} or float32")
+        wt = _DTYPE[w_dtype]
     if gate is not None:
-        if (not gate.is_cuda or gate.device.index != dev or gate.dim() not in (1, 2)
-                or gate.shape[-1] != d or not gate.is_contiguous()
-                or gate.dtype not in (x.dtype, torch.float32)):
+        if (gate.get_device() != dev or gate.dim() not in (1, 2) or gate.shape[-1] != d
+                or not gate.is_contiguous()
+                or (gate.dtype is not dtype and gate.dtype is not torch.float32)):
             raise ValueError(f"gate must be a contiguous tensor of shape ({d},) or (rows, {d}) on "
-                             f"the current CUDA device, of {x.dtype} or float32")
+                             f"the current CUDA device, of {dtype} or float32")
         rows = 1 if gate.dim() == 1 else gate.shape[0]
         if N > 0 and (rows == 0 or N % rows != 0):
             raise ValueError(f"gate has {rows} rows; they must divide the {N} rows of x")
-    return (N, d, _DTYPE[x.dtype], _lib.SLM_F32 if w is None else _DTYPE[w.dtype],
-            _lib.SLM_F32 if gate is None else _DTYPE[gate.dtype], rows)
+        gt = _DTYPE[gate.dtype]
+    return N, d, dt, ldx, ldy, wt, gt, rows
 
 
 def _overlap(a, b):
@@ -136,37 +145,38 @@ def block_norm_fwd(x, y=None, w_pre=None, w_post=None, gate=None, residual_scale
     residual.  ``residual`` and ``hidden`` may be preallocated contiguous outputs;
     ``residual`` may be ``x`` itself, which is then updated in place (a backward needs the old
     ``x``)."""
-    N, d, dt, wt, gt, rows = _check_block(x, y, w_pre, w_post, gate)
-    if y is None and residual_scale != 1.0:
-        raise ValueError("residual_scale needs y: without a block the stream is x itself")
-    if y is None and residual is not None:
-        raise ValueError("residual is an output of the block's add: there is none without y")
+    dev, stream = _current(x)
+    N, d, dt, ldx, ldy, wt, gt, rows = _check_block(x, y, w_pre, w_post, gate, dev)
+    if y is None:
+        if residual_scale != 1.0:
+            raise ValueError("residual_scale needs y: without a block the stream is x itself")
+        if residual is not None:
+            raise ValueError("residual is an output of the block's add: there is none without y")
     if w_pre is None and hidden is not None:
         raise ValueError("hidden is made by the norm before the next block: there is no w_pre")
     if not eps > 0:
         raise ValueError("eps must be positive")
-    given = [(n, t) for n, t in (("residual", residual), ("hidden", hidden)) if t is not None]
-    if given:
+    if residual is not None or hidden is not None:
+        given = [(n, t) for n, t in (("residual", residual), ("hidden", hidden)) if t is not None]
         for name, t in given:
-            _check_rows(name, t, (N, d), x.dtype, x.device.index)
+            _check_rows(name, t, N, d, x.dtype, dev)
             if not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
         _check_outputs(given, [("x", x), ("y", y), ("w_pre", w_pre), ("w_post", w_post),
                                ("gate", gate)], ("residual", "x"))
     if y is not None and residual is None:
-        residual = torch.empty(N, d, dtype=x.dtype, device=x.device)
+        residual = torch.empty((N, d), dtype=x.dtype, device=x.device)
     if w_pre is not None and hidden is None:
-        hidden = torch.empty(N, d, dtype=x.dtype, device=x.device)
-    post = None if w_post is None else torch.empty(N, dtype=torch.float32, device=x.device)
-    pre = None if w_pre is None else torch.empty(N, dtype=torch.float32, device=x.device)
-    st = _lib.slm_block_norm_fwd(dt, _ptr(x), _ld(x, d), _ptr(y), _ld(y, d), _ptr(w_post),
-                                 _ptr(w_pre), wt, _ptr(gate), gt, rows, N, d, residual_scale,
-                                 block_scale, eps, weight_offset,
-                                 _ptr(residual) if y is not None else None, _ptr(hidden),
-                                 _ptr(post), _ptr(pre), _stream())
+        hidden = torch.empty((N, d), dtype=x.dtype, device=x.device)
+    stats = torch.empty((2, N), dtype=torch.float32, device=x.device)
+    at = stats.data_ptr()
+    st = _lib.slm_block_norm_fwd(dt, x.data_ptr(), ldx, _ptr(y), ldy, _ptr(w_post), _ptr(w_pre),
+                                 wt, _ptr(gate), gt, rows, N, d, residual_scale, block_scale, eps,
+                                 weight_offset, _ptr(residual), _ptr(hidden), at, at + 4 * N,
+                                 stream)
     _lib.check(st, "slm_block_norm_fwd")
-    return BlockNormResult(x if y is None else residual, hidden, post, pre,
-                           float(residual_scale), float(block_scale), float(weight_offset))
+    return BlockNormResult(x if y is None else residual, hidden, stats, float(residual_scale),
+                           float(block_scale), float(weight_offset))
 
 
 def block_norm_bwd(fwd: BlockNormResult, x, y=None, w_pre=None, w_post=None, gate=None,
@@ -178,36 +188,39 @@ def block_norm_bwd(fwd: BlockNormResult, x, y=None, w_pre=None, w_post=None, gat
     type (summed over the rows that share a gate row), the weights' gradients are float32.
     The sums run in a fixed order.  ``workspace`` may hold a uint8 tensor of
     ``slm_block_norm_workspace_bytes``."""
-    N, d, dt, wt, gt, rows = _check_block(x, y, w_pre, w_post, gate)
-    dev = x.device
+    dev, stream = _current(x)
+    N, d, dt, ldx, ldy, wt, gt, rows = _check_block(x, y, w_pre, w_post, gate, dev)
     if (w_pre is None) != (d_hidden is None) or (d_hidden is None and d_residual is None):
         raise ValueError("d_hidden is the gradient of hidden, made with w_pre: give both or "
                          "neither, and at least one gradient")
-    for name, t in (("d_residual", d_residual), ("d_hidden", d_hidden)):
-        if t is not None:
-            _check_rows(name, t, (N, d), x.dtype, dev.index)
-    for name, t, w in (("rstd_post", fwd.rstd_post, w_post), ("rstd_pre", fwd.rstd_pre, w_pre)):
-        if (t is None) != (w is None) or (t is not None and (t.shape != (N,) or t.device != dev)):
-            raise ValueError("fwd does not come from a forward over these inputs")
+    ld_dr = ld_dh = d
+    if d_residual is not None:
+        ld_dr = _check_rows("d_residual", d_residual, N, d, x.dtype, dev)
+    if d_hidden is not None:
+        ld_dh = _check_rows("d_hidden", d_hidden, N, d, x.dtype, dev)
+    stats = fwd.stats
+    if stats.shape != (2, N) or stats.get_device() != dev:
+        raise ValueError("fwd does not come from a forward over these inputs")
+    device = x.device
     need = _lib.slm_block_norm_workspace_bytes(N, d, rows if N > 0 else 0)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif (workspace.dtype != torch.uint8 or workspace.device != dev
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif (workspace.dtype != torch.uint8 or workspace.device != device
           or not workspace.is_contiguous() or workspace.numel() < need):
-        raise ValueError(f"workspace must be a contiguous uint8 tensor of {need} bytes on {dev}")
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of {need} bytes on {device}")
     g = BlockNormGrads(
-        torch.empty(N, d, dtype=x.dtype, device=dev),
-        None if y is None else torch.empty(N, d, dtype=x.dtype, device=dev),
+        torch.empty((N, d), dtype=x.dtype, device=device),
+        None if y is None else torch.empty((N, d), dtype=x.dtype, device=device),
         None if gate is None else (torch.empty_like(gate) if N > 0 else torch.zeros_like(gate)),
-        None if w_pre is None else torch.empty(d, dtype=torch.float32, device=dev),
-        None if w_post is None else torch.empty(d, dtype=torch.float32, device=dev))
-    st = _lib.slm_block_norm_bwd(dt, _ptr(x), _ld(x, d), _ptr(y), _ld(y, d), _ptr(w_post),
-                                 _ptr(w_pre), wt, _ptr(gate), gt, rows, _ptr(d_residual),
-                                 _ld(d_residual, d), _ptr(d_hidden), _ld(d_hidden, d),
-                                 _ptr(fwd.rstd_post), _ptr(fwd.rstd_pre), N, d,
-                                 fwd.residual_scale, fwd.block_scale, fwd.weight_offset,
-                                 _ptr(g.dx), _ptr(g.dy), _ptr(g.dgate), _ptr(g.dw_post),
-                                 _ptr(g.dw_pre), _ptr(workspace), workspace.numel(), _stream())
+        None if w_pre is None else torch.empty(d, dtype=torch.float32, device=device),
+        None if w_post is None else torch.empty(d, dtype=torch.float32, device=device))
+    at = stats.data_ptr()
+    st = _lib.slm_block_norm_bwd(dt, x.data_ptr(), ldx, _ptr(y), ldy, _ptr(w_post), _ptr(w_pre),
+                                 wt, _ptr(gate), gt, rows, _ptr(d_residual), ld_dr,
+                                 _ptr(d_hidden), ld_dh, at, at + 4 * N, N, d, fwd.residual_scale,
+                                 fwd.block_scale, fwd.weight_offset, g.dx.data_ptr(), _ptr(g.dy),
+                                 _ptr(g.dgate), _ptr(g.dw_post), _ptr(g.dw_pre),
+                                 workspace.data_ptr(), workspace.numel(), stream)
     _lib.check(st, "slm_block_norm_bwd")
     return g
 
@@ -219,14 +232,14 @@ class BlockNorm(torch.autograd.Function):
     def forward(ctx, x, y, w_pre, w_post, gate, residual_scale, block_scale, eps, weight_offset):
         fwd = block_norm_fwd(x, y, w_pre, w_post, gate, residual_scale, block_scale, eps,
                              weight_offset)
-        ctx.save_for_backward(x, y, w_pre, w_post, gate, fwd.rstd_post, fwd.rstd_pre)
+        ctx.save_for_backward(x, y, w_pre, w_post, gate, fwd.stats)
         ctx.scales = (fwd.residual_scale, fwd.block_scale, fwd.weight_offset)
         ctx.set_materialize_grads(False)
         return None if y is None else fwd.residual, fwd.hidden
 
     @staticmethod
     def backward(ctx, d_residual, d_hidden):
-        x, y, w_pre, w_post, gate, rstd_post, rstd_pre = ctx.saved_tensors
+        x, y, w_pre, w_post, gate, stats = ctx.saved_tensors
         if d_residual is None and d_hidden is None:
             return (None,) * 9
         if w_pre is not None and d_hidden is None:   # hidden was not used
@@ -234,7 +247,7 @@ class BlockNorm(torch.autograd.Function):
         d_residual, d_hidden = (
             None if t is None else t if t.stride(-1) == 1 and t.stride(0) >= t.shape[1]
             else t.contiguous() for t in (d_residual, d_hidden))
-        fwd = BlockNormResult(None, None, rstd_post, rstd_pre, *ctx.scales)
+        fwd = BlockNormResult(None, None, stats, *ctx.scales)
         g = block_norm_bwd(fwd, x, y, w_pre, w_post, gate, d_residual, d_hidden)
         return (g.dx, g.dy, None if w_pre is None else g.dw_pre.to(w_pre.dtype),
                 None if w_post is None else g.dw_post.to(w_post.dtype), g.dgate,

@@ -120,4 +120,4 @@ def test_wrapper_refusals():
         with pytest.raises(ValueError):
             block_norm_bwd(f, **{**ok, **kw})
     with pytest.raises(ValueError):
-        block_norm_bwd(BlockNormResult(x, x, None, None, 1.0, 1.0, 0.0), **ok, **g)
+        block_norm_bwd(BlockNormResult(x, x, torch.empty(2, 5, device="cuda"), 1.0, 1.0, 0.0), **ok, **g)
