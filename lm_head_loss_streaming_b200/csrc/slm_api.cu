@@ -1201,7 +1201,6 @@ int slm_block_norm_bwd(int dtype, const void* x, int64_t ldx, const void* y, int
                   reinterpret_cast<float*>(ws + L.pre_off),
                   reinterpret_cast<float*>(ws + L.gate_off)};
   int* status = reinterpret_cast<int*>(ws + L.status_off);
-  SLM_TRY_CUDA(cudaMemsetAsync(status, 0, sizeof(int), s));
   SLM_LAUNCH(kTrNorm, launch_norm_bwd(dtype, p, make_ctl(status), s));
   return SLM_OK;
 }

@@ -174,7 +174,8 @@ __device__ __forceinline__ BwdElem<T> bwd_elem(const NormBwd& p, int64_t n, int6
 }
 
 template <class T>
-__global__ void __launch_bounds__(kAnyThreads) norm_bwd_rows_any(const NormBwd p) {
+__global__ void __launch_bounds__(kAnyThreads) norm_bwd_rows_any(const NormBwd p, int* status) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
   const float inv_d = 1.f / static_cast<float>(p.d);
   for (int64_t n = blockIdx.x; n < p.N; n += gridDim.x) {
     const float iy = p.w_post ? p.rstd_post[n] : 1.f;
@@ -484,7 +485,7 @@ constexpr int kMaxStages = 6;
 constexpr int kPartStride = kMaxCluster * kRingWarps + 8;  // the three sums in banks apart
 
 struct RingCtl {
-  uint64_t full[kMaxStages], empty[kMaxStages], sums[2];
+  uint64_t full[kMaxStages], empty[kMaxStages], sums[4];
   int abort;
   float part[4][3 * kPartStride];
 };
@@ -503,26 +504,6 @@ struct RingCfg {
       128 + kCtl + kScratch + kSeg + static_cast<size_t>(kStages) * kStage;
   static_assert(kStages >= 4, "two batches in use, two under way");
 };
-
-// wait_warp for a barrier that other blocks of the cluster arrive on after storing to this
-// block's shared memory.
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                             const DevCtl& ctl) {
-  const uint32_t a = smem_u32(bar);
-  bool done = mbar_try_wait_cluster(a, parity);
-  if (!done) {
-    const long long t0 = clock64();
-    while (!(done = mbar_try_wait_cluster(a, parity))) {
-      if (*abort) break;
-      if (clock64() - t0 > ctl.timeout_cycles) {
-        *abort = 1;
-        atomicOr(ctl.status, kFlagTimeout);
-        break;
-      }
-    }
-  }
-  return __all_sync(0xffffffffu, done);
-}
 
 // Three sums over the warp with six shuffles instead of fifteen: the first two steps also deal
 // the sums out, so that lanes 8 k .. 8 k + 7 end with sum k (k = 0, 1, 2).
@@ -563,6 +544,9 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1)
   const bool has_y = p.y != nullptr, has_dr = p.d_residual != nullptr, pre = p.w_pre != nullptr;
   volatile int* abort = &rc->abort;
 
+  // The status word is cleared here, without a launch for it: a wait can only run out long
+  // after the first block has started.
+  if (blockIdx.x == 0 && threadIdx.x == 0) *ctl.status = 0;
   for (int i = threadIdx.x; i < C::kSeg / 16; i += kRingThreads + 32)
     reinterpret_cast<uint4*>(zeros)[i] = make_uint4(0, 0, 0, 0);
   if (threadIdx.x == 0) {
@@ -570,7 +554,7 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1)
       mbar_init(&rc->full[s], 1);
       mbar_init(&rc->empty[s], kRingWarps);
     }
-    for (int s = 0; s < 2; ++s) mbar_init(&rc->sums[s], cs * kRingWarps);
+    for (int s = 0; s < 4; ++s) mbar_init(&rc->sums[s], 1);
     rc->abort = 0;
     fence_barrier_init();
   }
@@ -597,6 +581,7 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1)
         const int valid = static_cast<int>(min(static_cast<int64_t>(kRows), n1 - n));
         if (lane == 0) mbar_arrive_expect_tx(&rc->full[s], row_bytes * valid);
         __syncwarp();
+        // Rows that lie end to end come as one copy (short rows would be bound by their number).
         uint8_t* st = ring + s * C::kStage;
         for (int q = lane; q < valid * 5; q += 32) {
           const int arr = q % 5, rw = q / 5;
@@ -605,16 +590,13 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1)
                             : GATE ? p.gate : nullptr;
           const int64_t ld = arr == 0 ? p.ldx : arr == 1 ? p.ldy : arr == 2 ? p.ld_dr
                              : arr == 3 ? p.ld_dh : p.d;
-          if (!src) continue;
-          const int64_t at = (n + rw) * ld * static_cast<int64_t>(sizeof(T)) +
-                             static_cast<int64_t>(piece0) * 16;
-          if (arr < 4)
-            bulk_load(st + (arr * kRows + rw) * C::kSeg, static_cast<const uint8_t*>(src) + at,
-                      bytes, &rc->full[s]);
-          else
-            bulk_load(st + 4 * kRows * C::kSeg + rw * C::kGateSeg,
-                      static_cast<const uint8_t*>(src) + at * (GATE == 2 ? 2 : 1), gbytes,
-                      &rc->full[s]);
+          const bool dense = !CL && ld == p.d;
+          if (!src || (dense && rw > 0)) continue;
+          const uint32_t size = (arr < 4 ? bytes : gbytes);
+          const int64_t at = ((n + rw) * ld * static_cast<int64_t>(sizeof(T)) +
+                              static_cast<int64_t>(piece0) * 16) * (arr < 4 ? 1 : GATE == 2 ? 2 : 1);
+          bulk_load(st + arr * kRows * C::kSeg + rw * size, static_cast<const uint8_t*>(src) + at,
+                    dense ? size * valid : size, &rc->full[s]);
         }
         __syncwarp();
       }
@@ -709,7 +691,7 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const bool there = q == 1 ? has_y : q == 2 ? has_dr : pre;
-      arr[q] = (there ? ring + (q * kRows + rw) * C::kSeg : zeros) + t * 16;
+      arr[q] = (there ? ring + q * kRows * C::kSeg + rw * mine * 16 : zeros) + t * 16;
       step[q] = there ? C::kStage : 0;
     }
     // This thread's piece v of a stage: y, dr, the gate, i_y a (gate), r and dh.
@@ -720,7 +702,8 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1)
       P::unpack(*reinterpret_cast<const uint4*>(arr[2] + s * step[2] + v * TPR * 16), dr);
       P::unpack(*reinterpret_cast<const uint4*>(arr[3] + s * step[3] + v * TPR * 16), dh);
       if (GATE) {
-        const uint8_t* sg = ring + s * C::kStage + 4 * kRows * C::kSeg + rw * C::kGateSeg;
+        const uint8_t* sg = ring + s * C::kStage + 4 * kRows * C::kSeg +
+                            rw * mine * (GATE == 2 ? 32 : 16);
         const int i = t + v * TPR;
         if (GATE == 1) {
           P::unpack(reinterpret_cast<const uint4*>(sg)[i], gate);
@@ -764,14 +747,15 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1)
       if (TPR == 32) return v;
       const int slot = (lane >> 3) * kPartStride + rank * kRingWarps + warp;
       if (CL) {
-        // Lane c of each eight serves block c.  Four buffers: a block that sends batch it has
-        // received every warp's sums of batch it - 2, so that none of them still reads those
-        // of batch it - 4.
+        // Lane c of each eight serves block c; the stores count themselves on its barrier, so
+        // that nothing waits for this thread's earlier stores to global memory.  Four buffers
+        // and barriers: a block that sends batch it has received every warp's sums of batch
+        // it - 2, which each sent after it had received and read those of batch it - 4.
+        if (threadIdx.x == 0)
+          mbar_arrive_expect_tx(&rc->sums[it & 3], static_cast<uint32_t>(cs * kRingWarps * 12));
         if (lane < 24 && (lane & 7) < cs)
-          st_shared_cluster_u32(mapa_shared(smem_u32(&rc->part[it & 3][slot]), lane & 7),
-                                __float_as_uint(v));
-        __syncwarp();
-        if (lane < cs) mbar_arrive_cluster(mapa_shared(smem_u32(&rc->sums[it & 1]), lane));
+          st_async_cluster(mapa_shared(smem_u32(&rc->part[it & 3][slot]), lane & 7), v,
+                           mapa_shared(smem_u32(&rc->sums[it & 3]), lane & 7));
         __syncwarp();
       } else if (lane < 24 && (lane & 7) == 0) {
         rc->part[it & 3][slot] = v;
@@ -805,7 +789,7 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1)
         float sum = mysum;
         const int s_next = s + 1 == S ? 0 : s + 1;
         if (b + 1 < batches) mysum = sweep1(it + 1, s_next, n + kRows < n1, iy1, ir1);
-        if (CL) wait_cluster(&rc->sums[it & 1], (it >> 1) & 1u, abort, ctl);
+        if (CL) wait_warp(&rc->sums[it & 3], (it >> 2) & 1u, abort, ctl);
         if (TPR > 32) {
           const float* part = rc->part[it & 3] + (lane >> 3) * kPartStride;
           const int w0 = CL ? 0 : rw * (TPR / 32), nw = CL ? cs * kRingWarps : TPR / 32;
@@ -1018,7 +1002,7 @@ cudaError_t bwd_t(const NormBwd& p, const DevCtl& c, cudaStream_t s) {
     return bwd_vec<T, 1>(p, c, s);
   }
   const int64_t grid = std::min<int64_t>(p.N, int64_t(1) << 20);
-  norm_bwd_rows_any<T><<<static_cast<unsigned>(grid), kAnyThreads, 0, s>>>(p);
+  norm_bwd_rows_any<T><<<static_cast<unsigned>(grid), kAnyThreads, 0, s>>>(p, c.status);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !(p.w_post || p.w_pre || p.plan.shared_gate)) return e;
   const dim3 gc(static_cast<unsigned>((p.d + 127) / 128), static_cast<unsigned>(p.plan.blocks));

@@ -237,9 +237,13 @@ __device__ __forceinline__ void st_shared_cluster_u32(uint32_t cluster_addr, uin
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 
-__device__ __forceinline__ void st_shared_cluster_v4(uint32_t cluster_addr, float4 v) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "f"(v.x),
-               "f"(v.y), "f"(v.z), "f"(v.w)
+// The same, counting its four bytes on an mbarrier of that CTA once it has landed (both
+// addresses from mapa_shared, of the same CTA).
+__device__ __forceinline__ void st_async_cluster(uint32_t cluster_addr, float v,
+                                                 uint32_t cluster_bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
+                   cluster_addr),
+               "r"(__float_as_uint(v)), "r"(cluster_bar)
                : "memory");
 }
 

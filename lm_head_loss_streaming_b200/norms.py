@@ -8,6 +8,7 @@ and ``slm_block_norm_bwd``.
 
 from __future__ import annotations
 
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -43,7 +44,7 @@ def _current(x):
     """(current device, raw stream handle of its current stream), once x is seen to be on a GPU."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError("the inputs must be CUDA tensors")
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()
     return dev, torch._C._cuda_getCurrentRawStream(dev)
 
 
@@ -56,18 +57,25 @@ def _check_rows(name, t, N, d, dtype, dev):
     ld, step = t.stride()
     if N <= 1:
         ld = d
-    if (step != 1 and d > 1) or ld < d:
+    if ld < d or (step != 1 and d > 1):
         raise ValueError(f"{name} must have adjacent channels and rows that do not overlap; its "
                          f"strides are {t.stride()}")
     return ld
 
 
+def _check_weight(name, t, d, dtype, dev):
+    if t.shape != (d,) or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape ({d},) on the "
+                         f"current CUDA device (both weights of the inputs' type, or float32)")
+
+
 def _check_block(x, y, w_pre, w_post, gate, dev):
     """Raises ValueError unless the inputs are what the kernels are told; returns
     (N, d, dtype id, row strides of x and y, weight dtype id, gate dtype id, gate rows)."""
-    if x.dim() != 2 or x.dtype not in _DTYPE:
-        raise ValueError("x must be a 2-D bf16, fp16 or fp32 CUDA tensor")
     dtype = x.dtype
+    dt = _DTYPE.get(dtype)
+    if dt is None or x.dim() != 2:
+        raise ValueError("x must be a 2-D bf16, fp16 or fp32 CUDA tensor")
     N, d = x.shape
     if d < 1:
         raise ValueError("x has rows of no channels")
@@ -78,29 +86,35 @@ def _check_block(x, y, w_pre, w_post, gate, dev):
         raise ValueError("w_post and gate apply to y, which is missing")
     elif w_pre is None:
         raise ValueError("nothing to do: neither y nor w_pre is given")
-    wt = gt = dt = _DTYPE[dtype]
+    wt = gt = dt
     rows = 0
-    if w_post is not None or w_pre is not None:
-        w_dtype = (w_post if w_post is not None else w_pre).dtype
-        for name, t in (("w_post", w_post), ("w_pre", w_pre)):
-            if t is not None and (t.get_device() != dev or t.shape != (d,) or t.dtype is not w_dtype
-                                  or not t.is_contiguous()):
-                raise ValueError(f"{name} must be a contiguous tensor of shape ({d},) on the "
-                                 f"current CUDA device, of the same type as the other weight")
-        if w_dtype is not dtype and w_dtype is not torch.float32:
-            raise ValueError(f"the weights must be {dtype} or float32")
-        wt = _DTYPE[w_dtype]
+    if w_pre is not None or w_post is not None:
+        w_dtype = (w_pre if w_pre is not None else w_post).dtype
+        if w_dtype is not dtype:
+            if w_dtype is not torch.float32:
+                raise ValueError(f"the weights must be {dtype} or float32")
+            wt = _lib.SLM_F32
+        if w_pre is not None:
+            _check_weight("w_pre", w_pre, d, w_dtype, dev)
+        if w_post is not None:
+            _check_weight("w_post", w_post, d, w_dtype, dev)
     if gate is not None:
-        if (gate.get_device() != dev or gate.dim() not in (1, 2) or gate.shape[-1] != d
-                or not gate.is_contiguous()
-                or (gate.dtype is not dtype and gate.dtype is not torch.float32)):
+        shape = gate.shape
+        if (gate.get_device() != dev or len(shape) not in (1, 2) or shape[-1] != d
+                or not gate.is_contiguous() or gate.dtype not in (dtype, torch.float32)):
             raise ValueError(f"gate must be a contiguous tensor of shape ({d},) or (rows, {d}) on "
                              f"the current CUDA device, of {dtype} or float32")
-        rows = 1 if gate.dim() == 1 else gate.shape[0]
+        rows = 1 if len(shape) == 1 else shape[0]
         if N > 0 and (rows == 0 or N % rows != 0):
             raise ValueError(f"gate has {rows} rows; they must divide the {N} rows of x")
-        gt = _DTYPE[gate.dtype]
+        if gate.dtype is not dtype:
+            gt = _lib.SLM_F32
     return N, d, dt, ldx, ldy, wt, gt, rows
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(N, d, rows):
+    return _lib.slm_block_norm_workspace_bytes(N, d, rows)
 
 
 def _overlap(a, b):
@@ -165,18 +179,19 @@ def block_norm_fwd(x, y=None, w_pre=None, w_post=None, gate=None, residual_scale
         _check_outputs(given, [("x", x), ("y", y), ("w_pre", w_pre), ("w_post", w_post),
                                ("gate", gate)], ("residual", "x"))
     if y is not None and residual is None:
-        residual = torch.empty((N, d), dtype=x.dtype, device=x.device)
+        residual = torch.empty_like(x) if ldx == d else x.new_empty((N, d))
     if w_pre is not None and hidden is None:
-        hidden = torch.empty((N, d), dtype=x.dtype, device=x.device)
-    stats = torch.empty((2, N), dtype=torch.float32, device=x.device)
+        hidden = torch.empty_like(x) if ldx == d else x.new_empty((N, d))
+    stats = x.new_empty((2, N), dtype=torch.float32)
     at = stats.data_ptr()
     st = _lib.slm_block_norm_fwd(dt, x.data_ptr(), ldx, _ptr(y), ldy, _ptr(w_post), _ptr(w_pre),
                                  wt, _ptr(gate), gt, rows, N, d, residual_scale, block_scale, eps,
                                  weight_offset, _ptr(residual), _ptr(hidden), at, at + 4 * N,
                                  stream)
-    _lib.check(st, "slm_block_norm_fwd")
-    return BlockNormResult(x if y is None else residual, hidden, stats, float(residual_scale),
-                           float(block_scale), float(weight_offset))
+    if st:
+        raise _lib.SLMError(st, "slm_block_norm_fwd")
+    return BlockNormResult(x if y is None else residual, hidden, stats, residual_scale,
+                           block_scale, weight_offset)
 
 
 def block_norm_bwd(fwd: BlockNormResult, x, y=None, w_pre=None, w_post=None, gate=None,
@@ -202,18 +217,17 @@ def block_norm_bwd(fwd: BlockNormResult, x, y=None, w_pre=None, w_post=None, gat
     if stats.shape != (2, N) or stats.get_device() != dev:
         raise ValueError("fwd does not come from a forward over these inputs")
     device = x.device
-    need = _lib.slm_block_norm_workspace_bytes(N, d, rows if N > 0 else 0)
+    need = _workspace_bytes(N, d, rows if N > 0 else 0)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = x.new_empty(need, dtype=torch.uint8)
     elif (workspace.dtype != torch.uint8 or workspace.device != device
           or not workspace.is_contiguous() or workspace.numel() < need):
         raise ValueError(f"workspace must be a contiguous uint8 tensor of {need} bytes on {device}")
     g = BlockNormGrads(
-        torch.empty((N, d), dtype=x.dtype, device=device),
-        None if y is None else torch.empty((N, d), dtype=x.dtype, device=device),
-        None if gate is None else (torch.empty_like(gate) if N > 0 else torch.zeros_like(gate)),
-        None if w_pre is None else torch.empty(d, dtype=torch.float32, device=device),
-        None if w_post is None else torch.empty(d, dtype=torch.float32, device=device))
+        x.new_empty((N, d)), None if y is None else x.new_empty((N, d)),
+        None if gate is None else torch.empty_like(gate) if N > 0 else torch.zeros_like(gate),
+        None if w_pre is None else x.new_empty(d, dtype=torch.float32),
+        None if w_post is None else x.new_empty(d, dtype=torch.float32))
     at = stats.data_ptr()
     st = _lib.slm_block_norm_bwd(dt, x.data_ptr(), ldx, _ptr(y), ldy, _ptr(w_post), _ptr(w_pre),
                                  wt, _ptr(gate), gt, rows, _ptr(d_residual), ld_dr,
@@ -221,7 +235,8 @@ def block_norm_bwd(fwd: BlockNormResult, x, y=None, w_pre=None, w_post=None, gat
                                  fwd.block_scale, fwd.weight_offset, g.dx.data_ptr(), _ptr(g.dy),
                                  _ptr(g.dgate), _ptr(g.dw_post), _ptr(g.dw_pre),
                                  workspace.data_ptr(), workspace.numel(), stream)
-    _lib.check(st, "slm_block_norm_bwd")
+    if st:
+        raise _lib.SLMError(st, "slm_block_norm_bwd")
     return g
 
 
