@@ -487,6 +487,7 @@ constexpr int kPartStride = kMaxCluster * kRingWarps + 8;  // the three sums in 
 struct RingCtl {
   uint64_t full[kMaxStages], empty[kMaxStages], sums[4];
   int abort;
+  float2 factor[kMaxStages][kRingWarps];  // i_y, i_r of the batch's rows
   float part[4][3 * kPartStride];
 };
 
@@ -570,6 +571,16 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1)
     const uint32_t row_bytes = bytes * (has_y + has_dr + 2 * pre) + (GATE ? gbytes : 0);
     uint32_t it = 0;
     bool ok = true;
+    // The norms' factors of row n + lane (lanes below kRows), fetched a batch ahead.
+    auto factors = [&](int64_t n) {
+      float2 f = make_float2(1.f, 0.f);
+      if (lane < kRows && n + lane < p.N) {
+        if (p.w_post) f.x = __ldg(p.rstd_post + n + lane);
+        if (pre) f.y = __ldg(p.rstd_pre + n + lane);
+      }
+      return f;
+    };
+    float2 f = factors(rows.begin(rows.g0));
     for (int64_t g = rows.g0; ok && g < rows.g1; ++g) {
       const int64_t n1 = rows.end(g);
       for (int64_t n = rows.begin(g); n < n1; n += kRows, ++it) {
@@ -579,8 +590,11 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1)
           break;
         }
         const int valid = static_cast<int>(min(static_cast<int64_t>(kRows), n1 - n));
+        if (lane < kRows) rc->factor[s][lane] = f;
+        __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(&rc->full[s], row_bytes * valid);
         __syncwarp();
+        f = factors(n + kRows < n1 ? n + kRows : rows.begin(g + 1));
         // Rows that lie end to end come as one copy (short rows would be bound by their number).
         uint8_t* st = ring + s * C::kStage;
         for (int q = lane; q < valid * 5; q += 32) {
@@ -681,10 +695,6 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1)
       else
         reinterpret_cast<uint4*>(static_cast<T*>(p.dgate) + row * p.d)[piece0 + t + v * TPR] = P::pack(w);
     };
-    auto factors = [&](int64_t n, int64_t n1, float& iy, float& ir) {
-      iy = p.w_post && n < n1 ? __ldg(p.rstd_post + n) : 1.f;
-      ir = pre && n < n1 ? __ldg(p.rstd_pre + n) : 0.f;
-    };
     // Where this thread's pieces of x, y, dr and dh lie in stage 0, and how far on in the next.
     const uint8_t* arr[4];
     int step[4];
@@ -724,11 +734,11 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1)
     };
     // Sweep 1: sum u r, sum a yh (dr + i_r u), sum a yh r over the rows of the batch, handed on
     // to the warps that share a row (the factor i_r of rh comes in afterwards).
-    auto sweep1 = [&](uint32_t it, int s, bool live, float iy, float ir) {
+    auto sweep1 = [&](uint32_t it, int s, bool live) {
       wait_warp(&rc->full[s], (it / S) & 1u, abort, ctl);
       float2 s0 = zero, s1 = zero, s2 = zero;
       if (live) {
-        const float2 iy2 = pair(iy), ir2 = pair(ir);
+        const float2 f = rc->factor[s][rw], iy2 = pair(f.x), ir2 = pair(f.y);
 #pragma unroll
         for (int v = 0; v < NV; ++v)
           if (col[v]) {
@@ -777,18 +787,13 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1)
         }
       const int64_t n1 = rows.end(g);
       int64_t n = rows.begin(g) + rw;
-      float iy, ir, iy1, ir1;
-      factors(n, n1, iy, ir);
-      factors(n + kRows, n1, iy1, ir1);
-      float mysum = sweep1(it, s, n < n1, iy, ir);
+      float mysum = sweep1(it, s, n < n1);
       const int batches = static_cast<int>((n1 - rows.begin(g) + kRows - 1) / kRows);
       for (int b = 0; b < batches; ++b, n += kRows, ++it) {
-        float iy2, ir2;
-        factors(n + 2 * kRows, n1, iy2, ir2);
         if (!CL && TPR > 32) consumers_sync();  // the sums of this batch are there
         float sum = mysum;
         const int s_next = s + 1 == S ? 0 : s + 1;
-        if (b + 1 < batches) mysum = sweep1(it + 1, s_next, n + kRows < n1, iy1, ir1);
+        if (b + 1 < batches) mysum = sweep1(it + 1, s_next, n + kRows < n1);
         if (CL) wait_warp(&rc->sums[it & 3], (it >> 2) & 1u, abort, ctl);
         if (TPR > 32) {
           const float* part = rc->part[it & 3] + (lane >> 3) * kPartStride;
@@ -799,6 +804,8 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1)
 #pragma unroll
           for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         }
+        const float2 f = rc->factor[s][rw];
+        const float iy = f.x, ir = f.y;
         const float c1 = __shfl_sync(0xffffffffu, sum, 0) * ir * inv_d;
         const float s1 = __shfl_sync(0xffffffffu, sum, 8), s2 = __shfl_sync(0xffffffffu, sum, 16);
         const float c2 = p.w_post ? (s1 - ir * ir * c1 * s2) * inv_d : 0.f;
@@ -823,9 +830,14 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1)
                 for (int k = 0; k < K; ++k) {
                   o[k] = mul2(ay[k], g2[k]);
                   if (p.w_post) o[k] = fma2(ky, y[k], o[k]);
-                  const float2 yg = mul2(mul2(y[k], py), g2[k]);
-                  acc_s[v][k] = GATE ? fma2(gate[k], yg, acc_s[v][k]) : add2(yg, acc_s[v][k]);
-                  if (GATE) g2[k] = mul2(a[v][k], yg);
+                  g2[k] = mul2(py, g2[k]);
+                  if (GATE) {
+                    const float2 yg = mul2(y[k], g2[k]);
+                    acc_s[v][k] = fma2(gate[k], yg, acc_s[v][k]);
+                    g2[k] = mul2(a[v][k], yg);
+                  } else {
+                    acc_s[v][k] = fma2(y[k], g2[k], acc_s[v][k]);
+                  }
                 }
                 __stcs(static_cast<uint4*>(p.dy) + at, P::pack(o));
                 if (GATE) store_gate_grad(GATE == 2 || std::is_same_v<T, float>, n, v, g2);
@@ -835,10 +847,6 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&rc->empty[s]);
         s = s_next;
-        iy = iy1;
-        ir = ir1;
-        iy1 = iy2;
-        ir1 = ir2;
       }
       if (GATE == 0 && (p.w_post || p.gate)) {
         // The group's end: its S into the gate's and the post weight's gradients.
