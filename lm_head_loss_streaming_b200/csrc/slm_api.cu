@@ -525,24 +525,38 @@ bool make_map_stack(CUtensorMap* m, const void* base, int64_t inner, int64_t out
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Tile grid of one product and its tile width: the width (256 or 128 columns) whose rounds of
-// tiles over the pairs take less time; a tile's time is taken as proportional to its width.
+// Tile grid of one product and its tile width (512, 256 or 128 columns): the one whose rounds
+// of tiles over the CTA pairs are estimated to take least.  Per 64-wide K block a tile takes
+// its MMAs (27 TFLOP/s per pair) or its operands' way from L2 (9.3 TB/s shared by the pairs
+// that are busy), whichever is longer; both rates as measured on the products of 4096 x 4096
+// matrices.  A round also costs its epilogue, about 1 us per 128 columns.  Wide tiles read
+// less from L2 per flop, narrow ones leave fewer pairs idle: 4096 x 4096 updates take 178 us at
+// 128 columns and 98 at 512, 256 x 256 ones run only on as many pairs as there are tiles.
 int orth_tiles(OrthGemm* g, int64_t rows, int64_t cols, int64_t k, int64_t batch, bool sym) {
   const int64_t pairs = std::max(1, sm_count() / 2);
-  int best = 256;
-  int64_t best_cost = 0;
-  for (int bn : {256, 128}) {
+  int best = 0;
+  double best_cost = 0;
+  for (int bn : {512, 256, 128}) {
     const int64_t nm = ceil_div(rows, kPairM), nn = ceil_div(cols, bn);
-    const int64_t w = kPairM / bn;
-    const int64_t per = sym ? w * (nm - 1) * nm / 2 + nn : nm * nn;
-    const int64_t cost = ceil_div(per * batch, pairs) * bn;
-    if (best_cost == 0 || cost < best_cost) {
+    // Symmetric: the tiles that reach below the diagonal.
+    const int64_t per = !sym ? nm * nn : bn == 512 ? (nm + 1) * (nm + 1) / 4
+                        : (kPairM / bn) * (nm - 1) * nm / 2 + nn;
+    const int64_t units = per * batch;
+    const double kb = static_cast<double>(ceil_div(k, kBK));
+    auto round = [&](int64_t busy) {
+      const double mma = 2.0 * kPairM * bn * kBK / 27e12;
+      const double l2 = (kPairM + bn) * kBK * 2.0 * static_cast<double>(busy) / 9.3e12;
+      return kb * std::max(mma, l2) + 1e-6 * bn / 128;
+    };
+    const double cost = static_cast<double>(units / pairs) * round(pairs) +
+                        (units % pairs != 0 ? round(units % pairs) : 0.0);
+    if (best == 0 || cost < best_cost) {
       best_cost = cost;
       best = bn;
       g->num_m = static_cast<int>(nm);
       g->num_n = static_cast<int>(nn);
       g->units_per = static_cast<int>(per);
-      g->num_units = static_cast<int>(per * batch);
+      g->num_units = static_cast<int>(units);
     }
   }
   g->k_blocks = static_cast<int>(ceil_div(k, kBK));
@@ -1255,7 +1269,7 @@ int slm_orthogonalize(int dtype, const void* grad, int64_t ld, int64_t batch_str
   square.diag_out = diag[1];
   update.ld = L.ldx;
   update.diag_in = diag[1];
-  update.diag_n = k;
+  gram.diag_n = square.diag_n = update.diag_n = k;
   update.lo = lo;
   update.out = static_cast<__nv_bfloat16*>(out);
   update.tall = tall ? 1 : 0;
@@ -1267,23 +1281,22 @@ int slm_orthogonalize(int dtype, const void* grad, int64_t ld, int64_t batch_str
   for (int i = 0; i < 2; ++i) {
     // The A and B operands of X X^T; of X^T X both are MN-major.
     if (!make_map_stack(&xa[i], hi[i], n, m, L.ldx, batch, 64, tall ? 64 : kBM)) return SLM_ERR_CUDA;
-    if (!make_map_stack(&xb[i], hi[i], n, m, L.ldx, batch, 64, tall ? 64 : bn_gram / 2))
+    if (!make_map_stack(&xb[i], hi[i], n, m, L.ldx, batch, 64, tall ? 64 : std::min(bn_gram, 256) / 2))
       return SLM_ERR_CUDA;
   }
   if (!make_map_stack(&ra, mat[0], k, k, L.ldk, batch, 64, kBM) ||
-      !make_map_stack(&rb, mat[0], k, k, L.ldk, batch, 64, bn_square / 2) ||
+      !make_map_stack(&rb, mat[0], k, k, L.ldk, batch, 64, std::min(bn_square, 256) / 2) ||
       !make_map_stack(&ba, mat[1], k, k, L.ldk, batch, 64, kBM) ||
-      !make_map_stack(&bb, mat[1], k, k, L.ldk, batch, 64, bn_update / 2))
+      !make_map_stack(&bb, mat[1], k, k, L.ldk, batch, 64, std::min(bn_update, 256) / 2))
     return SLM_ERR_CUDA;
   CUtensorMap xu[2];  // X in the update: X B has it as K-major A, B X as MN-major B
   for (int i = 0; i < 2; ++i)
     if (!make_map_stack(&xu[i], hi[i], n, m, L.ldx, batch, 64, tall ? kBM : 64)) return SLM_ERR_CUDA;
 
-  SLM_TRY_CUDA(cudaMemsetAsync(status, 0, sizeof(int), s));
   const DevCtl ctl = make_ctl(status);
   const OrthPrep prep{grad, m, n, ld, batch_stride, L.ldx, momentum, static_cast<float>(beta),
                       static_cast<float>(1.0 - beta), eps, nesterov,
-                      reinterpret_cast<double*>(ws + L.sums_off), hi[0], lo};
+                      reinterpret_cast<double*>(ws + L.sums_off), hi[0], lo, status};
   SLM_LAUNCH(kTrOrth, launch_orth_prep(dtype, prep, batch, s));
   for (int i = 0; i < steps; ++i) {
     const int cur = i & 1;

@@ -312,6 +312,7 @@ struct OrthPrep {
   int nesterov;
   double* sums;  // [batch][kOrthSums]
   __half *hi, *lo;
+  int* status;
 };
 // One product over the stack: rows x cols outputs per matrix, tiles of 256 x bn.
 struct OrthGemm {
@@ -324,7 +325,7 @@ struct OrthGemm {
   const __half* hi_in;
   __half *hi_out, *lo;
   __nv_bfloat16* out;
-  int64_t diag_n;  // kUpdate: entries of D_B per matrix
+  int64_t diag_n;  // entries of a diagonal per matrix
   float a, b, c;
   int tall, out_vec;
 };

@@ -41,40 +41,89 @@ constexpr float kScaleX = 16384.f;  // 2^14
 constexpr float kScaleA = 16384.f;
 constexpr float kScaleB = 4096.f;  // 2^12
 
-template <class T>
-__device__ __forceinline__ float ld_elem(const void* p, int64_t i);
-template <>
-__device__ __forceinline__ float ld_elem<float>(const void* p, int64_t i) {
-  return static_cast<const float*>(p)[i];
-}
-template <>
-__device__ __forceinline__ float ld_elem<__nv_bfloat16>(const void* p, int64_t i) {
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
-template <>
-__device__ __forceinline__ float ld_elem<__half>(const void* p, int64_t i) {
-  return __half2float(static_cast<const __half*>(p)[i]);
-}
-
 constexpr int kPrepThreads = 256;
 
+// V consecutive elements (V = 8: whole 16-byte pieces; V = 1).
+template <class T, int V>
+__device__ __forceinline__ void ld_elems(const T* p, float (&v)[V]) {
+  if constexpr (V == 1) {
+    if constexpr (std::is_same_v<T, float>)
+      v[0] = *p;
+    else if constexpr (std::is_same_v<T, __half>)
+      v[0] = __half2float(*p);
+    else
+      v[0] = __bfloat162float(*p);
+  } else if constexpr (std::is_same_v<T, float>) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 f;
+      if constexpr (std::is_same_v<T, __half>)
+        f = __half22float2(*reinterpret_cast<const __half2*>(&a[i]));
+      else
+        f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&a[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+}
+
+// Where group `i` of V elements of a matrix lies in the gradient, in the momentum (contiguous)
+// and in hi / lo (rows of ldx).
+struct OrthAt {
+  int64_t grad, mom, x;
+};
+template <int V>
+__device__ __forceinline__ OrthAt orth_at(const OrthPrep& p, int64_t b, int64_t i) {
+  const int64_t per_row = p.n / V;
+  int64_t r, c;
+  if (p.m * per_row < (int64_t(1) << 32)) {
+    r = static_cast<uint32_t>(i) / static_cast<uint32_t>(per_row);
+    c = static_cast<uint32_t>(i) - static_cast<uint32_t>(r) * static_cast<uint32_t>(per_row);
+  } else {
+    r = i / per_row;
+    c = i - r * per_row;
+  }
+  c *= V;
+  return {b * p.grad_batch + r * p.ldg + c, (b * p.m + r) * p.n + c, (b * p.m + r) * p.ldx + c};
+}
+
 // Momentum update and the partial sums of u^2 (64 bits: the squares of fp32 gradients may
-// leave fp32's range).  Block (i, b): rows i, i + gridDim.x, ... of matrix b.
-template <class T>
+// leave fp32's range).  Blocks (., b) share matrix b.
+template <class T, int V>
 __global__ void __launch_bounds__(kPrepThreads) orth_moment(const OrthPrep p) {
   const int64_t b = blockIdx.y;
+  const int64_t groups = p.m * (p.n / V);
+  if (blockIdx.x == 0 && b == 0 && threadIdx.x == 0) *p.status = 0;
   double s = 0.0;
-  for (int64_t r = blockIdx.x; r < p.m; r += gridDim.x) {
-    const int64_t g0 = b * p.grad_batch + r * p.ldg, m0 = (b * p.m + r) * p.n;
-    for (int64_t c = threadIdx.x; c < p.n; c += kPrepThreads) {
-      float u = ld_elem<T>(p.grad, g0 + c);
-      if (p.momentum) {
-        const float mom = p.beta * p.momentum[m0 + c] + p.rest * u;
-        p.momentum[m0 + c] = mom;
-        u = p.nesterov ? p.beta * mom + p.rest * u : mom;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPrepThreads + threadIdx.x; i < groups;
+       i += static_cast<int64_t>(gridDim.x) * kPrepThreads) {
+    const OrthAt at = orth_at<V>(p, b, i);
+    float u[V];
+    ld_elems<T, V>(static_cast<const T*>(p.grad) + at.grad, u);
+    if (p.momentum) {
+      float mom[V];
+      ld_elems<float, V>(p.momentum + at.mom, mom);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        mom[e] = p.beta * mom[e] + p.rest * u[e];
+        u[e] = p.nesterov ? p.beta * mom[e] + p.rest * u[e] : mom[e];
       }
-      s += static_cast<double>(u) * static_cast<double>(u);
+      if constexpr (V == 8) {
+        float4* o = reinterpret_cast<float4*>(p.momentum + at.mom);
+        o[0] = make_float4(mom[0], mom[1], mom[2], mom[3]);
+        o[1] = make_float4(mom[4], mom[5], mom[6], mom[7]);
+      } else {
+        p.momentum[at.mom] = mom[0];
+      }
     }
+#pragma unroll
+    for (int e = 0; e < V; ++e) s = fma(static_cast<double>(u[e]), static_cast<double>(u[e]), s);
   }
   __shared__ double part[kPrepThreads / 32];
 #pragma unroll
@@ -89,7 +138,7 @@ __global__ void __launch_bounds__(kPrepThreads) orth_moment(const OrthPrep p) {
 }
 
 // X = u / (||u|| + eps) as hi + lo; the norm from the partial sums, added in a fixed order.
-template <class T>
+template <class T, int V>
 __global__ void __launch_bounds__(kPrepThreads) orth_scale(const OrthPrep p, int nsums) {
   __shared__ float inv_sh;
   const int64_t b = blockIdx.y;
@@ -103,33 +152,50 @@ __global__ void __launch_bounds__(kPrepThreads) orth_scale(const OrthPrep p, int
   }
   __syncthreads();
   const float inv = inv_sh;
-  for (int64_t r = blockIdx.x; r < p.m; r += gridDim.x) {
-    const int64_t g0 = b * p.grad_batch + r * p.ldg, m0 = (b * p.m + r) * p.n;
-    const int64_t x0 = (b * p.m + r) * p.ldx;
-    for (int64_t c = threadIdx.x; c < p.n; c += kPrepThreads) {
-      float u = ld_elem<T>(p.grad, g0 + c);
-      if (p.momentum) {
-        const float mom = p.momentum[m0 + c];
-        u = p.nesterov ? p.beta * mom + p.rest * u : mom;
-      }
-      const float x = u * inv;
-      const __half hi = __float2half_rn(x);
-      p.hi[x0 + c] = hi;
-      p.lo[x0 + c] = __float2half_rn(x - __half2float(hi));
+  const int64_t groups = p.m * (p.n / V);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPrepThreads + threadIdx.x; i < groups;
+       i += static_cast<int64_t>(gridDim.x) * kPrepThreads) {
+    const OrthAt at = orth_at<V>(p, b, i);
+    float u[V];
+    ld_elems<T, V>(static_cast<const T*>(p.grad) + at.grad, u);
+    if (p.momentum) {
+      float mom[V];
+      ld_elems<float, V>(p.momentum + at.mom, mom);
+#pragma unroll
+      for (int e = 0; e < V; ++e) u[e] = p.nesterov ? p.beta * mom[e] + p.rest * u[e] : mom[e];
+    }
+    alignas(16) __half hi[V], lo[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float x = u[e] * inv;
+      hi[e] = __float2half_rn(x);
+      lo[e] = __float2half_rn(x - __half2float(hi[e]));
+    }
+    if constexpr (V == 8) {
+      *reinterpret_cast<uint4*>(p.hi + at.x) = *reinterpret_cast<const uint4*>(hi);
+      *reinterpret_cast<uint4*>(p.lo + at.x) = *reinterpret_cast<const uint4*>(lo);
+    } else {
+      p.hi[at.x] = hi[0];
+      p.lo[at.x] = lo[0];
     }
   }
 }
 
 // ----------------------------------------------------------------------------------------
-// The products: a persistent 2-SM GEMM (M = 256 rows per CTA pair, BN columns, fp16 operands,
-// two TMEM accumulators so that one tile's epilogue overlaps the next tile's MMAs).  Warp 0
+// The products: a persistent 2-SM GEMM (M = 256 rows per CTA pair, fp16 operands).  Warp 0
 // loads, warp 1 issues the MMAs, eight warps run the epilogue, each warpgroup over half of the
 // columns.  Operands are K-major or MN-major as they lie in memory, so that no transpose of X
 // is ever stored.
-//   kGram    R, D of A = X X^T:  a symmetric product, only tiles on and below the diagonal
+//   kGram    R, D of A = X X^T:  a symmetric product, only blocks on and below the diagonal
 //            are computed and each is written to its mirrored place too
 //   kSquare  R_B, D_B of B = b A + c A^2, symmetric in the same way
 //   kUpdate  hi, lo of a X + B X; in the last step the result in bf16
+// The tensor memory holds two accumulator slots of BNI columns.  NSUB = 1: tiles take the slots
+// in turn, so that a tile's epilogue overlaps the next tile's MMAs.  NSUB = 2: a tile of 512
+// columns takes both; the operands then cross from L2 at 170 instead of 128 flops per byte, and
+// L2 is what bounds these products (about 9.3 TB/s measured over the 74 pairs: 256-column
+// tiles reach 1.2 PFLOP/s).  The next tile's MMAs for the first slot start while the epilogue
+// still drains the second.
 // ----------------------------------------------------------------------------------------
 enum OrthOp { kGram = 0, kSquare = 1, kUpdate = 2 };
 constexpr int kOrthWG = 2;
@@ -142,27 +208,37 @@ struct OrthCtl {
   int abort;
 };
 
-template <int BN>
+template <int BNI, int NSUB>
 struct OrthCfg {
-  static constexpr int kSliceN = BN / 2;  // columns whose operand rows each CTA holds
+  static constexpr int kTileN = BNI * NSUB;
+  static constexpr int kSliceN = BNI / 2;  // columns of a slot whose operand rows each CTA holds
   static constexpr uint32_t kABytes = kBM * kBK * 2;
-  static constexpr uint32_t kBBytes = kSliceN * kBK * 2;
-  static constexpr uint32_t kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = BN == 256 ? 6 : 8;
+  static constexpr uint32_t kSliceBytes = kSliceN * kBK * 2;
+  static constexpr uint32_t kStageBytes = kABytes + NSUB * kSliceBytes;
+  static constexpr int kStages = NSUB == 2 ? 4 : BNI == 256 ? 6 : 8;
   static constexpr size_t kSmem =
       1024 + kStages * static_cast<size_t>(kStageBytes) + sizeof(OrthCtl<kStages>);
-  static_assert(2 * BN <= 512, "two accumulators in TMEM");
   static_assert(kSmem <= 232448, "shared memory per CTA");
 };
 
-// Tile of unit u: matrix z, pair row tile i, column tile j.
-template <int BN, bool SYM>
-__device__ __forceinline__ void orth_unit(const OrthGemm& g, int u, int& z, int& i, int& j) {
+// Tile of unit u: matrix z, pair row tile i, column tile j, and how many of its slots' columns
+// are wanted (of a symmetric product, the blocks right of the diagonal are not).
+template <int BNI, int NSUB, bool SYM>
+__device__ __forceinline__ void orth_unit(const OrthGemm& g, int u, int& z, int& i, int& j,
+                                          int& nsub) {
   z = u / g.units_per;
   const int t = u - z * g.units_per;
-  if (SYM) {
-    // Row tile i has the column tiles 0 .. W (i + 1) - 1, W = 256 / BN; rows before i: W i (i + 1) / 2.
-    constexpr int W = 256 / BN;
+  nsub = NSUB;
+  if (SYM && NSUB == 2) {
+    // Row tile i has i / 2 + 1 column tiles; rows before it (i + 1)^2 / 4.
+    i = max(0, static_cast<int>(2.f * sqrtf(static_cast<float>(t))) - 1);
+    while ((i + 1) * (i + 1) / 4 > t) --i;
+    while ((i + 2) * (i + 2) / 4 <= t) ++i;
+    j = t - (i + 1) * (i + 1) / 4;
+    nsub = min(2, i + 1 - 2 * j);
+  } else if (SYM) {
+    // Row tile i has W (i + 1) column tiles, W = 256 / BNI; rows before it W i (i + 1) / 2.
+    constexpr int W = 256 / BNI;
     i = static_cast<int>((sqrtf(8.f / W * t + 1.f) - 1.f) * 0.5f);
     while (W * i * (i + 1) / 2 > t) --i;
     while (W * (i + 1) * (i + 2) / 2 <= t) ++i;
@@ -177,134 +253,177 @@ __device__ __forceinline__ void orth_unit(const OrthGemm& g, int u, int& z, int&
   }
 }
 
-// 32 consecutive fp16 numbers of a row; `n` of them exist (the rest read as 0).
-__device__ __forceinline__ void ld_half32(const __half* p, int n, float (&v)[32]) {
-  if (n >= 32) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint4 w = reinterpret_cast<const uint4*>(p)[q];
-      const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a[e]));
-        v[8 * q + 2 * e] = f.x;
-        v[8 * q + 2 * e + 1] = f.y;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 32; ++e) v[e] = e < n ? __half2float(p[e]) : 0.f;
-  }
-}
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_half2(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 __device__ __forceinline__ uint32_t pack_bf162(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void st_half32(__half* p, int n, const float (&v)[32]) {
+// 32 consecutive fp16 numbers of a row, packed; `n` of them exist (the rest read as 0).
+__device__ __forceinline__ void ld_half32(const __half* p, int n, uint32_t (&w)[16]) {
+  if (n >= 32) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint4 v = reinterpret_cast<const uint4*>(p)[q];
+      w[4 * q] = v.x;
+      w[4 * q + 1] = v.y;
+      w[4 * q + 2] = v.z;
+      w[4 * q + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      w[e] = (2 * e < n ? static_cast<uint32_t>(__half_as_ushort(p[2 * e])) : 0u) |
+             (2 * e + 1 < n ? static_cast<uint32_t>(__half_as_ushort(p[2 * e + 1])) << 16 : 0u);
+  }
+}
+__device__ __forceinline__ void st_half32(__half* p, int n, const uint32_t (&w)[16]) {
   if (n >= 32) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      reinterpret_cast<uint4*>(p)[q] =
-          make_uint4(pack_half2(v[8 * q], v[8 * q + 1]), pack_half2(v[8 * q + 2], v[8 * q + 3]),
-                     pack_half2(v[8 * q + 4], v[8 * q + 5]), pack_half2(v[8 * q + 6], v[8 * q + 7]));
+      reinterpret_cast<uint4*>(p)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
   } else {
 #pragma unroll
-    for (int e = 0; e < 32; ++e)
-      if (e < n) p[e] = __float2half_rn(v[e]);
+    for (int e = 0; e < 16; ++e) {
+      if (2 * e < n) p[2 * e] = __ushort_as_half(static_cast<unsigned short>(w[e]));
+      if (2 * e + 1 < n) p[2 * e + 1] = __ushort_as_half(static_cast<unsigned short>(w[e] >> 16));
+    }
   }
 }
 
-// One thread's 32 columns [col, col + 32) of row `row` (row < rows) of matrix z.
+// What the epilogue reads for one thread's 32 columns [col, col + 32) of row `row`: fetched a
+// chunk ahead, so that its latency passes behind the MMAs or the chunk before.
+template <int OP>
+struct OrthIn {
+  static constexpr int kSets = OP == kGram ? 0 : OP == kSquare ? 1 : 2;
+  uint32_t w[kSets == 0 ? 1 : kSets][16];  // kSquare: R; kUpdate: hi, lo
+  float dcol;                              // lane l: the diagonal's entry of column col + l
+  __device__ __forceinline__ void fetch(const OrthGemm& g, int z, int64_t row, int64_t col,
+                                        int lane) {
+    if (OP == kGram || col >= g.cols) return;
+    if (OP == kSquare || g.tall)
+      dcol = col + lane < g.cols ? g.diag_in[static_cast<int64_t>(z) * g.diag_n + col + lane] : 0.f;
+    if (row >= g.rows) return;
+    const int n = static_cast<int>(min(static_cast<int64_t>(32), g.cols - col));
+    const int64_t at = (static_cast<int64_t>(z) * g.rows + row) * g.ld + col;
+    if (OP == kSquare) {
+      ld_half32(g.a_in + at, n, w[0]);
+    } else {
+      ld_half32(g.hi_in + at, n, w[0]);
+      ld_half32(g.lo + at, n, w[kSets - 1]);
+    }
+  }
+};
+
+// One thread's 32 columns [col, col + 32) of row `row` of matrix z (the whole warp calls; rows
+// and columns outside the matrix are left out of every store).
 template <int OP, bool LAST>
 __device__ __forceinline__ void orth_epilogue(const OrthGemm& g, int z, int64_t row, int64_t col,
-                                              bool mirror, float (&v)[32]) {
+                                              bool mirror, float drow, const OrthIn<OP>& in,
+                                              float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
   const int n = static_cast<int>(min(static_cast<int64_t>(32), g.cols - col));
+  const int64_t at = (static_cast<int64_t>(z) * g.rows + row) * g.ld + col;
+  const bool live = row < g.rows;
+  uint32_t out[16];
   if (OP == kGram || OP == kSquare) {
-    const int64_t at = (static_cast<int64_t>(z) * g.rows + row) * g.ld + col;
+    const int e = static_cast<int>(row - col);  // the diagonal's column of the chunk, if in it
+    float d = 0.f;
     if (OP == kGram) {
-      const int e = static_cast<int>(row - col);
 #pragma unroll
       for (int c = 0; c < 32; ++c) {
-        if (c == e) g.diag_out[static_cast<int64_t>(z) * g.rows + row] = v[c] * (1.f / (kScaleX * kScaleX));
+        if (c == e) d = v[c] * (1.f / (kScaleX * kScaleX));
         v[c] = c == e ? 0.f : v[c] * (kScaleA / (kScaleX * kScaleX));
       }
     } else {
-      float r[32];
-      ld_half32(g.a_in + at, n, r);
-      const float* dg = g.diag_in + static_cast<int64_t>(z) * g.rows;
-      const float di = dg[row];
-      const int e = static_cast<int>(row - col);
 #pragma unroll
       for (int c = 0; c < 32; ++c) {
-        const float dj = c < n ? dg[col + c] : 0.f;
+        const float dj = __shfl_sync(0xffffffffu, in.dcol, c);
+        const float2 r2 = unpack_half2(in.w[0][c / 2]);
         const float rr = v[c] * (1.f / (kScaleA * kScaleA));
-        if (c == e) {
-          g.diag_out[static_cast<int64_t>(z) * g.rows + row] = fmaf(g.c, fmaf(di, di, rr), g.b * di);
-          v[c] = 0.f;
-        } else {
-          const float a = r[c] * (1.f / kScaleA);
-          v[c] = kScaleB * fmaf(g.c, fmaf(di + dj, a, rr), g.b * a);
-        }
+        const float a = (c & 1 ? r2.y : r2.x) * (1.f / kScaleA);
+        if (c == e) d = fmaf(g.c, fmaf(drow, drow, rr), g.b * drow);
+        v[c] = c == e ? 0.f : kScaleB * fmaf(g.c, fmaf(drow + dj, a, rr), g.b * a);
       }
     }
-    st_half32(g.a_out + at, n, v);
-    if (mirror) {
-      // Lanes hold consecutive rows: each column goes out as one run of 32 fp16 numbers.
-      __half* dst = g.a_out + (static_cast<int64_t>(z) * g.rows + col) * g.ld + row;
 #pragma unroll
-      for (int c = 0; c < 32; ++c)
-        if (c < n) dst[static_cast<int64_t>(c) * g.ld] = __float2half_rn(v[c]);
+    for (int c = 0; c < 16; ++c) out[c] = pack_half2(v[2 * c], v[2 * c + 1]);
+    if (live) {
+      if (e >= 0 && e < 32) g.diag_out[static_cast<int64_t>(z) * g.diag_n + row] = d;
+      st_half32(g.a_out + at, n, out);
+    }
+    if (mirror) {
+      // Column c of the block goes out as row c: lanes hold consecutive rows, and two lanes
+      // trade halves so that each store carries two rows (a row past the last lands in the
+      // padding, which is not read).
+      __half* dst = g.a_out + (static_cast<int64_t>(z) * g.rows + col) * g.ld + (row & ~1);
+      const bool odd = lane & 1;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const uint32_t q = __shfl_xor_sync(0xffffffffu, out[c], 1);
+        const uint32_t w = odd ? __byte_perm(q, out[c], 0x7632) : __byte_perm(out[c], q, 0x5410);
+        const int cc = 2 * c + odd;
+        if ((row & ~1) < g.rows && cc < n)
+          *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(cc) * g.ld) = w;
+      }
     }
   } else {
-    const int64_t at = (static_cast<int64_t>(z) * g.rows + row) * g.ld + col;
-    float hi[32], lo[32];
-    ld_half32(g.hi_in + at, n, hi);
-    ld_half32(g.lo + at, n, lo);
-    const float* dg = g.diag_in + static_cast<int64_t>(z) * g.diag_n;
-    const float drow = g.tall ? 0.f : dg[row];
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
-      const float db = g.tall ? (c < n ? dg[col + c] : 0.f) : drow;
-      v[c] = fmaf(v[c], 1.f / kScaleB, fmaf(db, hi[c], g.a * (hi[c] + lo[c])));
+    for (int c = 0; c < 32; c += 2) {
+      const float2 hi = unpack_half2(in.w[0][c / 2]);
+      const float2 lo = unpack_half2(in.w[OrthIn<OP>::kSets - 1][c / 2]);
+      float d0 = drow, d1 = drow;
+      if (g.tall) {
+        d0 = __shfl_sync(0xffffffffu, in.dcol, c);
+        d1 = __shfl_sync(0xffffffffu, in.dcol, c + 1);
+      }
+      v[c] = fmaf(v[c], 1.f / kScaleB, fmaf(d0, hi.x, g.a * (hi.x + lo.x)));
+      v[c + 1] = fmaf(v[c + 1], 1.f / kScaleB, fmaf(d1, hi.y, g.a * (hi.y + lo.y)));
     }
+    if (!live) return;
     if (LAST) {
-      __nv_bfloat16* out = g.out + (static_cast<int64_t>(z) * g.rows + row) * g.cols + col;
+      __nv_bfloat16* dst = g.out + (static_cast<int64_t>(z) * g.rows + row) * g.cols + col;
 #pragma unroll
       for (int c = 0; c < 32; ++c) v[c] *= 1.f / kScaleX;
       if (g.out_vec && n >= 32) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          reinterpret_cast<uint4*>(out)[q] = make_uint4(
+          reinterpret_cast<uint4*>(dst)[q] = make_uint4(
               pack_bf162(v[8 * q], v[8 * q + 1]), pack_bf162(v[8 * q + 2], v[8 * q + 3]),
               pack_bf162(v[8 * q + 4], v[8 * q + 5]), pack_bf162(v[8 * q + 6], v[8 * q + 7]));
       } else {
 #pragma unroll
         for (int c = 0; c < 32; ++c)
-          if (c < n) out[c] = __float2bfloat16_rn(v[c]);
+          if (c < n) dst[c] = __float2bfloat16_rn(v[c]);
       }
     } else {
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        hi[c] = __half2float(__float2half_rn(v[c]));
-        lo[c] = v[c] - hi[c];
+      for (int c = 0; c < 16; ++c) {
+        out[c] = pack_half2(v[2 * c], v[2 * c + 1]);
+        const float2 hi = unpack_half2(out[c]);
+        v[2 * c] -= hi.x;
+        v[2 * c + 1] -= hi.y;
       }
-      st_half32(g.hi_out + at, n, hi);
-      st_half32(g.lo + at, n, lo);
+      st_half32(g.hi_out + at, n, out);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) out[c] = pack_half2(v[2 * c], v[2 * c + 1]);
+      st_half32(g.lo + at, n, out);
     }
   }
 }
 
-template <int BN, bool A_MN, bool B_MN, int OP, bool LAST>
+template <int BNI, int NSUB, bool A_MN, bool B_MN, int OP, bool LAST>
 __global__ void __launch_bounds__(kOrthThreads, 1)
     orth_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const OrthGemm g, const DevCtl ctl) {
-  using C = OrthCfg<BN>;
+  using C = OrthCfg<BNI, NSUB>;
   constexpr int STAGES = C::kStages;
-  constexpr uint32_t kIdesc = idesc_f16_f32(2 * kBM, BN, A_MN, B_MN);
+  constexpr uint32_t kIdesc = idesc_f16_f32(2 * kBM, BNI, A_MN, B_MN);
   constexpr bool kSym = OP != kUpdate;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -317,6 +436,9 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   const int pair = blockIdx.x >> 1;
   const int npairs = gridDim.x >> 1;
 
+  // The next launch of the chain may begin its set-up; this one's is done before it waits for
+  // the launch before it, whose results everything below reads.
+  launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&pc->full[s], 1);
@@ -343,16 +465,16 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   tc_fence_after();
   const uint32_t tmem = pc->tmem_base;
   volatile int* abort = &pc->abort;
+  wait_prior_launch();
 
   if (warp == 0) {
     // TMA producer (both CTAs); both CTAs' copies complete on the leader's "full" barrier.
     uint32_t it = 0;
     bool ok = true;
     for (int u = pair; ok && u < g.num_units; u += npairs) {
-      int z, i, j;
-      orth_unit<BN, kSym>(g, u, z, i, j);
+      int z, i, j, nsub;
+      orth_unit<BNI, NSUB, kSym>(g, u, z, i, j, nsub);
       const int mrow = i * 2 * kBM + static_cast<int>(rank) * kBM;
-      const int ncol = j * BN + static_cast<int>(rank) * C::kSliceN;
       for (int kb = 0; kb < g.k_blocks; ++kb, ++it) {
         const int s = it % STAGES;
         if (!wait_warp(&pc->empty[s], ((it / STAGES) & 1u) ^ 1u, abort, ctl)) {
@@ -361,8 +483,8 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         }
         if (lane == 0) {
           uint8_t* st = smem + s * C::kStageBytes;
-          uint8_t* bst = st + C::kABytes;
-          if (leader) mbar_arrive_expect_tx(&pc->full[s], 2 * C::kStageBytes);
+          if (leader)
+            mbar_arrive_expect_tx(&pc->full[s], 2 * (C::kABytes + nsub * C::kSliceBytes));
           const int k0 = kb * kBK;
           if (A_MN) {
             tma_load_3d_pair(st, &tmA, &pc->full[s], mrow, k0, z);
@@ -370,12 +492,18 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
           } else {
             tma_load_3d_pair(st, &tmA, &pc->full[s], k0, mrow, z);
           }
-          if (B_MN) {
 #pragma unroll
-            for (int q = 0; q < C::kSliceN / 64; ++q)
-              tma_load_3d_pair(bst + q * 8192, &tmB, &pc->full[s], ncol + q * 64, k0, z);
-          } else {
-            tma_load_3d_pair(bst, &tmB, &pc->full[s], k0, ncol, z);
+          for (int h = 0; h < NSUB; ++h) {
+            if (h >= nsub) break;
+            uint8_t* bst = st + C::kABytes + h * C::kSliceBytes;
+            const int ncol = j * C::kTileN + h * BNI + static_cast<int>(rank) * C::kSliceN;
+            if (B_MN) {
+#pragma unroll
+              for (int q = 0; q < C::kSliceN / 64; ++q)
+                tma_load_3d_pair(bst + q * 8192, &tmB, &pc->full[s], ncol + q * 64, k0, z);
+            } else {
+              tma_load_3d_pair(bst, &tmB, &pc->full[s], k0, ncol, z);
+            }
           }
         }
         __syncwarp();
@@ -401,14 +529,56 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   } else if (warp == 1) {
     // MMA issuer (leader only).
     if (leader) {
-      uint32_t it = 0, t = 0;
+      uint32_t it = 0, t = 0, used0 = 0, used1 = 0;
       bool ok = true;
+      // The MMAs of stage `st` into slot b (operand slice h); first = the tile's first K block.
+      auto issue = [&](int st, int h, int b, bool first) {
+        const uint32_t a_addr = smem_u32(smem + st * C::kStageBytes);
+        const uint32_t b_addr = a_addr + C::kABytes + h * C::kSliceBytes;
+#pragma unroll
+        for (int kk = 0; kk < kBK / 16; ++kk) {
+          const uint64_t ad = A_MN ? smem_desc_sw128(a_addr + kk * 2048, 8192, 1024)
+                                   : smem_desc_sw128(a_addr + kk * 32, 16, 1024);
+          const uint64_t bd = B_MN ? smem_desc_sw128(b_addr + kk * 2048, 8192, 1024)
+                                   : smem_desc_sw128(b_addr + kk * 32, 16, 1024);
+          umma_bf16_pair(tmem + b * BNI, ad, bd, kIdesc, (!first || kk != 0) ? 1u : 0u);
+        }
+      };
       for (int u = pair; ok && u < g.num_units; u += npairs, ++t) {
-        const int b = static_cast<int>(t & 1u);
-        if (!wait_warp(&pc->tempty[b], ((t >> 1) & 1u) ^ 1u, abort, ctl)) break;
+        int z, i, j, nsub;
+        orth_unit<BNI, NSUB, kSym>(g, u, z, i, j, nsub);
+        const int b0 = NSUB == 2 ? 0 : static_cast<int>(t & 1u);
+        uint32_t& used = b0 ? used1 : used0;
+        if (!wait_warp(&pc->tempty[b0], (used & 1u) ^ 1u, abort, ctl)) break;
+        ++used;
         tc_fence_after();
-        const uint32_t dcol = tmem + b * BN;
-        for (int kb = 0; kb < g.k_blocks; ++kb, ++it) {
+        int kb = 0;
+        if (NSUB == 2 && nsub == 2) {
+          // The first slot over the stages that are there already, then, once the second slot
+          // is free, its MMAs for them, with the stages' releases.
+          const int pre = min(STAGES, g.k_blocks);
+          for (; kb < pre; ++kb) {
+            const uint32_t q = it + kb;
+            if (!wait_warp(&pc->full[q % STAGES], (q / STAGES) & 1u, abort, ctl)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (lane == 0) issue(q % STAGES, 0, 0, kb == 0);
+            __syncwarp();
+          }
+          if (!ok || !wait_warp(&pc->tempty[1], (used1 & 1u) ^ 1u, abort, ctl)) break;
+          ++used1;
+          tc_fence_after();
+          for (int q = 0; q < pre; ++q, ++it) {
+            if (lane == 0) {
+              issue(it % STAGES, 1, 1, q == 0);
+              umma_commit_pair_mc(&pc->empty[it % STAGES], 0x3);
+            }
+            __syncwarp();
+          }
+        }
+        for (; kb < g.k_blocks; ++kb, ++it) {
           const int s = it % STAGES;
           if (!wait_warp(&pc->full[s], (it / STAGES) & 1u, abort, ctl)) {
             ok = false;
@@ -416,22 +586,17 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
           }
           tc_fence_after();
           if (lane == 0) {
-            const uint32_t a_addr = smem_u32(smem + s * C::kStageBytes);
-            const uint32_t b_addr = a_addr + C::kABytes;
-#pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk) {
-              const uint64_t ad = A_MN ? smem_desc_sw128(a_addr + kk * 2048, 8192, 1024)
-                                       : smem_desc_sw128(a_addr + kk * 32, 16, 1024);
-              const uint64_t bd = B_MN ? smem_desc_sw128(b_addr + kk * 2048, 8192, 1024)
-                                       : smem_desc_sw128(b_addr + kk * 32, 16, 1024);
-              umma_bf16_pair(dcol, ad, bd, kIdesc, (kb | kk) != 0 ? 1u : 0u);
-            }
+            issue(s, 0, b0, kb == 0);
+            if (NSUB == 2 && nsub == 2) issue(s, 1, 1, false);
             umma_commit_pair_mc(&pc->empty[s], 0x3);
           }
           __syncwarp();
         }
         if (!ok) break;
-        if (lane == 0) umma_commit_pair_mc(&pc->tfull[b], 0x3);
+        if (lane == 0) {
+          umma_commit_pair_mc(&pc->tfull[b0], 0x3);
+          if (NSUB == 2 && nsub == 2) umma_commit_pair_mc(&pc->tfull[1], 0x3);
+        }
         __syncwarp();
       }
       // Every MMA must be complete (in both CTAs' TMEM) before TMEM is released.
@@ -444,31 +609,49 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     const int q = warp & 3;  // a warp may only touch TMEM lanes [32 * (warp % 4), +32)
     const int wg = (warp - 2) >> 2;
     const uint32_t lane_bits = static_cast<uint32_t>(q * 32) << 16;
-    constexpr int kShare = BN / kOrthWG;
+    constexpr int kShare = BNI / kOrthWG, kChunks = kShare / 32;
     const uint32_t tempty0 = mapa_shared(smem_u32(&pc->tempty[0]), 0);
     const uint32_t tempty1 = mapa_shared(smem_u32(&pc->tempty[1]), 0);
-    uint32_t t = 0;
-    for (int u = pair; u < g.num_units; u += npairs, ++t) {
-      int z, i, j;
-      orth_unit<BN, kSym>(g, u, z, i, j);
-      const int b = static_cast<int>(t & 1u);
-      if (!wait_warp(&pc->tfull[b], (t >> 1) & 1u, abort, ctl)) break;
-      tc_fence_after();
+    uint32_t t = 0, used0 = 0, used1 = 0;
+    bool ok = true;
+    for (int u = pair; ok && u < g.num_units; u += npairs, ++t) {
+      int z, i, j, nsub;
+      orth_unit<BNI, NSUB, kSym>(g, u, z, i, j, nsub);
       const int64_t row = static_cast<int64_t>(i) * 2 * kBM + rank * kBM + q * 32 + lane;
-      const int64_t col0 = static_cast<int64_t>(j) * BN;
-      const bool mirror = kSym && col0 + BN <= static_cast<int64_t>(i) * 2 * kBM;
-#pragma unroll 1
-      for (int c = wg * kShare; c < (wg + 1) * kShare; c += 32) {
-        float v[32];
-        tmem_ld32(tmem + lane_bits + b * BN + c, v);
-        tmem_ld_wait();
-        if (row < g.rows && col0 + c < g.cols)
-          orth_epilogue<OP, LAST>(g, z, row, col0 + c, mirror, v);
+      float drow = 0.f;
+      if (OP == kSquare || (OP == kUpdate && !g.tall))
+        if (row < g.rows) drow = g.diag_in[static_cast<int64_t>(z) * g.diag_n + row];
+      for (int h = 0; h < nsub; ++h) {
+        const int b = NSUB == 2 ? h : static_cast<int>(t & 1u);
+        uint32_t& used = b ? used1 : used0;
+        const int64_t col0 = static_cast<int64_t>(j) * C::kTileN + h * BNI + wg * kShare;
+        const bool mirror = kSym && col0 - wg * kShare + BNI <= static_cast<int64_t>(i) * 2 * kBM;
+        OrthIn<OP> in[2];
+        in[0].fetch(g, z, row, col0, lane);
+        if (!wait_warp(&pc->tfull[b], used & 1u, abort, ctl)) {
+          ok = false;
+          break;
+        }
+        ++used;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          if (c + 1 < kChunks) in[(c + 1) & 1].fetch(g, z, row, col0 + (c + 1) * 32, lane);
+          float v[32];
+          tmem_ld32(tmem + lane_bits + b * BNI + wg * kShare + c * 32, v);
+          tmem_ld_wait();
+          if (c == kChunks - 1) {
+            // The slot is drained once this load has completed.
+            tc_fence_before();
+            __syncwarp();
+            // Test hook (fault == 1): withhold the release of the first accumulator.
+            if (lane == 0 && !(ctl.fault == 1 && t == 0))
+              mbar_arrive_cluster(b ? tempty1 : tempty0);
+          }
+          if (col0 + c * 32 < g.cols)
+            orth_epilogue<OP, LAST>(g, z, row, col0 + c * 32, mirror, drow, in[c & 1], v);
+        }
       }
-      tc_fence_before();
-      __syncwarp();
-      // Test hook (fault == 1): withhold the release of the first accumulator.
-      if (lane == 0 && !(ctl.fault == 1 && t == 0)) mbar_arrive_cluster(b ? tempty1 : tempty0);
     }
   }
 
@@ -479,21 +662,24 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
-template <int BN, bool A_MN, bool B_MN, int OP, bool LAST>
+template <int BNI, int NSUB, bool A_MN, bool B_MN, int OP, bool LAST>
 cudaError_t launch_orth(const CUtensorMap& a, const CUtensorMap& b, const OrthGemm& g,
                         const DevCtl& c, cudaStream_t s) {
-  using C = OrthCfg<BN>;
-  auto kern = orth_gemm<BN, A_MN, B_MN, OP, LAST>;
+  using C = OrthCfg<BNI, NSUB>;
+  auto kern = orth_gemm<BNI, NSUB, A_MN, B_MN, OP, LAST>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  // Set-up overlaps the end of the launch before it (the kernel waits for its results).
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.blockDim = dim3(kOrthThreads, 1, 1);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
@@ -510,36 +696,47 @@ cudaError_t launch_orth(const CUtensorMap& a, const CUtensorMap& b, const OrthGe
     if ((e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg)) != cudaSuccess) return e;
     max_clusters[dev] = n > 0 ? n : 1;
   }
+  cfg.numAttrs = 2;
   cfg.gridDim = dim3(2 * std::max(1, std::min(g.num_units, max_clusters[dev])), 1, 1);
   return cudaLaunchKernelEx(&cfg, kern, a, b, g, c);
 }
 
-template <int BN>
+template <int BNI, int NSUB>
 cudaError_t launch_op(int op, bool tall, bool last, const CUtensorMap& a, const CUtensorMap& b,
                       const OrthGemm& g, const DevCtl& c, cudaStream_t s) {
   if (op == kGram)
-    return tall ? launch_orth<BN, true, true, kGram, false>(a, b, g, c, s)
-                : launch_orth<BN, false, false, kGram, false>(a, b, g, c, s);
-  if (op == kSquare) return launch_orth<BN, false, false, kSquare, false>(a, b, g, c, s);
+    return tall ? launch_orth<BNI, NSUB, true, true, kGram, false>(a, b, g, c, s)
+                : launch_orth<BNI, NSUB, false, false, kGram, false>(a, b, g, c, s);
+  if (op == kSquare) return launch_orth<BNI, NSUB, false, false, kSquare, false>(a, b, g, c, s);
   if (tall)
-    return last ? launch_orth<BN, false, false, kUpdate, true>(a, b, g, c, s)
-                : launch_orth<BN, false, false, kUpdate, false>(a, b, g, c, s);
-  return last ? launch_orth<BN, false, true, kUpdate, true>(a, b, g, c, s)
-              : launch_orth<BN, false, true, kUpdate, false>(a, b, g, c, s);
+    return last ? launch_orth<BNI, NSUB, false, false, kUpdate, true>(a, b, g, c, s)
+                : launch_orth<BNI, NSUB, false, false, kUpdate, false>(a, b, g, c, s);
+  return last ? launch_orth<BNI, NSUB, false, true, kUpdate, true>(a, b, g, c, s)
+              : launch_orth<BNI, NSUB, false, true, kUpdate, false>(a, b, g, c, s);
 }
 
 }  // namespace
 
 cudaError_t launch_orth_prep(int dtype, const OrthPrep& p, int64_t batch, cudaStream_t s) {
-  const int64_t blocks = std::min<int64_t>(p.m, kOrthSums);
-  const dim3 g1(static_cast<unsigned>(blocks), static_cast<unsigned>(batch));
-  const dim3 g2(static_cast<unsigned>(std::min<int64_t>(p.m, 4096)), static_cast<unsigned>(batch));
+  auto aligned = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
+  const bool vec = p.n % 8 == 0 && p.ldg % 8 == 0 && p.grad_batch % 8 == 0 && aligned(p.grad) &&
+                   aligned(p.momentum);
+  const int64_t groups = p.m * (vec ? p.n / 8 : p.n);
+  const int64_t want = (groups + kPrepThreads - 1) / kPrepThreads;
+  const dim3 g1(static_cast<unsigned>(std::min<int64_t>(want, kOrthSums)), static_cast<unsigned>(batch));
+  const dim3 g2(static_cast<unsigned>(std::min<int64_t>(want, 4096)), static_cast<unsigned>(batch));
   auto run = [&](auto t) {
     using T = decltype(t);
-    orth_moment<T><<<g1, kPrepThreads, 0, s>>>(p);
+    if (vec)
+      orth_moment<T, 8><<<g1, kPrepThreads, 0, s>>>(p);
+    else
+      orth_moment<T, 1><<<g1, kPrepThreads, 0, s>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    orth_scale<T><<<g2, kPrepThreads, 0, s>>>(p, static_cast<int>(blocks));
+    if (vec)
+      orth_scale<T, 8><<<g2, kPrepThreads, 0, s>>>(p, static_cast<int>(g1.x));
+    else
+      orth_scale<T, 1><<<g2, kPrepThreads, 0, s>>>(p, static_cast<int>(g1.x));
     return cudaGetLastError();
   };
   if (dtype == 0) return run(__nv_bfloat16{});
@@ -550,8 +747,9 @@ cudaError_t launch_orth_prep(int dtype, const OrthPrep& p, int64_t batch, cudaSt
 cudaError_t launch_orth_gemm(int op, int bn, bool tall, bool last, const CUtensorMap& a,
                              const CUtensorMap& b, const OrthGemm& g, const DevCtl& c,
                              cudaStream_t s) {
-  return bn == 128 ? launch_op<128>(op, tall, last, a, b, g, c, s)
-                   : launch_op<256>(op, tall, last, a, b, g, c, s);
+  if (bn == 512) return launch_op<256, 2>(op, tall, last, a, b, g, c, s);
+  return bn == 128 ? launch_op<128, 1>(op, tall, last, a, b, g, c, s)
+                   : launch_op<256, 1>(op, tall, last, a, b, g, c, s);
 }
 
 }  // namespace slm
