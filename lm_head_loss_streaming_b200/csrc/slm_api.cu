@@ -509,9 +509,11 @@ bool orth_coefficients_ok(const float* co, int steps) {
 }
 
 // 3-D fp16 tensor map over a stack of row-major [outer, inner] matrices with `ld` elements per
-// row, outer * ld per matrix; box {box_inner, box_outer, 1}, 128-byte swizzle.
+// row, outer * ld per matrix; box {box_inner, box_outer, 1}, 128-byte swizzle (64-byte for the
+// store maps' boxes of 32 elements per row).
 bool make_map_stack(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t ld,
-                    int64_t stack, int box_inner, int box_outer) {
+                    int64_t stack, int box_inner, int box_outer,
+                    CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_FLOAT16) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer),
@@ -520,8 +522,9 @@ bool make_map_stack(CUtensorMap* m, const void* base, int64_t inner, int64_t out
                            static_cast<cuuint64_t>(outer) * static_cast<cuuint64_t>(ld) * 2};
   cuuint32_t box[3] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_outer), 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return fn(m, type, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            box_inner == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1293,6 +1296,17 @@ int slm_orthogonalize(int dtype, const void* grad, int64_t ld, int64_t batch_str
   for (int i = 0; i < 2; ++i)
     if (!make_map_stack(&xu[i], hi[i], n, m, L.ldx, batch, 64, tall ? kBM : 64)) return SLM_ERR_CUDA;
 
+  // Store maps: hi (two buffers), lo, R, R_B and the result.
+  CUtensorMap s_hi[2], s_lo, s_mat[2], s_out{};
+  for (int i = 0; i < 2; ++i)
+    if (!make_map_stack(&s_hi[i], hi[i], n, m, L.ldx, batch, 32, 32) ||
+        !make_map_stack(&s_mat[i], mat[i], k, k, L.ldk, batch, 32, 32))
+      return SLM_ERR_CUDA;
+  if (!make_map_stack(&s_lo, lo, n, m, L.ldx, batch, 32, 32) ||
+      (update.out_vec &&
+       !make_map_stack(&s_out, out, n, m, n, batch, 32, 32, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16)))
+    return SLM_ERR_CUDA;
+
   const DevCtl ctl = make_ctl(status);
   const OrthPrep prep{grad, m, n, ld, batch_stride, L.ldx, momentum, static_cast<float>(beta),
                       static_cast<float>(1.0 - beta), eps, nesterov,
@@ -1301,15 +1315,19 @@ int slm_orthogonalize(int dtype, const void* grad, int64_t ld, int64_t batch_str
   for (int i = 0; i < steps; ++i) {
     const int cur = i & 1;
     const bool last = i == steps - 1;
-    SLM_LAUNCH(kTrOrth, launch_orth_gemm(0, bn_gram, tall, false, xa[cur], xb[cur], gram, ctl, s));
+    SLM_LAUNCH(kTrOrth, launch_orth_gemm(0, bn_gram, tall, false, xa[cur], xb[cur],
+                                         OrthMaps{&s_mat[0], &s_mat[0]}, gram, ctl, s));
     square.b = coefficients[3 * i + 1];
     square.c = coefficients[3 * i + 2];
-    SLM_LAUNCH(kTrOrth, launch_orth_gemm(1, bn_square, tall, false, ra, rb, square, ctl, s));
+    SLM_LAUNCH(kTrOrth, launch_orth_gemm(1, bn_square, tall, false, ra, rb,
+                                         OrthMaps{&s_mat[1], &s_mat[1]}, square, ctl, s));
     update.a = coefficients[3 * i];
     update.hi_in = hi[cur];
     update.hi_out = hi[cur ^ 1];
     SLM_LAUNCH(kTrOrth, launch_orth_gemm(2, bn_update, tall, last, tall ? xu[cur] : ba,
-                                         tall ? bb : xu[cur], update, ctl, s));
+                                         tall ? bb : xu[cur],
+                                         OrthMaps{last ? &s_out : &s_hi[cur ^ 1], &s_lo}, update,
+                                         ctl, s));
   }
   return SLM_OK;
 }

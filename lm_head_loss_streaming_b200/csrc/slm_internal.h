@@ -331,9 +331,14 @@ struct OrthGemm {
 };
 // op: 0 R and D of X X^T (X^T X when tall), 1 R_B and D_B, 2 the update of X (`last`: to out).
 cudaError_t launch_orth_prep(int dtype, const OrthPrep& p, int64_t batch, cudaStream_t s);
+// out0: the store map of a_out, hi_out or out; out1: that of lo (kUpdate).  Boxes of 32 x 32,
+// 64-byte swizzle.
+struct OrthMaps {
+  const CUtensorMap *out0, *out1;
+};
 cudaError_t launch_orth_gemm(int op, int bn, bool tall, bool last, const CUtensorMap& a,
-                             const CUtensorMap& b, const OrthGemm& g, const DevCtl& c,
-                             cudaStream_t s);
+                             const CUtensorMap& b, const OrthMaps& st, const OrthGemm& g,
+                             const DevCtl& c, cudaStream_t s);
 
 constexpr int kCombineThreads = 256;
 

@@ -200,6 +200,12 @@ __global__ void __launch_bounds__(kPrepThreads) orth_scale(const OrthPrep p, int
 enum OrthOp { kGram = 0, kSquare = 1, kUpdate = 2 };
 constexpr int kOrthWG = 2;
 constexpr int kOrthThreads = 64 + 128 * kOrthWG;
+// Staging of an epilogue warp: two blocks of 32 rows x 32 fp16 columns, 64 bytes per row, in
+// the 64-byte swizzle of the store maps (16-byte piece k of row r at k ^ (r / 2 % 4)).
+constexpr int kOrthStage = 4096;
+__device__ __forceinline__ int stage_piece(int row, int k) {
+  return row * 4 + (k ^ ((row >> 1) & 3));
+}
 
 template <int STAGES>
 struct OrthCtl {
@@ -216,8 +222,9 @@ struct OrthCfg {
   static constexpr uint32_t kSliceBytes = kSliceN * kBK * 2;
   static constexpr uint32_t kStageBytes = kABytes + NSUB * kSliceBytes;
   static constexpr int kStages = NSUB == 2 ? 4 : BNI == 256 ? 6 : 8;
+  static constexpr size_t kRing = kStages * static_cast<size_t>(kStageBytes);
   static constexpr size_t kSmem =
-      1024 + kStages * static_cast<size_t>(kStageBytes) + sizeof(OrthCtl<kStages>);
+      1024 + kRing + 4 * kOrthWG * kOrthStage + sizeof(OrthCtl<kStages>);
   static_assert(kSmem <= 232448, "shared memory per CTA");
 };
 
@@ -264,75 +271,71 @@ __device__ __forceinline__ uint32_t pack_bf162(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// 32 consecutive fp16 numbers of a row, packed; `n` of them exist (the rest read as 0).
-__device__ __forceinline__ void ld_half32(const __half* p, int n, uint32_t (&w)[16]) {
-  if (n >= 32) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint4 v = reinterpret_cast<const uint4*>(p)[q];
-      w[4 * q] = v.x;
-      w[4 * q + 1] = v.y;
-      w[4 * q + 2] = v.z;
-      w[4 * q + 3] = v.w;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-      w[e] = (2 * e < n ? static_cast<uint32_t>(__half_as_ushort(p[2 * e])) : 0u) |
-             (2 * e + 1 < n ? static_cast<uint32_t>(__half_as_ushort(p[2 * e + 1])) << 16 : 0u);
-  }
-}
-__device__ __forceinline__ void st_half32(__half* p, int n, const uint32_t (&w)[16]) {
-  if (n >= 32) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      reinterpret_cast<uint4*>(p)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      if (2 * e < n) p[2 * e] = __ushort_as_half(static_cast<unsigned short>(w[e]));
-      if (2 * e + 1 < n) p[2 * e + 1] = __ushort_as_half(static_cast<unsigned short>(w[e] >> 16));
-    }
-  }
-}
 
-// What the epilogue reads for one thread's 32 columns [col, col + 32) of row `row`: fetched a
-// chunk ahead, so that its latency passes behind the MMAs or the chunk before.
+// What the epilogue reads for a warp's block of 32 rows x 32 columns: fetched a block ahead, so
+// that its latency passes behind the MMAs or the block before.  Four lanes share a row, so that
+// every load covers whole 64-byte pieces of rows.
 template <int OP>
 struct OrthIn {
   static constexpr int kSets = OP == kGram ? 0 : OP == kSquare ? 1 : 2;
-  uint32_t w[kSets == 0 ? 1 : kSets][16];  // kSquare: R; kUpdate: hi, lo
-  float dcol;                              // lane l: the diagonal's entry of column col + l
-  __device__ __forceinline__ void fetch(const OrthGemm& g, int z, int64_t row, int64_t col,
+  uint4 w[kSets == 0 ? 1 : kSets][4];  // kSquare: R; kUpdate: hi, lo
+  float dcol;                          // lane l: the diagonal's entry of column col + l
+  __device__ __forceinline__ void fetch(const OrthGemm& g, int z, int64_t row0, int64_t col,
                                         int lane) {
     if (OP == kGram || col >= g.cols) return;
     if (OP == kSquare || g.tall)
       dcol = col + lane < g.cols ? g.diag_in[static_cast<int64_t>(z) * g.diag_n + col + lane] : 0.f;
-    if (row >= g.rows) return;
-    const int n = static_cast<int>(min(static_cast<int64_t>(32), g.cols - col));
-    const int64_t at = (static_cast<int64_t>(z) * g.rows + row) * g.ld + col;
-    if (OP == kSquare) {
-      ld_half32(g.a_in + at, n, w[0]);
-    } else {
-      ld_half32(g.hi_in + at, n, w[0]);
-      ld_half32(g.lo + at, n, w[kSets - 1]);
+    const int64_t c = col + (lane & 3) * 8;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t row = row0 + q * 8 + (lane >> 2);
+      const int64_t at = (static_cast<int64_t>(z) * g.rows + row) * g.ld + c;
+      const bool in = row < g.rows && c < g.cols;  // rows are padded to whole pieces
+      const uint4 none = make_uint4(0, 0, 0, 0);
+      w[0][q] = !in ? none
+                    : *reinterpret_cast<const uint4*>((OP == kSquare ? g.a_in : g.hi_in) + at);
+      if (OP == kUpdate) w[kSets - 1][q] = !in ? none : *reinterpret_cast<const uint4*>(g.lo + at);
     }
+  }
+  // Into the warp's staging blocks.
+  __device__ __forceinline__ void put(uint4* stage, int lane) const {
+#pragma unroll
+    for (int e = 0; e < kSets; ++e)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        stage[e * 128 + stage_piece(q * 8 + (lane >> 2), lane & 3)] = w[e][q];
   }
 };
 
-// One thread's 32 columns [col, col + 32) of row `row` of matrix z (the whole warp calls; rows
-// and columns outside the matrix are left out of every store).
+// One warp's block: this lane's row `row`, columns [col, col + 32) of matrix z.  The block's
+// inputs lie in the staging blocks; its outputs take their place, each lane its own row, and go
+// out by bulk stores, which leave out rows and columns outside the matrix.
 template <int OP, bool LAST>
-__device__ __forceinline__ void orth_epilogue(const OrthGemm& g, int z, int64_t row, int64_t col,
-                                              bool mirror, float drow, const OrthIn<OP>& in,
-                                              float (&v)[32]) {
+__device__ __forceinline__ void orth_epilogue(const OrthGemm& g, const CUtensorMap* st0,
+                                              const CUtensorMap* st1, uint4* stage, int z,
+                                              int64_t row, int64_t col, bool mirror, float drow,
+                                              float dcol, float (&v)[32]) {
   const int lane = threadIdx.x & 31;
-  const int n = static_cast<int>(min(static_cast<int64_t>(32), g.cols - col));
-  const int64_t at = (static_cast<int64_t>(z) * g.rows + row) * g.ld + col;
-  const bool live = row < g.rows;
+  uint32_t in[2][16];
+#pragma unroll
+  for (int e = 0; e < OrthIn<OP>::kSets; ++e)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint4 w = stage[e * 128 + stage_piece(lane, q)];
+      in[e][4 * q] = w.x;
+      in[e][4 * q + 1] = w.y;
+      in[e][4 * q + 2] = w.z;
+      in[e][4 * q + 3] = w.w;
+    }
+  auto put_row = [&](int e, const uint32_t(&w)[16]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      stage[e * 128 + stage_piece(lane, q)] =
+          make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+  };
   uint32_t out[16];
   if (OP == kGram || OP == kSquare) {
-    const int e = static_cast<int>(row - col);  // the diagonal's column of the chunk, if in it
+    const int e = static_cast<int>(row - col);  // the diagonal's column of the block, if in it
     float d = 0.f;
     if (OP == kGram) {
 #pragma unroll
@@ -343,8 +346,8 @@ __device__ __forceinline__ void orth_epilogue(const OrthGemm& g, int z, int64_t 
     } else {
 #pragma unroll
       for (int c = 0; c < 32; ++c) {
-        const float dj = __shfl_sync(0xffffffffu, in.dcol, c);
-        const float2 r2 = unpack_half2(in.w[0][c / 2]);
+        const float dj = __shfl_sync(0xffffffffu, dcol, c);
+        const float2 r2 = unpack_half2(in[0][c / 2]);
         const float rr = v[c] * (1.f / (kScaleA * kScaleA));
         const float a = (c & 1 ? r2.y : r2.x) * (1.f / kScaleA);
         if (c == e) d = fmaf(g.c, fmaf(drow, drow, rr), g.b * drow);
@@ -353,53 +356,45 @@ __device__ __forceinline__ void orth_epilogue(const OrthGemm& g, int z, int64_t 
     }
 #pragma unroll
     for (int c = 0; c < 16; ++c) out[c] = pack_half2(v[2 * c], v[2 * c + 1]);
-    if (live) {
-      if (e >= 0 && e < 32) g.diag_out[static_cast<int64_t>(z) * g.diag_n + row] = d;
-      st_half32(g.a_out + at, n, out);
-    }
+    if (row < g.rows && e >= 0 && e < 32)
+      g.diag_out[static_cast<int64_t>(z) * g.diag_n + row] = d;
+    put_row(0, out);
     if (mirror) {
-      // Column c of the block goes out as row c: lanes hold consecutive rows, and two lanes
-      // trade halves so that each store carries two rows (a row past the last lands in the
-      // padding, which is not read).
-      __half* dst = g.a_out + (static_cast<int64_t>(z) * g.rows + col) * g.ld + (row & ~1);
+      // The block's transpose: two lanes trade halves, so that each word holds two rows.
+      uint32_t* t = reinterpret_cast<uint32_t*>(stage + 128);
       const bool odd = lane & 1;
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
         const uint32_t q = __shfl_xor_sync(0xffffffffu, out[c], 1);
-        const uint32_t w = odd ? __byte_perm(q, out[c], 0x7632) : __byte_perm(out[c], q, 0x5410);
-        const int cc = 2 * c + odd;
-        if ((row & ~1) < g.rows && cc < n)
-          *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(cc) * g.ld) = w;
+        const int cc = 2 * c + odd, word = lane >> 1;
+        t[stage_piece(cc, word >> 2) * 4 + (word & 3)] =
+            odd ? __byte_perm(q, out[c], 0x7632) : __byte_perm(out[c], q, 0x5410);
       }
     }
   } else {
 #pragma unroll
     for (int c = 0; c < 32; c += 2) {
-      const float2 hi = unpack_half2(in.w[0][c / 2]);
-      const float2 lo = unpack_half2(in.w[OrthIn<OP>::kSets - 1][c / 2]);
+      const float2 hi = unpack_half2(in[0][c / 2]), lo = unpack_half2(in[1][c / 2]);
       float d0 = drow, d1 = drow;
       if (g.tall) {
-        d0 = __shfl_sync(0xffffffffu, in.dcol, c);
-        d1 = __shfl_sync(0xffffffffu, in.dcol, c + 1);
+        d0 = __shfl_sync(0xffffffffu, dcol, c);
+        d1 = __shfl_sync(0xffffffffu, dcol, c + 1);
       }
       v[c] = fmaf(v[c], 1.f / kScaleB, fmaf(d0, hi.x, g.a * (hi.x + lo.x)));
       v[c + 1] = fmaf(v[c + 1], 1.f / kScaleB, fmaf(d1, hi.y, g.a * (hi.y + lo.y)));
     }
-    if (!live) return;
     if (LAST) {
-      __nv_bfloat16* dst = g.out + (static_cast<int64_t>(z) * g.rows + row) * g.cols + col;
+      if (g.out_vec) {
 #pragma unroll
-      for (int c = 0; c < 32; ++c) v[c] *= 1.f / kScaleX;
-      if (g.out_vec && n >= 32) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          reinterpret_cast<uint4*>(dst)[q] = make_uint4(
-              pack_bf162(v[8 * q], v[8 * q + 1]), pack_bf162(v[8 * q + 2], v[8 * q + 3]),
-              pack_bf162(v[8 * q + 4], v[8 * q + 5]), pack_bf162(v[8 * q + 6], v[8 * q + 7]));
-      } else {
+        for (int c = 0; c < 16; ++c)
+          out[c] = pack_bf162(v[2 * c] * (1.f / kScaleX), v[2 * c + 1] * (1.f / kScaleX));
+        put_row(0, out);
+      } else if (row < g.rows) {
+        // Rows of the result that do not start on 16-byte boundaries.
+        __nv_bfloat16* dst = g.out + (static_cast<int64_t>(z) * g.rows + row) * g.cols + col;
 #pragma unroll
         for (int c = 0; c < 32; ++c)
-          if (c < n) dst[c] = __float2bfloat16_rn(v[c]);
+          if (col + c < g.cols) dst[c] = __float2bfloat16_rn(v[c] * (1.f / kScaleX));
       }
     } else {
 #pragma unroll
@@ -409,10 +404,21 @@ __device__ __forceinline__ void orth_epilogue(const OrthGemm& g, int z, int64_t 
         v[2 * c] -= hi.x;
         v[2 * c + 1] -= hi.y;
       }
-      st_half32(g.hi_out + at, n, out);
+      put_row(0, out);
 #pragma unroll
       for (int c = 0; c < 16; ++c) out[c] = pack_half2(v[2 * c], v[2 * c + 1]);
-      st_half32(g.lo + at, n, out);
+      put_row(1, out);
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0 && !(LAST && !g.out_vec)) {
+    const int r0 = static_cast<int>(row), c0 = static_cast<int>(col);
+    if (r0 < g.rows) {
+      tma_store_3d(st0, stage, c0, r0, z);
+      if (OP == kUpdate && !LAST) tma_store_3d(st1, stage + 128, c0, r0, z);
+      if (OP != kUpdate && mirror) tma_store_3d(st0, stage + 128, r0, c0, z);
+      bulk_commit();
     }
   }
 }
@@ -420,7 +426,8 @@ __device__ __forceinline__ void orth_epilogue(const OrthGemm& g, int z, int64_t 
 template <int BNI, int NSUB, bool A_MN, bool B_MN, int OP, bool LAST>
 __global__ void __launch_bounds__(kOrthThreads, 1)
     orth_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-              const OrthGemm g, const DevCtl ctl) {
+              const __grid_constant__ CUtensorMap st0, const __grid_constant__ CUtensorMap st1,
+              const __grid_constant__ OrthGemm g, const DevCtl ctl) {
   using C = OrthCfg<BNI, NSUB>;
   constexpr int STAGES = C::kStages;
   constexpr uint32_t kIdesc = idesc_f16_f32(2 * kBM, BNI, A_MN, B_MN);
@@ -428,7 +435,8 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  OrthCtl<STAGES>* pc = reinterpret_cast<OrthCtl<STAGES>*>(smem + STAGES * C::kStageBytes);
+  OrthCtl<STAGES>* pc =
+      reinterpret_cast<OrthCtl<STAGES>*>(smem + C::kRing + 4 * kOrthWG * kOrthStage);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -610,6 +618,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     const int wg = (warp - 2) >> 2;
     const uint32_t lane_bits = static_cast<uint32_t>(q * 32) << 16;
     constexpr int kShare = BNI / kOrthWG, kChunks = kShare / 32;
+    uint4* stage = reinterpret_cast<uint4*>(smem + C::kRing + (warp - 2) * kOrthStage);
     const uint32_t tempty0 = mapa_shared(smem_u32(&pc->tempty[0]), 0);
     const uint32_t tempty1 = mapa_shared(smem_u32(&pc->tempty[1]), 0);
     uint32_t t = 0, used0 = 0, used1 = 0;
@@ -626,19 +635,25 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         uint32_t& used = b ? used1 : used0;
         const int64_t col0 = static_cast<int64_t>(j) * C::kTileN + h * BNI + wg * kShare;
         const bool mirror = kSym && col0 - wg * kShare + BNI <= static_cast<int64_t>(i) * 2 * kBM;
-        OrthIn<OP> in[2];
-        in[0].fetch(g, z, row, col0, lane);
+        const int64_t row0 = row - lane;
+        OrthIn<OP> in;
+        in.fetch(g, z, row0, col0, lane);
         if (!wait_warp(&pc->tfull[b], used & 1u, abort, ctl)) {
           ok = false;
           break;
         }
         ++used;
         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < kChunks; ++c) {
-          if (c + 1 < kChunks) in[(c + 1) & 1].fetch(g, z, row, col0 + (c + 1) * 32, lane);
           float v[32];
           tmem_ld32(tmem + lane_bits + b * BNI + wg * kShare + c * 32, v);
+          // The staging blocks are free once the stores of the block before have read them.
+          if (lane == 0) bulk_wait_read_all();
+          __syncwarp();
+          in.put(stage, lane);
+          const float dcol = in.dcol;
+          if (c + 1 < kChunks) in.fetch(g, z, row0, col0 + (c + 1) * 32, lane);
           tmem_ld_wait();
           if (c == kChunks - 1) {
             // The slot is drained once this load has completed.
@@ -647,12 +662,17 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
             // Test hook (fault == 1): withhold the release of the first accumulator.
             if (lane == 0 && !(ctl.fault == 1 && t == 0))
               mbar_arrive_cluster(b ? tempty1 : tempty0);
+          } else {
+            __syncwarp();
           }
           if (col0 + c * 32 < g.cols)
-            orth_epilogue<OP, LAST>(g, z, row, col0 + c * 32, mirror, drow, in[c & 1], v);
+            orth_epilogue<OP, LAST>(g, &st0, &st1, stage, z, row, col0 + c * 32, mirror, drow,
+                                    dcol, v);
         }
       }
     }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
   }
 
   // Neither CTA leaves while the other may still signal its barriers or use its TMEM.
@@ -663,7 +683,8 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
 }
 
 template <int BNI, int NSUB, bool A_MN, bool B_MN, int OP, bool LAST>
-cudaError_t launch_orth(const CUtensorMap& a, const CUtensorMap& b, const OrthGemm& g,
+cudaError_t launch_orth(const CUtensorMap& a, const CUtensorMap& b, const OrthMaps& st,
+                        const OrthGemm& g,
                         const DevCtl& c, cudaStream_t s) {
   using C = OrthCfg<BNI, NSUB>;
   auto kern = orth_gemm<BNI, NSUB, A_MN, B_MN, OP, LAST>;
@@ -698,21 +719,21 @@ cudaError_t launch_orth(const CUtensorMap& a, const CUtensorMap& b, const OrthGe
   }
   cfg.numAttrs = 2;
   cfg.gridDim = dim3(2 * std::max(1, std::min(g.num_units, max_clusters[dev])), 1, 1);
-  return cudaLaunchKernelEx(&cfg, kern, a, b, g, c);
+  return cudaLaunchKernelEx(&cfg, kern, a, b, *st.out0, *st.out1, g, c);
 }
 
 template <int BNI, int NSUB>
 cudaError_t launch_op(int op, bool tall, bool last, const CUtensorMap& a, const CUtensorMap& b,
-                      const OrthGemm& g, const DevCtl& c, cudaStream_t s) {
+                      const OrthMaps& st, const OrthGemm& g, const DevCtl& c, cudaStream_t s) {
   if (op == kGram)
-    return tall ? launch_orth<BNI, NSUB, true, true, kGram, false>(a, b, g, c, s)
-                : launch_orth<BNI, NSUB, false, false, kGram, false>(a, b, g, c, s);
-  if (op == kSquare) return launch_orth<BNI, NSUB, false, false, kSquare, false>(a, b, g, c, s);
+    return tall ? launch_orth<BNI, NSUB, true, true, kGram, false>(a, b, st, g, c, s)
+                : launch_orth<BNI, NSUB, false, false, kGram, false>(a, b, st, g, c, s);
+  if (op == kSquare) return launch_orth<BNI, NSUB, false, false, kSquare, false>(a, b, st, g, c, s);
   if (tall)
-    return last ? launch_orth<BNI, NSUB, false, false, kUpdate, true>(a, b, g, c, s)
-                : launch_orth<BNI, NSUB, false, false, kUpdate, false>(a, b, g, c, s);
-  return last ? launch_orth<BNI, NSUB, false, true, kUpdate, true>(a, b, g, c, s)
-              : launch_orth<BNI, NSUB, false, true, kUpdate, false>(a, b, g, c, s);
+    return last ? launch_orth<BNI, NSUB, false, false, kUpdate, true>(a, b, st, g, c, s)
+                : launch_orth<BNI, NSUB, false, false, kUpdate, false>(a, b, st, g, c, s);
+  return last ? launch_orth<BNI, NSUB, false, true, kUpdate, true>(a, b, st, g, c, s)
+              : launch_orth<BNI, NSUB, false, true, kUpdate, false>(a, b, st, g, c, s);
 }
 
 }  // namespace
@@ -745,11 +766,11 @@ cudaError_t launch_orth_prep(int dtype, const OrthPrep& p, int64_t batch, cudaSt
 }
 
 cudaError_t launch_orth_gemm(int op, int bn, bool tall, bool last, const CUtensorMap& a,
-                             const CUtensorMap& b, const OrthGemm& g, const DevCtl& c,
-                             cudaStream_t s) {
-  if (bn == 512) return launch_op<256, 2>(op, tall, last, a, b, g, c, s);
-  return bn == 128 ? launch_op<128, 1>(op, tall, last, a, b, g, c, s)
-                   : launch_op<256, 1>(op, tall, last, a, b, g, c, s);
+                             const CUtensorMap& b, const OrthMaps& st, const OrthGemm& g,
+                             const DevCtl& c, cudaStream_t s) {
+  if (bn == 512) return launch_op<256, 2>(op, tall, last, a, b, st, g, c, s);
+  return bn == 128 ? launch_op<128, 1>(op, tall, last, a, b, st, g, c, s)
+                   : launch_op<256, 1>(op, tall, last, a, b, st, g, c, s);
 }
 
 }  // namespace slm
