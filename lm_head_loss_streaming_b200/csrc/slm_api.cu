@@ -448,8 +448,6 @@ int norm_checks(int dtype, const void* x, int64_t ldx, const void* y, int64_t ld
 }
 
 // Orthogonalised update.
-constexpr int kMaxOrthSteps = 64;
-
 struct OrthLayout {
   size_t status_off, sums_off, diag_off[2], a_off[2], hi_off[2], lo_off, total;
   int64_t k, ldx, ldk;
@@ -528,44 +526,51 @@ bool make_map_stack(CUtensorMap* m, const void* base, int64_t inner, int64_t out
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Tile grid of one product and its tile width (512, 256 or 128 columns): the one whose rounds
-// of tiles over the CTA pairs are estimated to take least.  Per 64-wide K block a tile takes
-// its MMAs (27 TFLOP/s per pair) or its operands' way from L2 (9.3 TB/s shared by the pairs
-// that are busy), whichever is longer; both rates as measured on the products of 4096 x 4096
-// matrices.  A round also costs its epilogue, about 1 us per 128 columns.  Wide tiles read
-// less from L2 per flop, narrow ones leave fewer pairs idle: 4096 x 4096 updates take 178 us at
-// 128 columns and 98 at 512, 256 x 256 ones run only on as many pairs as there are tiles.
-int orth_tiles(OrthGemm* g, int64_t rows, int64_t cols, int64_t k, int64_t batch, bool sym) {
+// Tile grid of one product (rows x cols outputs over k, tiles of 256 x bn) and its estimated
+// seconds.  Per 64-wide K block a tile takes its MMAs (27 TFLOP/s per pair) or its operands' way
+// from L2 (9.3 TB/s shared by the pairs that are busy), whichever is longer; both rates as
+// measured on the products of 4096 x 4096 matrices.  A round of tiles also costs its epilogue,
+// about 0.5 us per 128 columns.
+double orth_tiles(OrthGeom* g, int bn, int64_t rows, int64_t cols, int64_t k, int64_t batch,
+                  bool sym) {
   const int64_t pairs = std::max(1, sm_count() / 2);
+  const int64_t nm = ceil_div(rows, kPairM), nn = ceil_div(cols, bn);
+  // Symmetric: the tiles that reach below the diagonal.
+  const int64_t per = !sym ? nm * nn : bn == 512 ? (nm + 1) * (nm + 1) / 4
+                      : (kPairM / bn) * (nm - 1) * nm / 2 + nn;
+  const int64_t units = per * batch;
+  g->num_m = static_cast<int>(nm);
+  g->num_n = static_cast<int>(nn);
+  g->units_per = static_cast<int>(per);
+  g->num_units = static_cast<int>(units);
+  g->k_blocks = static_cast<int>(ceil_div(k, kBK));
+  auto round = [&](int64_t busy) {
+    const double mma = 2.0 * kPairM * bn * kBK / 27e12;
+    const double l2 = (kPairM + bn) * kBK * 2.0 * static_cast<double>(busy) / 9.3e12;
+    return g->k_blocks * std::max(mma, l2) + 0.5e-6 * bn / 128;
+  };
+  return static_cast<double>(units / pairs) * round(pairs) +
+         (units % pairs != 0 ? round(units % pairs) : 0.0);
+}
+
+// The tile grids of a step's three products and their tiles' width: of 512, 256 and 128 columns
+// the one whose rounds are estimated to take least.  Wide tiles read less from L2 per flop,
+// narrow ones leave fewer pairs idle: the update of a 4096 x 4096 matrix took 178 us at 128
+// columns and 125 at 512, the products of a 2048 x 2048 one run on half of the pairs at 512.
+int orth_plan(OrthChain* ch, int64_t m, int64_t n, int64_t batch) {
+  const int64_t k = std::min(m, n), l = std::max(m, n);
   int best = 0;
   double best_cost = 0;
   for (int bn : {512, 256, 128}) {
-    const int64_t nm = ceil_div(rows, kPairM), nn = ceil_div(cols, bn);
-    // Symmetric: the tiles that reach below the diagonal.
-    const int64_t per = !sym ? nm * nn : bn == 512 ? (nm + 1) * (nm + 1) / 4
-                        : (kPairM / bn) * (nm - 1) * nm / 2 + nn;
-    const int64_t units = per * batch;
-    const double kb = static_cast<double>(ceil_div(k, kBK));
-    auto round = [&](int64_t busy) {
-      const double mma = 2.0 * kPairM * bn * kBK / 27e12;
-      const double l2 = (kPairM + bn) * kBK * 2.0 * static_cast<double>(busy) / 9.3e12;
-      return kb * std::max(mma, l2) + 1e-6 * bn / 128;
-    };
-    const double cost = static_cast<double>(units / pairs) * round(pairs) +
-                        (units % pairs != 0 ? round(units % pairs) : 0.0);
-    if (best == 0 || cost < best_cost) {
-      best_cost = cost;
-      best = bn;
-      g->num_m = static_cast<int>(nm);
-      g->num_n = static_cast<int>(nn);
-      g->units_per = static_cast<int>(per);
-      g->num_units = static_cast<int>(units);
-    }
+    OrthGeom g[3];
+    const double cost = orth_tiles(&g[0], bn, k, k, l, batch, true) +
+                        orth_tiles(&g[1], bn, k, k, k, batch, true) +
+                        orth_tiles(&g[2], bn, m, n, k, batch, false);
+    if (best != 0 && cost >= best_cost) continue;
+    best = bn;
+    best_cost = cost;
+    std::copy(g, g + 3, ch->geom);
   }
-  g->k_blocks = static_cast<int>(ceil_div(k, kBK));
-  g->group_m = std::min(kGroupPairs, g->num_m);
-  g->rows = rows;
-  g->cols = cols;
   return best;
 }
 
@@ -1257,78 +1262,59 @@ int slm_orthogonalize(int dtype, const void* grad, int64_t ld, int64_t batch_str
   float* diag[2] = {reinterpret_cast<float*>(ws + L.diag_off[0]),
                     reinterpret_cast<float*>(ws + L.diag_off[1])};
   const bool tall = m > n;
-  const int64_t k = L.k, l = std::max(m, n);
-
-  OrthGemm gram{}, square{}, update{};
-  const int bn_gram = orth_tiles(&gram, k, k, l, batch, true);
-  const int bn_square = orth_tiles(&square, k, k, k, batch, true);
-  const int bn_update = orth_tiles(&update, m, n, k, batch, false);
-  gram.ld = square.ld = L.ldk;
-  gram.a_out = mat[0];
-  gram.diag_out = diag[0];
-  square.a_in = mat[0];
-  square.a_out = mat[1];
-  square.diag_in = diag[0];
-  square.diag_out = diag[1];
-  update.ld = L.ldx;
-  update.diag_in = diag[1];
-  gram.diag_n = square.diag_n = update.diag_n = k;
-  update.lo = lo;
-  update.out = static_cast<__nv_bfloat16*>(out);
-  update.tall = tall ? 1 : 0;
-  update.out_vec = n % 8 == 0 && !misaligned(out, 16);
-
-  // Operand maps.  A K-major operand has boxes of 64 (K) x 128 rows, its B form the columns
-  // that one CTA holds; an MN-major operand (X seen from its long side's other end) 64 x 64.
-  CUtensorMap xa[2], xb[2], ra, rb, ba, bb;
+  const int64_t k = L.k;
+  OrthChain ch{};
+  const int bn = orth_plan(&ch, m, n, batch);
+  ch.steps = steps;
+  ch.out_vec = n % 8 == 0 && !misaligned(out, 16);
+  ch.m = m;
+  ch.n = n;
+  ch.k = k;
+  ch.ldx = L.ldx;
+  ch.ldk = L.ldk;
+  ch.lo = lo;
+  ch.out = static_cast<__nv_bfloat16*>(out);
+  ch.counter = status + 1;
   for (int i = 0; i < 2; ++i) {
-    // The A and B operands of X X^T; of X^T X both are MN-major.
-    if (!make_map_stack(&xa[i], hi[i], n, m, L.ldx, batch, 64, tall ? 64 : kBM)) return SLM_ERR_CUDA;
-    if (!make_map_stack(&xb[i], hi[i], n, m, L.ldx, batch, 64, tall ? 64 : std::min(bn_gram, 256) / 2))
+    ch.hi[i] = hi[i];
+    ch.mat[i] = mat[i];
+    ch.diag[i] = diag[i];
+  }
+  memcpy(ch.co, coefficients, static_cast<size_t>(steps) * 3 * sizeof(float));
+
+  // Operand maps: a K-major operand has boxes of 64 (K) x its rows per CTA (128 of A, half a
+  // slot's columns of B), an MN-major one (X seen from its other end) of 64 x 64.
+  OrthMaps maps;
+  const int slice = std::min(bn, 256) / 2;
+  for (int i = 0; i < 2; ++i) {
+    // X X^T, or X^T X with both operands MN-major; B X with X MN-major, or X B.
+    if (!make_map_stack(&maps.a[0][i], hi[i], n, m, L.ldx, batch, 64, tall ? 64 : kBM) ||
+        !make_map_stack(&maps.b[0][i], hi[i], n, m, L.ldx, batch, 64, tall ? 64 : slice) ||
+        !make_map_stack(tall ? &maps.a[2][i] : &maps.b[2][i], hi[i], n, m, L.ldx, batch, 64,
+                        tall ? kBM : 64) ||
+        !make_map_stack(&maps.hi[i], hi[i], n, m, L.ldx, batch, 32, 32) ||
+        !make_map_stack(&maps.mat[i], mat[i], k, k, L.ldk, batch, 32, 32))
       return SLM_ERR_CUDA;
   }
-  if (!make_map_stack(&ra, mat[0], k, k, L.ldk, batch, 64, kBM) ||
-      !make_map_stack(&rb, mat[0], k, k, L.ldk, batch, 64, std::min(bn_square, 256) / 2) ||
-      !make_map_stack(&ba, mat[1], k, k, L.ldk, batch, 64, kBM) ||
-      !make_map_stack(&bb, mat[1], k, k, L.ldk, batch, 64, std::min(bn_update, 256) / 2))
+  if (!make_map_stack(&maps.a[1][0], mat[0], k, k, L.ldk, batch, 64, kBM) ||
+      !make_map_stack(&maps.b[1][0], mat[0], k, k, L.ldk, batch, 64, slice) ||
+      !make_map_stack(tall ? &maps.b[2][0] : &maps.a[2][0], mat[1], k, k, L.ldk, batch, 64,
+                      tall ? slice : kBM) ||
+      !make_map_stack(&maps.lo, lo, n, m, L.ldx, batch, 32, 32))
     return SLM_ERR_CUDA;
-  CUtensorMap xu[2];  // X in the update: X B has it as K-major A, B X as MN-major B
-  for (int i = 0; i < 2; ++i)
-    if (!make_map_stack(&xu[i], hi[i], n, m, L.ldx, batch, 64, tall ? kBM : 64)) return SLM_ERR_CUDA;
-
-  // Store maps: hi (two buffers), lo, R, R_B and the result.
-  CUtensorMap s_hi[2], s_lo, s_mat[2], s_out{};
-  for (int i = 0; i < 2; ++i)
-    if (!make_map_stack(&s_hi[i], hi[i], n, m, L.ldx, batch, 32, 32) ||
-        !make_map_stack(&s_mat[i], mat[i], k, k, L.ldk, batch, 32, 32))
-      return SLM_ERR_CUDA;
-  if (!make_map_stack(&s_lo, lo, n, m, L.ldx, batch, 32, 32) ||
-      (update.out_vec &&
-       !make_map_stack(&s_out, out, n, m, n, batch, 32, 32, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16)))
+  maps.a[1][1] = maps.a[1][0];
+  maps.b[1][1] = maps.b[1][0];
+  (tall ? maps.b : maps.a)[2][1] = (tall ? maps.b : maps.a)[2][0];
+  maps.out = maps.lo;  // unused unless the result can be stored in bulk
+  if (ch.out_vec &&
+      !make_map_stack(&maps.out, out, n, m, n, batch, 32, 32, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16))
     return SLM_ERR_CUDA;
 
-  const DevCtl ctl = make_ctl(status);
   const OrthPrep prep{grad, m, n, ld, batch_stride, L.ldx, momentum, static_cast<float>(beta),
                       static_cast<float>(1.0 - beta), eps, nesterov,
-                      reinterpret_cast<double*>(ws + L.sums_off), hi[0], lo, status};
+                      reinterpret_cast<double*>(ws + L.sums_off), hi[0], lo, status, ch.counter};
   SLM_LAUNCH(kTrOrth, launch_orth_prep(dtype, prep, batch, s));
-  for (int i = 0; i < steps; ++i) {
-    const int cur = i & 1;
-    const bool last = i == steps - 1;
-    SLM_LAUNCH(kTrOrth, launch_orth_gemm(0, bn_gram, tall, false, xa[cur], xb[cur],
-                                         OrthMaps{&s_mat[0], &s_mat[0]}, gram, ctl, s));
-    square.b = coefficients[3 * i + 1];
-    square.c = coefficients[3 * i + 2];
-    SLM_LAUNCH(kTrOrth, launch_orth_gemm(1, bn_square, tall, false, ra, rb,
-                                         OrthMaps{&s_mat[1], &s_mat[1]}, square, ctl, s));
-    update.a = coefficients[3 * i];
-    update.hi_in = hi[cur];
-    update.hi_out = hi[cur ^ 1];
-    SLM_LAUNCH(kTrOrth, launch_orth_gemm(2, bn_update, tall, last, tall ? xu[cur] : ba,
-                                         tall ? bb : xu[cur],
-                                         OrthMaps{last ? &s_out : &s_hi[cur ^ 1], &s_lo}, update,
-                                         ctl, s));
-  }
+  SLM_LAUNCH(kTrOrth, launch_orth_chain(bn, tall, ch, maps, make_ctl(status), s));
   return SLM_OK;
 }
 

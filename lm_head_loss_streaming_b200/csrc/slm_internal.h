@@ -312,33 +312,45 @@ struct OrthPrep {
   int nesterov;
   double* sums;  // [batch][kOrthSums]
   __half *hi, *lo;
-  int* status;
+  int *status, *counter;
 };
-// One product over the stack: rows x cols outputs per matrix, tiles of 256 x bn.
-struct OrthGemm {
-  int num_m, num_n, units_per, num_units, k_blocks, group_m;
-  int64_t rows, cols, ld;  // of the output (fp16 matrices: ld elements per row)
-  const __half* a_in;      // kSquare: R
-  __half* a_out;           // kGram: R; kSquare: R_B
-  const float* diag_in;    // kSquare: D; kUpdate: D_B
-  float* diag_out;         // kGram: D; kSquare: D_B
-  const __half* hi_in;
-  __half *hi_out, *lo;
+// The products' tile grids and data.  Products 0 (R and D of A), 1 (R_B and D_B) and 2 (the
+// update of X) of each step; [i] of hi and of the maps is the buffer that step i & 1 reads.
+constexpr int kMaxOrthSteps = 64;
+constexpr int kOrthGroup = 8;  // row tiles per raster group of the update
+struct OrthGeom {
+  int num_m, num_n, units_per, num_units, k_blocks;
+};
+struct OrthChain {
+  OrthGeom geom[3];
+  int steps, out_vec;       // out_vec: the result's rows start on 16-byte boundaries
+  int64_t m, n, k, ldx, ldk;
+  __half *hi[2], *lo, *mat[2];  // mat: R, R_B
+  float* diag[2];               // D, D_B: [batch][k]
   __nv_bfloat16* out;
-  int64_t diag_n;  // entries of a diagonal per matrix
-  float a, b, c;
-  int tall, out_vec;
+  int* counter;  // arrivals at the meetings between products; zero at launch
+  float co[kMaxOrthSteps][3];
 };
-// op: 0 R and D of X X^T (X^T X when tall), 1 R_B and D_B, 2 the update of X (`last`: to out).
-cudaError_t launch_orth_prep(int dtype, const OrthPrep& p, int64_t batch, cudaStream_t s);
-// out0: the store map of a_out, hi_out or out; out1: that of lo (kUpdate).  Boxes of 32 x 32,
-// 64-byte swizzle.
 struct OrthMaps {
-  const CUtensorMap *out0, *out1;
+  CUtensorMap a[3][2], b[3][2];         // operands of the products
+  CUtensorMap hi[2], lo, mat[2], out;   // stores: boxes of 32 x 32, 64-byte swizzle
 };
-cudaError_t launch_orth_gemm(int op, int bn, bool tall, bool last, const CUtensorMap& a,
-                             const CUtensorMap& b, const OrthMaps& st, const OrthGemm& g,
-                             const DevCtl& c, cudaStream_t s);
+// What one product's epilogue sees of it.
+struct OrthView {
+  int64_t rows, cols, ld, diag_n;
+  const __half* in;  // kSquare: R; kUpdate: hi
+  const __half* lo;
+  const float* diag_in;
+  float* diag_out;
+  __nv_bfloat16* out;
+  float a, b, c;
+  bool tall;
+  int out_vec;
+};
+cudaError_t launch_orth_prep(int dtype, const OrthPrep& p, int64_t batch, cudaStream_t s);
+// bn: the tiles' columns (512, 256 or 128); operand maps as their boxes need it.
+cudaError_t launch_orth_chain(int bn, bool tall, const OrthChain& ch, const OrthMaps& maps,
+                              const DevCtl& c, cudaStream_t s);
 
 constexpr int kCombineThreads = 256;
 

@@ -99,7 +99,10 @@ template <class T, int V>
 __global__ void __launch_bounds__(kPrepThreads) orth_moment(const OrthPrep p) {
   const int64_t b = blockIdx.y;
   const int64_t groups = p.m * (p.n / V);
-  if (blockIdx.x == 0 && b == 0 && threadIdx.x == 0) *p.status = 0;
+  if (blockIdx.x == 0 && b == 0 && threadIdx.x == 0) {
+    *p.status = 0;
+    *p.counter = 0;
+  }
   double s = 0.0;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPrepThreads + threadIdx.x; i < groups;
        i += static_cast<int64_t>(gridDim.x) * kPrepThreads) {
@@ -182,14 +185,18 @@ __global__ void __launch_bounds__(kPrepThreads) orth_scale(const OrthPrep p, int
 }
 
 // ----------------------------------------------------------------------------------------
-// The products: a persistent 2-SM GEMM (M = 256 rows per CTA pair, fp16 operands).  Warp 0
-// loads, warp 1 issues the MMAs, eight warps run the epilogue, each warpgroup over half of the
-// columns.  Operands are K-major or MN-major as they lie in memory, so that no transpose of X
-// is ever stored.
+// The products: all of them in one cooperative launch of 2-SM GEMMs (M = 256 rows per CTA pair,
+// fp16 operands).  Warp 0 loads, warp 1 issues the MMAs, eight warps run the epilogue, each
+// warpgroup over half of the columns.  Operands are K-major or MN-major as they lie in memory,
+// so that no transpose of X is ever stored.  Per step:
 //   kGram    R, D of A = X X^T:  a symmetric product, only blocks on and below the diagonal
 //            are computed and each is written to its mirrored place too
 //   kSquare  R_B, D_B of B = b A + c A^2, symmetric in the same way
 //   kUpdate  hi, lo of a X + B X; in the last step the result in bf16
+// A product reads what the one before wrote anywhere, so the CTAs meet between products (a
+// counter in the workspace, bounded waits; the cooperative launch makes them all resident).
+// A meeting costs about 2 us, a launch of its own with its set-up and drain 7 us: 256 x 256
+// matrices, which are all latency, took 116 us of GPU time in 15 launches.
 // The tensor memory holds two accumulator slots of BNI columns.  NSUB = 1: tiles take the slots
 // in turn, so that a tile's epilogue overlaps the next tile's MMAs.  NSUB = 2: a tile of 512
 // columns takes both; the operands then cross from L2 at 170 instead of 128 flops per byte, and
@@ -200,6 +207,42 @@ __global__ void __launch_bounds__(kPrepThreads) orth_scale(const OrthPrep p, int
 enum OrthOp { kGram = 0, kSquare = 1, kUpdate = 2 };
 constexpr int kOrthWG = 2;
 constexpr int kOrthThreads = 64 + 128 * kOrthWG;
+// Meeting of the CTAs between products.
+__device__ __forceinline__ int ld_acquire_s32(const int* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void red_release_add_s32(int* p, int v) {
+  asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ void fence_proxy_async_global() {
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+}
+// Waits (boundedly; lane 0 polls) until `target` arrivals are counted; what the arriving CTAs
+// wrote is then visible to this thread's loads and bulk copies.
+__device__ __forceinline__ bool wait_met(const int* counter, int target, volatile int* abort,
+                                         const DevCtl& ctl) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) {
+    const long long t0 = clock64();
+    while (ld_acquire_s32(counter) < target) {
+      if (*abort) {
+        ok = 0;
+        break;
+      }
+      if (clock64() - t0 > ctl.timeout_cycles) {
+        *abort = 1;
+        atomicOr(ctl.status, kFlagTimeout);
+        ok = 0;
+        break;
+      }
+    }
+    fence_proxy_async_global();
+  }
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
 // Staging of an epilogue warp: two blocks of 32 rows x 32 fp16 columns, 64 bytes per row, in
 // the 64-byte swizzle of the store maps (16-byte piece k of row r at k ^ (r / 2 % 4)).
 constexpr int kOrthStage = 4096;
@@ -209,9 +252,9 @@ __device__ __forceinline__ int stage_piece(int row, int k) {
 
 template <int STAGES>
 struct OrthCtl {
-  uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], fin;
+  uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], fin, met;
   uint32_t tmem_base;
-  int abort;
+  int abort, done;
 };
 
 template <int BNI, int NSUB>
@@ -231,7 +274,7 @@ struct OrthCfg {
 // Tile of unit u: matrix z, pair row tile i, column tile j, and how many of its slots' columns
 // are wanted (of a symmetric product, the blocks right of the diagonal are not).
 template <int BNI, int NSUB, bool SYM>
-__device__ __forceinline__ void orth_unit(const OrthGemm& g, int u, int& z, int& i, int& j,
+__device__ __forceinline__ void orth_unit(const OrthGeom& g, int u, int& z, int& i, int& j,
                                           int& nsub) {
   z = u / g.units_per;
   const int t = u - z * g.units_per;
@@ -251,12 +294,12 @@ __device__ __forceinline__ void orth_unit(const OrthGemm& g, int u, int& z, int&
     while (W * (i + 1) * (i + 2) / 2 <= t) ++i;
     j = t - W * i * (i + 1) / 2;
   } else {
-    const int per_group = g.group_m * g.num_n;
+    const int per_group = kOrthGroup * g.num_n;
     const int grp = t / per_group;
     const int r = t - grp * per_group;
-    const int gm = min(g.group_m, g.num_m - grp * g.group_m);
+    const int gm = min(kOrthGroup, g.num_m - grp * kOrthGroup);
     j = r / gm;
-    i = grp * g.group_m + (r - j * gm);
+    i = grp * kOrthGroup + (r - j * gm);
   }
 }
 
@@ -280,7 +323,7 @@ struct OrthIn {
   static constexpr int kSets = OP == kGram ? 0 : OP == kSquare ? 1 : 2;
   uint4 w[kSets == 0 ? 1 : kSets][4];  // kSquare: R; kUpdate: hi, lo
   float dcol;                          // lane l: the diagonal's entry of column col + l
-  __device__ __forceinline__ void fetch(const OrthGemm& g, int z, int64_t row0, int64_t col,
+  __device__ __forceinline__ void fetch(const OrthView& g, int z, int64_t row0, int64_t col,
                                         int lane) {
     if (OP == kGram || col >= g.cols) return;
     if (OP == kSquare || g.tall)
@@ -293,7 +336,7 @@ struct OrthIn {
       const bool in = row < g.rows && c < g.cols;  // rows are padded to whole pieces
       const uint4 none = make_uint4(0, 0, 0, 0);
       w[0][q] = !in ? none
-                    : *reinterpret_cast<const uint4*>((OP == kSquare ? g.a_in : g.hi_in) + at);
+                    : *reinterpret_cast<const uint4*>(g.in + at);
       if (OP == kUpdate) w[kSets - 1][q] = !in ? none : *reinterpret_cast<const uint4*>(g.lo + at);
     }
   }
@@ -311,7 +354,7 @@ struct OrthIn {
 // inputs lie in the staging blocks; its outputs take their place, each lane its own row, and go
 // out by bulk stores, which leave out rows and columns outside the matrix.
 template <int OP, bool LAST>
-__device__ __forceinline__ void orth_epilogue(const OrthGemm& g, const CUtensorMap* st0,
+__device__ __forceinline__ void orth_epilogue(const OrthView& g, const CUtensorMap* st0,
                                               const CUtensorMap* st1, uint4* stage, int z,
                                               int64_t row, int64_t col, bool mirror, float drow,
                                               float dcol, float (&v)[32]) {
@@ -384,17 +427,21 @@ __device__ __forceinline__ void orth_epilogue(const OrthGemm& g, const CUtensorM
       v[c + 1] = fmaf(v[c + 1], 1.f / kScaleB, fmaf(d1, hi.y, g.a * (hi.y + lo.y)));
     }
     if (LAST) {
-      if (g.out_vec) {
 #pragma unroll
-        for (int c = 0; c < 16; ++c)
-          out[c] = pack_bf162(v[2 * c] * (1.f / kScaleX), v[2 * c + 1] * (1.f / kScaleX));
-        put_row(0, out);
-      } else if (row < g.rows) {
-        // Rows of the result that do not start on 16-byte boundaries.
-        __nv_bfloat16* dst = g.out + (static_cast<int64_t>(z) * g.rows + row) * g.cols + col;
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if (col + c < g.cols) dst[c] = __float2bfloat16_rn(v[c] * (1.f / kScaleX));
+      for (int c = 0; c < 16; ++c)
+        out[c] = pack_bf162(v[2 * c] * (1.f / kScaleX), v[2 * c + 1] * (1.f / kScaleX));
+      put_row(0, out);
+      if (!g.out_vec) {
+        // Rows of the result that do not start on 16-byte boundaries: element stores, a row
+        // per instruction.
+        __syncwarp();
+        const __nv_bfloat16* el = reinterpret_cast<const __nv_bfloat16*>(stage);
+        const int64_t r0 = row - lane;
+        __nv_bfloat16* dst = g.out + (static_cast<int64_t>(z) * g.rows + r0) * g.cols + col + lane;
+        const int rows = static_cast<int>(min(static_cast<int64_t>(32), g.rows - r0));
+        if (col + lane < g.cols)
+          for (int r = 0; r < rows; ++r)
+            dst[r * g.cols] = el[stage_piece(r, lane >> 3) * 8 + (lane & 7)];
       }
     } else {
 #pragma unroll
@@ -423,15 +470,12 @@ __device__ __forceinline__ void orth_epilogue(const OrthGemm& g, const CUtensorM
   }
 }
 
-template <int BNI, int NSUB, bool A_MN, bool B_MN, int OP, bool LAST>
+template <int BNI, int NSUB, bool TALL>
 __global__ void __launch_bounds__(kOrthThreads, 1)
-    orth_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-              const __grid_constant__ CUtensorMap st0, const __grid_constant__ CUtensorMap st1,
-              const __grid_constant__ OrthGemm g, const DevCtl ctl) {
+    orth_chain(const __grid_constant__ OrthChain ch, const __grid_constant__ OrthMaps maps,
+               const DevCtl ctl) {
   using C = OrthCfg<BNI, NSUB>;
   constexpr int STAGES = C::kStages;
-  constexpr uint32_t kIdesc = idesc_f16_f32(2 * kBM, BNI, A_MN, B_MN);
-  constexpr bool kSym = OP != kUpdate;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -444,9 +488,6 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   const int pair = blockIdx.x >> 1;
   const int npairs = gridDim.x >> 1;
 
-  // The next launch of the chain may begin its set-up; this one's is done before it waits for
-  // the launch before it, whose results everything below reads.
-  launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&pc->full[s], 1);
@@ -457,12 +498,10 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
       mbar_init(&pc->tempty[b], 2 * 4 * kOrthWG);  // one arrive per epilogue warp, both CTAs
     }
     mbar_init(&pc->fin, 1);
+    mbar_init(&pc->met, 1);
     pc->abort = 0;
+    pc->done = 0;
     fence_barrier_init();
-  }
-  if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmB);
   }
   if (warp == 1) {
     tmem_alloc_pair(&pc->tmem_base, 512);
@@ -473,49 +512,73 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   tc_fence_after();
   const uint32_t tmem = pc->tmem_base;
   volatile int* abort = &pc->abort;
-  wait_prior_launch();
+  const int products = 3 * ch.steps;
 
   if (warp == 0) {
     // TMA producer (both CTAs); both CTAs' copies complete on the leader's "full" barrier.
     uint32_t it = 0;
     bool ok = true;
-    for (int u = pair; ok && u < g.num_units; u += npairs) {
-      int z, i, j, nsub;
-      orth_unit<BNI, NSUB, kSym>(g, u, z, i, j, nsub);
-      const int mrow = i * 2 * kBM + static_cast<int>(rank) * kBM;
-      for (int kb = 0; kb < g.k_blocks; ++kb, ++it) {
-        const int s = it % STAGES;
-        if (!wait_warp(&pc->empty[s], ((it / STAGES) & 1u) ^ 1u, abort, ctl)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          uint8_t* st = smem + s * C::kStageBytes;
-          if (leader)
-            mbar_arrive_expect_tx(&pc->full[s], 2 * (C::kABytes + nsub * C::kSliceBytes));
-          const int k0 = kb * kBK;
-          if (A_MN) {
-            tma_load_3d_pair(st, &tmA, &pc->full[s], mrow, k0, z);
-            tma_load_3d_pair(st + 8192, &tmA, &pc->full[s], mrow + 64, k0, z);
-          } else {
-            tma_load_3d_pair(st, &tmA, &pc->full[s], k0, mrow, z);
+    auto product = [&](auto opc, int cur) {
+      constexpr int OP = decltype(opc)::value;
+      constexpr bool A_MN = TALL && OP == kGram;
+      constexpr bool B_MN = (TALL && OP == kGram) || (!TALL && OP == kUpdate);
+      const OrthGeom& g = ch.geom[OP];
+      const CUtensorMap* ma = &maps.a[OP][cur];
+      const CUtensorMap* mb = &maps.b[OP][cur];
+      for (int u = pair; ok && u < g.num_units; u += npairs) {
+        int z, i, j, nsub;
+        orth_unit<BNI, NSUB, OP != kUpdate>(g, u, z, i, j, nsub);
+        const int mrow = i * 2 * kBM + static_cast<int>(rank) * kBM;
+        for (int kb = 0; kb < g.k_blocks; ++kb, ++it) {
+          const int s = it % STAGES;
+          if (!wait_warp(&pc->empty[s], ((it / STAGES) & 1u) ^ 1u, abort, ctl)) {
+            ok = false;
+            break;
           }
-#pragma unroll
-          for (int h = 0; h < NSUB; ++h) {
-            if (h >= nsub) break;
-            uint8_t* bst = st + C::kABytes + h * C::kSliceBytes;
-            const int ncol = j * C::kTileN + h * BNI + static_cast<int>(rank) * C::kSliceN;
-            if (B_MN) {
-#pragma unroll
-              for (int q = 0; q < C::kSliceN / 64; ++q)
-                tma_load_3d_pair(bst + q * 8192, &tmB, &pc->full[s], ncol + q * 64, k0, z);
+          if (lane == 0) {
+            uint8_t* st = smem + s * C::kStageBytes;
+            if (leader)
+              mbar_arrive_expect_tx(&pc->full[s], 2 * (C::kABytes + nsub * C::kSliceBytes));
+            const int k0 = kb * kBK;
+            if (A_MN) {
+              tma_load_3d_pair(st, ma, &pc->full[s], mrow, k0, z);
+              tma_load_3d_pair(st + 8192, ma, &pc->full[s], mrow + 64, k0, z);
             } else {
-              tma_load_3d_pair(bst, &tmB, &pc->full[s], k0, ncol, z);
+              tma_load_3d_pair(st, ma, &pc->full[s], k0, mrow, z);
+            }
+#pragma unroll
+            for (int h = 0; h < NSUB; ++h) {
+              if (h >= nsub) break;
+              uint8_t* bst = st + C::kABytes + h * C::kSliceBytes;
+              const int ncol = j * C::kTileN + h * BNI + static_cast<int>(rank) * C::kSliceN;
+              if (B_MN) {
+#pragma unroll
+                for (int q = 0; q < C::kSliceN / 64; ++q)
+                  tma_load_3d_pair(bst + q * 8192, mb, &pc->full[s], ncol + q * 64, k0, z);
+              } else {
+                tma_load_3d_pair(bst, mb, &pc->full[s], k0, ncol, z);
+              }
             }
           }
+          __syncwarp();
         }
-        __syncwarp();
       }
+    };
+    for (int p = 0; ok && p < products; ++p) {
+      if (p > 0) {
+        // Every CTA has finished the product before; let this CTA's epilogue know.
+        ok = wait_met(ch.counter, p * static_cast<int>(gridDim.x), abort, ctl);
+        if (lane == 0) mbar_arrive(&pc->met);
+        __syncwarp();
+        if (!ok) break;
+      }
+      const int cur = (p / 3) & 1;
+      if (p % 3 == 0)
+        product(std::integral_constant<int, kGram>{}, cur);
+      else if (p % 3 == 1)
+        product(std::integral_constant<int, kSquare>{}, 0);
+      else
+        product(std::integral_constant<int, kUpdate>{}, cur);
     }
     if (ok) {
       // No remote release of a stage may reach this CTA after it has exited: wait for the
@@ -539,73 +602,85 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     if (leader) {
       uint32_t it = 0, t = 0, used0 = 0, used1 = 0;
       bool ok = true;
-      // The MMAs of stage `st` into slot b (operand slice h); first = the tile's first K block.
-      auto issue = [&](int st, int h, int b, bool first) {
-        const uint32_t a_addr = smem_u32(smem + st * C::kStageBytes);
-        const uint32_t b_addr = a_addr + C::kABytes + h * C::kSliceBytes;
+      auto product = [&](auto opc) {
+        constexpr int OP = decltype(opc)::value;
+        constexpr bool A_MN = TALL && OP == kGram;
+        constexpr bool B_MN = (TALL && OP == kGram) || (!TALL && OP == kUpdate);
+        constexpr uint32_t kIdesc = idesc_f16_f32(2 * kBM, BNI, A_MN, B_MN);
+        const OrthGeom& g = ch.geom[OP];
+        // The MMAs of stage `st` into slot b (operand slice h); first = the tile's first K block.
+        auto issue = [&](int st, int h, int b, bool first) {
+          const uint32_t a_addr = smem_u32(smem + st * C::kStageBytes);
+          const uint32_t b_addr = a_addr + C::kABytes + h * C::kSliceBytes;
 #pragma unroll
-        for (int kk = 0; kk < kBK / 16; ++kk) {
-          const uint64_t ad = A_MN ? smem_desc_sw128(a_addr + kk * 2048, 8192, 1024)
-                                   : smem_desc_sw128(a_addr + kk * 32, 16, 1024);
-          const uint64_t bd = B_MN ? smem_desc_sw128(b_addr + kk * 2048, 8192, 1024)
-                                   : smem_desc_sw128(b_addr + kk * 32, 16, 1024);
-          umma_bf16_pair(tmem + b * BNI, ad, bd, kIdesc, (!first || kk != 0) ? 1u : 0u);
-        }
-      };
-      for (int u = pair; ok && u < g.num_units; u += npairs, ++t) {
-        int z, i, j, nsub;
-        orth_unit<BNI, NSUB, kSym>(g, u, z, i, j, nsub);
-        const int b0 = NSUB == 2 ? 0 : static_cast<int>(t & 1u);
-        uint32_t& used = b0 ? used1 : used0;
-        if (!wait_warp(&pc->tempty[b0], (used & 1u) ^ 1u, abort, ctl)) break;
-        ++used;
-        tc_fence_after();
-        int kb = 0;
-        if (NSUB == 2 && nsub == 2) {
-          // The first slot over the stages that are there already, then, once the second slot
-          // is free, its MMAs for them, with the stages' releases.
-          const int pre = min(STAGES, g.k_blocks);
-          for (; kb < pre; ++kb) {
-            const uint32_t q = it + kb;
-            if (!wait_warp(&pc->full[q % STAGES], (q / STAGES) & 1u, abort, ctl)) {
-              ok = false;
-              break;
+          for (int kk = 0; kk < kBK / 16; ++kk) {
+            const uint64_t ad = A_MN ? smem_desc_sw128(a_addr + kk * 2048, 8192, 1024)
+                                     : smem_desc_sw128(a_addr + kk * 32, 16, 1024);
+            const uint64_t bd = B_MN ? smem_desc_sw128(b_addr + kk * 2048, 8192, 1024)
+                                     : smem_desc_sw128(b_addr + kk * 32, 16, 1024);
+            umma_bf16_pair(tmem + b * BNI, ad, bd, kIdesc, (!first || kk != 0) ? 1u : 0u);
+          }
+        };
+        for (int u = pair; u < g.num_units; u += npairs, ++t) {
+          int z, i, j, nsub;
+          orth_unit<BNI, NSUB, OP != kUpdate>(g, u, z, i, j, nsub);
+          const int b0 = NSUB == 2 ? 0 : static_cast<int>(t & 1u);
+          uint32_t& used = b0 ? used1 : used0;
+          ok = wait_warp(&pc->tempty[b0], (used & 1u) ^ 1u, abort, ctl);
+          if (!ok) return;
+          ++used;
+          tc_fence_after();
+          int kb = 0;
+          if (NSUB == 2 && nsub == 2) {
+            // The first slot over the stages that are there already, then, once the second
+            // slot is free, its MMAs for them, with the stages' releases.
+            const int pre = min(STAGES, g.k_blocks);
+            for (; kb < pre; ++kb) {
+              const uint32_t q = it + kb;
+              ok = wait_warp(&pc->full[q % STAGES], (q / STAGES) & 1u, abort, ctl);
+              if (!ok) return;
+              tc_fence_after();
+              if (lane == 0) issue(q % STAGES, 0, 0, kb == 0);
+              __syncwarp();
             }
+            ok = wait_warp(&pc->tempty[1], (used1 & 1u) ^ 1u, abort, ctl);
+            if (!ok) return;
+            ++used1;
             tc_fence_after();
-            if (lane == 0) issue(q % STAGES, 0, 0, kb == 0);
-            __syncwarp();
+            for (int q = 0; q < pre; ++q, ++it) {
+              if (lane == 0) {
+                issue(it % STAGES, 1, 1, q == 0);
+                umma_commit_pair_mc(&pc->empty[it % STAGES], 0x3);
+              }
+              __syncwarp();
+            }
           }
-          if (!ok || !wait_warp(&pc->tempty[1], (used1 & 1u) ^ 1u, abort, ctl)) break;
-          ++used1;
-          tc_fence_after();
-          for (int q = 0; q < pre; ++q, ++it) {
+          for (; kb < g.k_blocks; ++kb, ++it) {
+            const int s = it % STAGES;
+            ok = wait_warp(&pc->full[s], (it / STAGES) & 1u, abort, ctl);
+            if (!ok) return;
+            tc_fence_after();
             if (lane == 0) {
-              issue(it % STAGES, 1, 1, q == 0);
-              umma_commit_pair_mc(&pc->empty[it % STAGES], 0x3);
+              issue(s, 0, b0, kb == 0);
+              if (NSUB == 2 && nsub == 2) issue(s, 1, 1, false);
+              umma_commit_pair_mc(&pc->empty[s], 0x3);
             }
             __syncwarp();
           }
-        }
-        for (; kb < g.k_blocks; ++kb, ++it) {
-          const int s = it % STAGES;
-          if (!wait_warp(&pc->full[s], (it / STAGES) & 1u, abort, ctl)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
           if (lane == 0) {
-            issue(s, 0, b0, kb == 0);
-            if (NSUB == 2 && nsub == 2) issue(s, 1, 1, false);
-            umma_commit_pair_mc(&pc->empty[s], 0x3);
+            umma_commit_pair_mc(&pc->tfull[b0], 0x3);
+            if (NSUB == 2 && nsub == 2) umma_commit_pair_mc(&pc->tfull[1], 0x3);
           }
           __syncwarp();
         }
-        if (!ok) break;
-        if (lane == 0) {
-          umma_commit_pair_mc(&pc->tfull[b0], 0x3);
-          if (NSUB == 2 && nsub == 2) umma_commit_pair_mc(&pc->tfull[1], 0x3);
-        }
-        __syncwarp();
+      };
+      for (int p = 0; ok && p < products; ++p) {
+        if (p % 3 == 0)
+          product(std::integral_constant<int, kGram>{});
+        else if (p % 3 == 1)
+          product(std::integral_constant<int, kSquare>{});
+        else
+          product(std::integral_constant<int, kUpdate>{});
       }
       // Every MMA must be complete (in both CTAs' TMEM) before TMEM is released.
       if (lane == 0) umma_commit_pair_mc(&pc->fin, 0x1);
@@ -623,52 +698,95 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     const uint32_t tempty1 = mapa_shared(smem_u32(&pc->tempty[1]), 0);
     uint32_t t = 0, used0 = 0, used1 = 0;
     bool ok = true;
-    for (int u = pair; ok && u < g.num_units; u += npairs, ++t) {
-      int z, i, j, nsub;
-      orth_unit<BNI, NSUB, kSym>(g, u, z, i, j, nsub);
-      const int64_t row = static_cast<int64_t>(i) * 2 * kBM + rank * kBM + q * 32 + lane;
-      float drow = 0.f;
-      if (OP == kSquare || (OP == kUpdate && !g.tall))
-        if (row < g.rows) drow = g.diag_in[static_cast<int64_t>(z) * g.diag_n + row];
-      for (int h = 0; h < nsub; ++h) {
-        const int b = NSUB == 2 ? h : static_cast<int>(t & 1u);
-        uint32_t& used = b ? used1 : used0;
-        const int64_t col0 = static_cast<int64_t>(j) * C::kTileN + h * BNI + wg * kShare;
-        const bool mirror = kSym && col0 - wg * kShare + BNI <= static_cast<int64_t>(i) * 2 * kBM;
+    auto product = [&](auto opc, auto lastc, int step) {
+      constexpr int OP = decltype(opc)::value;
+      constexpr bool LAST = decltype(lastc)::value;
+      constexpr bool kSym = OP != kUpdate;
+      const OrthGeom& geo = ch.geom[OP];
+      const int cur = step & 1;
+      const OrthView g{OP == kUpdate ? ch.m : ch.k, OP == kUpdate ? ch.n : ch.k,
+                       OP == kUpdate ? ch.ldx : ch.ldk, ch.k,
+                       OP == kUpdate ? ch.hi[cur] : ch.mat[0], ch.lo,
+                       OP == kSquare ? ch.diag[0] : ch.diag[1],
+                       OP == kGram ? ch.diag[0] : ch.diag[1], ch.out, ch.co[step][0],
+                       ch.co[step][1], ch.co[step][2], TALL, ch.out_vec};
+      const CUtensorMap* st0 = OP == kGram ? &maps.mat[0] : OP == kSquare ? &maps.mat[1]
+                               : LAST ? &maps.out : &maps.hi[cur ^ 1];
+      for (int u = pair; ok && u < geo.num_units; u += npairs, ++t) {
+        int z, i, j, nsub;
+        orth_unit<BNI, NSUB, kSym>(geo, u, z, i, j, nsub);
+        const int64_t row = static_cast<int64_t>(i) * 2 * kBM + rank * kBM + q * 32 + lane;
         const int64_t row0 = row - lane;
-        OrthIn<OP> in;
-        in.fetch(g, z, row0, col0, lane);
-        if (!wait_warp(&pc->tfull[b], used & 1u, abort, ctl)) {
-          ok = false;
-          break;
-        }
-        ++used;
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < kChunks; ++c) {
-          float v[32];
-          tmem_ld32(tmem + lane_bits + b * BNI + wg * kShare + c * 32, v);
-          // The staging blocks are free once the stores of the block before have read them.
-          if (lane == 0) bulk_wait_read_all();
-          __syncwarp();
-          in.put(stage, lane);
-          const float dcol = in.dcol;
-          if (c + 1 < kChunks) in.fetch(g, z, row0, col0 + (c + 1) * 32, lane);
-          tmem_ld_wait();
-          if (c == kChunks - 1) {
-            // The slot is drained once this load has completed.
-            tc_fence_before();
-            __syncwarp();
-            // Test hook (fault == 1): withhold the release of the first accumulator.
-            if (lane == 0 && !(ctl.fault == 1 && t == 0))
-              mbar_arrive_cluster(b ? tempty1 : tempty0);
-          } else {
-            __syncwarp();
+        float drow = 0.f;
+        if (OP == kSquare || (OP == kUpdate && !TALL))
+          if (row < g.rows) drow = g.diag_in[static_cast<int64_t>(z) * g.diag_n + row];
+        for (int h = 0; h < nsub; ++h) {
+          const int b = NSUB == 2 ? h : static_cast<int>(t & 1u);
+          uint32_t& used = b ? used1 : used0;
+          const int64_t col0 = static_cast<int64_t>(j) * C::kTileN + h * BNI + wg * kShare;
+          const bool mirror =
+              kSym && col0 - wg * kShare + BNI <= static_cast<int64_t>(i) * 2 * kBM;
+          OrthIn<OP> in;
+          in.fetch(g, z, row0, col0, lane);
+          if (!wait_warp(&pc->tfull[b], used & 1u, abort, ctl)) {
+            ok = false;
+            break;
           }
-          if (col0 + c * 32 < g.cols)
-            orth_epilogue<OP, LAST>(g, &st0, &st1, stage, z, row, col0 + c * 32, mirror, drow,
-                                    dcol, v);
+          ++used;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < kChunks; ++c) {
+            float v[32];
+            tmem_ld32(tmem + lane_bits + b * BNI + wg * kShare + c * 32, v);
+            // The staging blocks are free once the stores of the block before have read them.
+            if (lane == 0) bulk_wait_read_all();
+            __syncwarp();
+            in.put(stage, lane);
+            const float dcol = in.dcol;
+            if (c + 1 < kChunks) in.fetch(g, z, row0, col0 + (c + 1) * 32, lane);
+            tmem_ld_wait();
+            if (c == kChunks - 1) {
+              // The slot is drained once this load has completed.
+              tc_fence_before();
+              __syncwarp();
+              // Test hook (fault == 1): withhold the release of the first accumulator.
+              if (lane == 0 && !(ctl.fault == 1 && t == 0))
+                mbar_arrive_cluster(b ? tempty1 : tempty0);
+            } else {
+              __syncwarp();
+            }
+            if (col0 + c * 32 < g.cols)
+              orth_epilogue<OP, LAST>(g, st0, &maps.lo, stage, z, row, col0 + c * 32, mirror,
+                                      drow, dcol, v);
+          }
         }
+      }
+    };
+    for (int p = 0; ok && p < products; ++p) {
+      if (p > 0) ok = wait_warp(&pc->met, (p - 1) & 1u, abort, ctl);
+      if (!ok) break;
+      const int step = p / 3;
+      if (p % 3 == 0)
+        product(std::integral_constant<int, kGram>{}, std::false_type{}, step);
+      else if (p % 3 == 1)
+        product(std::integral_constant<int, kSquare>{}, std::false_type{}, step);
+      else if (step + 1 < ch.steps)
+        product(std::integral_constant<int, kUpdate>{}, std::false_type{}, step);
+      else
+        product(std::integral_constant<int, kUpdate>{}, std::true_type{}, step);
+      if (!ok) break;
+      // This warp's part of the product is in memory: bulk stores complete, plain stores fenced.
+      // The last of the CTA's warps reports (nobody blocks: after a wait that ran out, some
+      // warps may never come here).
+      if (lane == 0) {
+        bulk_wait_all();
+        fence_proxy_async_global();
+      }
+      __threadfence();
+      __syncwarp();
+      if (lane == 0 && atomicAdd(&pc->done, 1) == 4 * kOrthWG * (p + 1) - 1) {
+        __threadfence();
+        red_release_add_s32(ch.counter, 1);
       }
     }
     if (lane == 0) bulk_wait_all();
@@ -682,12 +800,11 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
-template <int BNI, int NSUB, bool A_MN, bool B_MN, int OP, bool LAST>
-cudaError_t launch_orth(const CUtensorMap& a, const CUtensorMap& b, const OrthMaps& st,
-                        const OrthGemm& g,
-                        const DevCtl& c, cudaStream_t s) {
+template <int BNI, int NSUB, bool TALL>
+cudaError_t launch_chain(const OrthChain& ch, const OrthMaps& maps, const DevCtl& c,
+                         cudaStream_t s) {
   using C = OrthCfg<BNI, NSUB>;
-  auto kern = orth_gemm<BNI, NSUB, A_MN, B_MN, OP, LAST>;
+  auto kern = orth_chain<BNI, NSUB, TALL>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -698,9 +815,9 @@ cudaError_t launch_orth(const CUtensorMap& a, const CUtensorMap& b, const OrthMa
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  // Set-up overlaps the end of the launch before it (the kernel waits for its results).
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  // The CTAs wait for one another: all of them resident, or none.
+  attr[1].id = cudaLaunchAttributeCooperative;
+  attr[1].val.cooperative = 1;
   cfg.blockDim = dim3(kOrthThreads, 1, 1);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
@@ -718,22 +835,10 @@ cudaError_t launch_orth(const CUtensorMap& a, const CUtensorMap& b, const OrthMa
     max_clusters[dev] = n > 0 ? n : 1;
   }
   cfg.numAttrs = 2;
-  cfg.gridDim = dim3(2 * std::max(1, std::min(g.num_units, max_clusters[dev])), 1, 1);
-  return cudaLaunchKernelEx(&cfg, kern, a, b, *st.out0, *st.out1, g, c);
-}
-
-template <int BNI, int NSUB>
-cudaError_t launch_op(int op, bool tall, bool last, const CUtensorMap& a, const CUtensorMap& b,
-                      const OrthMaps& st, const OrthGemm& g, const DevCtl& c, cudaStream_t s) {
-  if (op == kGram)
-    return tall ? launch_orth<BNI, NSUB, true, true, kGram, false>(a, b, st, g, c, s)
-                : launch_orth<BNI, NSUB, false, false, kGram, false>(a, b, st, g, c, s);
-  if (op == kSquare) return launch_orth<BNI, NSUB, false, false, kSquare, false>(a, b, st, g, c, s);
-  if (tall)
-    return last ? launch_orth<BNI, NSUB, false, false, kUpdate, true>(a, b, st, g, c, s)
-                : launch_orth<BNI, NSUB, false, false, kUpdate, false>(a, b, st, g, c, s);
-  return last ? launch_orth<BNI, NSUB, false, true, kUpdate, true>(a, b, st, g, c, s)
-              : launch_orth<BNI, NSUB, false, true, kUpdate, false>(a, b, st, g, c, s);
+  int units = 1;
+  for (const OrthGeom& g : ch.geom) units = std::max(units, g.num_units);
+  cfg.gridDim = dim3(2 * std::min(units, max_clusters[dev]), 1, 1);
+  return cudaLaunchKernelEx(&cfg, kern, ch, maps, c);
 }
 
 }  // namespace
@@ -765,12 +870,16 @@ cudaError_t launch_orth_prep(int dtype, const OrthPrep& p, int64_t batch, cudaSt
   return run(float{});
 }
 
-cudaError_t launch_orth_gemm(int op, int bn, bool tall, bool last, const CUtensorMap& a,
-                             const CUtensorMap& b, const OrthMaps& st, const OrthGemm& g,
-                             const DevCtl& c, cudaStream_t s) {
-  if (bn == 512) return launch_op<256, 2>(op, tall, last, a, b, st, g, c, s);
-  return bn == 128 ? launch_op<128, 1>(op, tall, last, a, b, st, g, c, s)
-                   : launch_op<256, 1>(op, tall, last, a, b, st, g, c, s);
+cudaError_t launch_orth_chain(int bn, bool tall, const OrthChain& ch, const OrthMaps& maps,
+                              const DevCtl& c, cudaStream_t s) {
+  if (bn == 512)
+    return tall ? launch_chain<256, 2, true>(ch, maps, c, s)
+                : launch_chain<256, 2, false>(ch, maps, c, s);
+  if (bn == 256)
+    return tall ? launch_chain<256, 1, true>(ch, maps, c, s)
+                : launch_chain<256, 1, false>(ch, maps, c, s);
+  return tall ? launch_chain<128, 1, true>(ch, maps, c, s)
+              : launch_chain<128, 1, false>(ch, maps, c, s);
 }
 
 }  // namespace slm

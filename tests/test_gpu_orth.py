@@ -190,3 +190,37 @@ def test_same_bits_each_time(shape):
     want = orthogonalize(g)
     for _ in range(5):
         assert torch.equal(orthogonalize(g), want)
+
+
+@pytest.mark.parametrize("shape", [(300, 200), (600, 1300)])
+def test_wait_runs_out_reports_timeout_and_the_next_call_is_right(shape):
+    from lm_head_loss_streaming_b200 import _lib
+    g = spectrum(*shape, "noise", 11).to(BF)
+    ws = torch.empty(orthogonalize_workspace_bytes(1, *shape), dtype=torch.uint8, device="cuda")
+    want = orthogonalize(g)
+    assert _lib.slm_debug_set(1, 100_000_000) == 0   # ~0.05-0.1 s per wait
+    try:
+        orthogonalize(g, workspace=ws)
+        st = _lib.slm_device_status(ws.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    finally:
+        assert _lib.slm_debug_set(0, 0) == 0
+    assert st == 7, _lib.status_string(st)   # SLM_ERR_TIMEOUT
+    assert torch.equal(orthogonalize(g, workspace=ws), want)
+    st = _lib.slm_device_status(ws.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+
+
+def test_many_calls_on_several_streams():
+    """Calls whose blocks wait for one another, at once on four streams."""
+    gs = [spectrum(400 + 64 * i, 900 - 50 * i, "noise", i).to(F32) for i in range(4)]
+    want = [orthogonalize(g) for g in gs]
+    streams = [torch.cuda.Stream() for _ in gs]
+    torch.cuda.synchronize()
+    got = [[] for _ in gs]
+    for _ in range(6):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(orthogonalize(gs[i]))
+    torch.cuda.synchronize()
+    for i in range(4):
+        assert all(torch.equal(g, want[i]) for g in got[i])
