@@ -439,7 +439,7 @@ SLM_API int slm_block_norm_bwd(int dtype, const void* x, int64_t ldx, const void
  * zeros gives zeros; one with a NaN or an infinity gives NaN throughout, and no other matrix of
  * the stack is touched by it.  Matrices with ||u||_F far below eps lose relative precision
  * (their X is below 2^-28).  batch, m or n = 0: nothing is done.
- * Returns SLM_ERR_SHAPE for bad sizes (m, n >= 2^31; batch > 65535; more than 2^31 - 1 tiles),
+ * Returns SLM_ERR_SHAPE for bad sizes (m, n >= 2^30; batch > 65535; 2^30 tiles of 256 x 128 or more),
  * strides, steps, beta outside [0, 1] or eps <= 0; the rest as everywhere. */
 SLM_API size_t slm_orthogonalize_workspace_bytes(int64_t batch, int64_t m, int64_t n);
 SLM_API int slm_orthogonalize(int dtype, const void* grad, int64_t ld, int64_t batch_stride,

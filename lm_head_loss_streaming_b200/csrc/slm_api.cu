@@ -480,7 +480,7 @@ OrthLayout orth_layout(int64_t batch, int64_t m, int64_t n) {
 }
 
 bool orth_sizes_ok(int64_t batch, int64_t m, int64_t n) {
-  const int64_t big = int64_t(1) << 31;
+  const int64_t big = int64_t(1) << 30;
   if (batch < 0 || m < 0 || n < 0 || batch > 65535 || m >= big || n >= big) return false;
   return ceil_div(m, 256) * ceil_div(n, 128) * batch < big;
 }
@@ -507,11 +507,9 @@ bool orth_coefficients_ok(const float* co, int steps) {
 }
 
 // 3-D fp16 tensor map over a stack of row-major [outer, inner] matrices with `ld` elements per
-// row, outer * ld per matrix; box {box_inner, box_outer, 1}, 128-byte swizzle (64-byte for the
-// store maps' boxes of 32 elements per row).
+// row, outer * ld per matrix; box {box_inner, box_outer, 1}, 128-byte swizzle.
 bool make_map_stack(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t ld,
-                    int64_t stack, int box_inner, int box_outer,
-                    CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_FLOAT16) {
+                    int64_t stack, int box_inner, int box_outer) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer),
@@ -520,19 +518,19 @@ bool make_map_stack(CUtensorMap* m, const void* base, int64_t inner, int64_t out
                            static_cast<cuuint64_t>(outer) * static_cast<cuuint64_t>(ld) * 2};
   cuuint32_t box[3] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_outer), 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, type, 3, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE,
-            box_inner == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Tile grid of one product (rows x cols outputs over k, tiles of 256 x bn) and its estimated
-// seconds.  Per 64-wide K block a tile takes its MMAs (27 TFLOP/s per pair) or its operands' way
-// from L2 (9.3 TB/s shared by the pairs that are busy), whichever is longer; both rates as
-// measured on the products of 4096 x 4096 matrices.  A round of tiles also costs its epilogue,
-// about 0.5 us per 128 columns.
-double orth_tiles(OrthGeom* g, int bn, int64_t rows, int64_t cols, int64_t k, int64_t batch,
-                  bool sym) {
+// seconds, the CTAs' meeting after it included.  Per 64-wide K block a tile takes its MMAs
+// (27 TFLOP/s per pair; two thirds of that at 128 columns) or its operands' way from L2 (9.3 TB/s
+// shared by the pairs that are busy), whichever is longer; the rates as measured on the products
+// of 4096 x 4096 matrices.  A round of tiles also costs its epilogue, about 0.5 us per 128
+// columns.  `own`: one pair works all tiles of a matrix.
+double orth_tiles(OrthGeom* g, int bn, bool own, int64_t rows, int64_t cols, int64_t k,
+                  int64_t batch, bool sym) {
   const int64_t pairs = std::max(1, sm_count() / 2);
   const int64_t nm = ceil_div(rows, kPairM), nn = ceil_div(cols, bn);
   // Symmetric: the tiles that reach below the diagonal.
@@ -545,32 +543,39 @@ double orth_tiles(OrthGeom* g, int bn, int64_t rows, int64_t cols, int64_t k, in
   g->num_units = static_cast<int>(units);
   g->k_blocks = static_cast<int>(ceil_div(k, kBK));
   auto round = [&](int64_t busy) {
-    const double mma = 2.0 * kPairM * bn * kBK / 27e12;
+    const double mma = 2.0 * kPairM * bn * kBK / (bn == 128 ? 18e12 : 27e12);
     const double l2 = (kPairM + bn) * kBK * 2.0 * static_cast<double>(busy) / 9.3e12;
     return g->k_blocks * std::max(mma, l2) + 0.5e-6 * bn / 128;
   };
+  if (own) {
+    const int64_t busy = std::min(batch, pairs);
+    return static_cast<double>(ceil_div(batch, pairs)) * (per * round(busy) + 2e-6);
+  }
   return static_cast<double>(units / pairs) * round(pairs) +
-         (units % pairs != 0 ? round(units % pairs) : 0.0);
+         (units % pairs != 0 ? round(units % pairs) : 0.0) + 4e-6;
 }
 
-// The tile grids of a step's three products and their tiles' width: of 512, 256 and 128 columns
-// the one whose rounds are estimated to take least.  Wide tiles read less from L2 per flop,
-// narrow ones leave fewer pairs idle: the update of a 4096 x 4096 matrix took 178 us at 128
-// columns and 125 at 512, the products of a 2048 x 2048 one run on half of the pairs at 512.
+// The tile grids of a step's three products, their tiles' width, and whether a pair works each
+// matrix alone: of the six ways the one that is estimated to take least.  Wide tiles read less
+// from L2 per flop, narrow ones leave fewer pairs idle: the update of a 4096 x 4096 matrix took
+// 178 us at 128 columns and 125 at 512, the products of a 2048 x 2048 one run on half of the
+// pairs at 512.
 int orth_plan(OrthChain* ch, int64_t m, int64_t n, int64_t batch) {
   const int64_t k = std::min(m, n), l = std::max(m, n);
   int best = 0;
   double best_cost = 0;
-  for (int bn : {512, 256, 128}) {
-    OrthGeom g[3];
-    const double cost = orth_tiles(&g[0], bn, k, k, l, batch, true) +
-                        orth_tiles(&g[1], bn, k, k, k, batch, true) +
-                        orth_tiles(&g[2], bn, m, n, k, batch, false);
-    if (best != 0 && cost >= best_cost) continue;
-    best = bn;
-    best_cost = cost;
-    std::copy(g, g + 3, ch->geom);
-  }
+  for (int own = 0; own < 2; ++own)
+    for (int bn : {512, 256, 128}) {
+      OrthGeom g[3];
+      const double cost = orth_tiles(&g[0], bn, own, k, k, l, batch, true) +
+                          orth_tiles(&g[1], bn, own, k, k, k, batch, true) +
+                          orth_tiles(&g[2], bn, own, m, n, k, batch, false);
+      if (best != 0 && cost >= best_cost) continue;
+      best = bn;
+      best_cost = cost;
+      ch->own = own;
+      std::copy(g, g + 3, ch->geom);
+    }
   return best;
 }
 
@@ -1266,12 +1271,13 @@ int slm_orthogonalize(int dtype, const void* grad, int64_t ld, int64_t batch_str
   OrthChain ch{};
   const int bn = orth_plan(&ch, m, n, batch);
   ch.steps = steps;
+  ch.batch = static_cast<int>(batch);
   ch.out_vec = n % 8 == 0 && !misaligned(out, 16);
-  ch.m = m;
-  ch.n = n;
-  ch.k = k;
-  ch.ldx = L.ldx;
-  ch.ldk = L.ldk;
+  ch.m = static_cast<int>(m);
+  ch.n = static_cast<int>(n);
+  ch.k = static_cast<int>(k);
+  ch.ldx = static_cast<int>(L.ldx);
+  ch.ldk = static_cast<int>(L.ldk);
   ch.lo = lo;
   ch.out = static_cast<__nv_bfloat16*>(out);
   ch.counter = status + 1;
@@ -1291,24 +1297,17 @@ int slm_orthogonalize(int dtype, const void* grad, int64_t ld, int64_t batch_str
     if (!make_map_stack(&maps.a[0][i], hi[i], n, m, L.ldx, batch, 64, tall ? 64 : kBM) ||
         !make_map_stack(&maps.b[0][i], hi[i], n, m, L.ldx, batch, 64, tall ? 64 : slice) ||
         !make_map_stack(tall ? &maps.a[2][i] : &maps.b[2][i], hi[i], n, m, L.ldx, batch, 64,
-                        tall ? kBM : 64) ||
-        !make_map_stack(&maps.hi[i], hi[i], n, m, L.ldx, batch, 32, 32) ||
-        !make_map_stack(&maps.mat[i], mat[i], k, k, L.ldk, batch, 32, 32))
+                        tall ? kBM : 64))
       return SLM_ERR_CUDA;
   }
   if (!make_map_stack(&maps.a[1][0], mat[0], k, k, L.ldk, batch, 64, kBM) ||
       !make_map_stack(&maps.b[1][0], mat[0], k, k, L.ldk, batch, 64, slice) ||
       !make_map_stack(tall ? &maps.b[2][0] : &maps.a[2][0], mat[1], k, k, L.ldk, batch, 64,
-                      tall ? slice : kBM) ||
-      !make_map_stack(&maps.lo, lo, n, m, L.ldx, batch, 32, 32))
+                      tall ? slice : kBM))
     return SLM_ERR_CUDA;
   maps.a[1][1] = maps.a[1][0];
   maps.b[1][1] = maps.b[1][0];
   (tall ? maps.b : maps.a)[2][1] = (tall ? maps.b : maps.a)[2][0];
-  maps.out = maps.lo;  // unused unless the result can be stored in bulk
-  if (ch.out_vec &&
-      !make_map_stack(&maps.out, out, n, m, n, batch, 32, 32, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16))
-    return SLM_ERR_CUDA;
 
   const OrthPrep prep{grad, m, n, ld, batch_stride, L.ldx, momentum, static_cast<float>(beta),
                       static_cast<float>(1.0 - beta), eps, nesterov,

@@ -323,8 +323,10 @@ struct OrthGeom {
 };
 struct OrthChain {
   OrthGeom geom[3];
-  int steps, out_vec;       // out_vec: the result's rows start on 16-byte boundaries
-  int64_t m, n, k, ldx, ldk;
+  int steps, batch;
+  int own;      // each matrix is worked by one CTA pair alone
+  int out_vec;  // the result's rows start on 16-byte boundaries
+  int m, n, k, ldx, ldk;
   __half *hi[2], *lo, *mat[2];  // mat: R, R_B
   float* diag[2];               // D, D_B: [batch][k]
   __nv_bfloat16* out;
@@ -332,19 +334,17 @@ struct OrthChain {
   float co[kMaxOrthSteps][3];
 };
 struct OrthMaps {
-  CUtensorMap a[3][2], b[3][2];         // operands of the products
-  CUtensorMap hi[2], lo, mat[2], out;   // stores: boxes of 32 x 32, 64-byte swizzle
+  CUtensorMap a[3][2], b[3][2];  // operands of the products
 };
 // What one product's epilogue sees of it.
 struct OrthView {
-  int64_t rows, cols, ld, diag_n;
+  int rows, cols, ld, diag_n;
   const __half* in;  // kSquare: R; kUpdate: hi
-  const __half* lo;
+  __half* lo;
   const float* diag_in;
   float* diag_out;
-  __nv_bfloat16* out;
+  void* out;  // R, R_B, hi or the result
   float a, b, c;
-  bool tall;
   int out_vec;
 };
 cudaError_t launch_orth_prep(int dtype, const OrthPrep& p, int64_t batch, cudaStream_t s);

@@ -219,6 +219,26 @@ __device__ __forceinline__ void red_release_add_s32(int* p, int v) {
 __device__ __forceinline__ void fence_proxy_async_global() {
   asm volatile("fence.proxy.async.global;" ::: "memory");
 }
+// Waits (boundedly) until both CTAs of the pair have arrived; what they wrote is then visible to
+// this warp's loads and bulk copies.
+__device__ __forceinline__ bool wait_both(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          const DevCtl& ctl) {
+  const uint32_t a = smem_u32(bar);
+  bool done = mbar_try_wait_cluster(a, parity);
+  if (!done) {
+    const long long t0 = clock64();
+    while (!(done = mbar_try_wait_cluster(a, parity))) {
+      if (*abort) break;
+      if (clock64() - t0 > ctl.timeout_cycles) {
+        *abort = 1;
+        atomicOr(ctl.status, kFlagTimeout);
+        break;
+      }
+    }
+  }
+  fence_proxy_async_global();
+  return __all_sync(0xffffffffu, done);
+}
 // Waits (boundedly; lane 0 polls) until `target` arrivals are counted; what the arriving CTAs
 // wrote is then visible to this thread's loads and bulk copies.
 __device__ __forceinline__ bool wait_met(const int* counter, int target, volatile int* abort,
@@ -243,8 +263,9 @@ __device__ __forceinline__ bool wait_met(const int* counter, int target, volatil
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
-// Staging of an epilogue warp: two blocks of 32 rows x 32 fp16 columns, 64 bytes per row, in
-// the 64-byte swizzle of the store maps (16-byte piece k of row r at k ^ (r / 2 % 4)).
+// Staging of an epilogue warp: two blocks of 32 rows x 32 fp16 columns, 64 bytes per row, with
+// 16-byte piece k of row r at k ^ (r / 2 % 4), so that neither a lane per row nor four lanes
+// per row conflict.
 constexpr int kOrthStage = 4096;
 __device__ __forceinline__ int stage_piece(int row, int k) {
   return row * 4 + (k ^ ((row >> 1) & 3));
@@ -252,9 +273,10 @@ __device__ __forceinline__ int stage_piece(int row, int k) {
 
 template <int STAGES>
 struct OrthCtl {
-  uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], fin, met;
+  uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], fin, met, done, both;
   uint32_t tmem_base;
-  int abort, done;
+  int abort;
+  alignas(16) float diag[4 * kOrthWG][32];  // the epilogue warps' entries of a block's columns
 };
 
 template <int BNI, int NSUB>
@@ -315,159 +337,160 @@ __device__ __forceinline__ uint32_t pack_bf162(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 // What the epilogue reads for a warp's block of 32 rows x 32 columns: fetched a block ahead, so
 // that its latency passes behind the MMAs or the block before.  Four lanes share a row, so that
 // every load covers whole 64-byte pieces of rows.
-template <int OP>
+template <int OP, bool TALL>
 struct OrthIn {
   static constexpr int kSets = OP == kGram ? 0 : OP == kSquare ? 1 : 2;
+  static constexpr bool kCols = OP == kSquare || (OP == kUpdate && TALL);
   uint4 w[kSets == 0 ? 1 : kSets][4];  // kSquare: R; kUpdate: hi, lo
   float dcol;                          // lane l: the diagonal's entry of column col + l
-  __device__ __forceinline__ void fetch(const OrthView& g, int z, int64_t row0, int64_t col,
-                                        int lane) {
+  __device__ __forceinline__ void fetch(const OrthView& g, int z, int row0, int col, int lane) {
     if (OP == kGram || col >= g.cols) return;
-    if (OP == kSquare || g.tall)
+    if (kCols)
       dcol = col + lane < g.cols ? g.diag_in[static_cast<int64_t>(z) * g.diag_n + col + lane] : 0.f;
-    const int64_t c = col + (lane & 3) * 8;
+    const int c = col + (lane & 3) * 8, row = row0 + (lane >> 2);
+    const int64_t at = (static_cast<int64_t>(z) * g.rows + row) * g.ld + c;
+    const int64_t step = static_cast<int64_t>(g.ld) * 8;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int64_t row = row0 + q * 8 + (lane >> 2);
-      const int64_t at = (static_cast<int64_t>(z) * g.rows + row) * g.ld + c;
-      const bool in = row < g.rows && c < g.cols;  // rows are padded to whole pieces
+      const bool in = row + q * 8 < g.rows && c < g.cols;  // rows are padded to whole pieces
       const uint4 none = make_uint4(0, 0, 0, 0);
-      w[0][q] = !in ? none
-                    : *reinterpret_cast<const uint4*>(g.in + at);
-      if (OP == kUpdate) w[kSets - 1][q] = !in ? none : *reinterpret_cast<const uint4*>(g.lo + at);
+      w[0][q] = !in ? none : *reinterpret_cast<const uint4*>(g.in + at + q * step);
+      if (OP == kUpdate)
+        w[kSets - 1][q] = !in ? none : *reinterpret_cast<const uint4*>(g.lo + at + q * step);
     }
   }
   // Into the warp's staging blocks.
-  __device__ __forceinline__ void put(uint4* stage, int lane) const {
+  __device__ __forceinline__ void put(uint4* stage, float* dstage, int lane) const {
 #pragma unroll
     for (int e = 0; e < kSets; ++e)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         stage[e * 128 + stage_piece(q * 8 + (lane >> 2), lane & 3)] = w[e][q];
+    if (kCols) dstage[lane] = dcol;
   }
 };
 
+// A staged block to rows [row0, row0 + 32), columns [col, col + 32) of the matrix at `dst`, whose
+// rows are padded to whole pieces: four lanes per row.  (Bulk stores from the staging measured
+// slower: each block waited about 0.7 us for the one before to be read.)
+__device__ __forceinline__ void unstage(const uint4* block, void* dst, int64_t ld, int row0,
+                                        int col, int rows, int cols, int lane) {
+  const int c = col + (lane & 3) * 8, row = row0 + (lane >> 2);
+  uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + row * ld + c);
+  const int64_t step = ld;  // 8 rows of ld / 8 pieces
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint4 w = block[stage_piece(q * 8 + (lane >> 2), lane & 3)];
+    if (row + q * 8 < rows && c < cols) out[q * step] = w;
+  }
+}
+
 // One warp's block: this lane's row `row`, columns [col, col + 32) of matrix z.  The block's
 // inputs lie in the staging blocks; its outputs take their place, each lane its own row, and go
-// out by bulk stores, which leave out rows and columns outside the matrix.
-template <int OP, bool LAST>
-__device__ __forceinline__ void orth_epilogue(const OrthView& g, const CUtensorMap* st0,
-                                              const CUtensorMap* st1, uint4* stage, int z,
-                                              int64_t row, int64_t col, bool mirror, float drow,
-                                              float dcol, float (&v)[32]) {
+// out from there.
+template <int OP, bool LAST, bool TALL>
+__device__ __forceinline__ void orth_epilogue(const OrthView& g, uint4* stage,
+                                              const float* dstage, int z, int row, int col,
+                                              bool mirror, float drow, float (&v)[32]) {
+  constexpr int kSets = OrthIn<OP, TALL>::kSets;
   const int lane = threadIdx.x & 31;
-  uint32_t in[2][16];
+  const float4* d4 = reinterpret_cast<const float4*>(dstage);
+  uint32_t lo_out[OP == kUpdate ? 16 : 1];
 #pragma unroll
-  for (int e = 0; e < OrthIn<OP>::kSets; ++e)
+  for (int q = 0; q < 4; ++q) {  // 8 columns at a time
+    uint32_t in[2][4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int e = 0; e < kSets; ++e) {
       const uint4 w = stage[e * 128 + stage_piece(lane, q)];
-      in[e][4 * q] = w.x;
-      in[e][4 * q + 1] = w.y;
-      in[e][4 * q + 2] = w.z;
-      in[e][4 * q + 3] = w.w;
+      in[e][0] = w.x;
+      in[e][1] = w.y;
+      in[e][2] = w.z;
+      in[e][3] = w.w;
     }
-  auto put_row = [&](int e, const uint32_t(&w)[16]) {
+    uint32_t out[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      stage[e * 128 + stage_piece(lane, q)] =
-          make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-  };
-  uint32_t out[16];
-  if (OP == kGram || OP == kSquare) {
-    const int e = static_cast<int>(row - col);  // the diagonal's column of the block, if in it
-    float d = 0.f;
-    if (OP == kGram) {
-#pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        if (c == e) d = v[c] * (1.f / (kScaleX * kScaleX));
-        v[c] = c == e ? 0.f : v[c] * (kScaleA / (kScaleX * kScaleX));
+    for (int h = 0; h < 4; ++h) {  // a pair of columns
+      const float2 x = make_float2(v[8 * q + 2 * h], v[8 * q + 2 * h + 1]);
+      float2 d = both(drow);
+      if (OrthIn<OP, TALL>::kCols) {
+        const float4 f = d4[2 * q + h / 2];
+        d = h & 1 ? make_float2(f.z, f.w) : make_float2(f.x, f.y);
       }
-    } else {
-#pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const float dj = __shfl_sync(0xffffffffu, dcol, c);
-        const float2 r2 = unpack_half2(in[0][c / 2]);
-        const float rr = v[c] * (1.f / (kScaleA * kScaleA));
-        const float a = (c & 1 ? r2.y : r2.x) * (1.f / kScaleA);
-        if (c == e) d = fmaf(g.c, fmaf(drow, drow, rr), g.b * drow);
-        v[c] = c == e ? 0.f : kScaleB * fmaf(g.c, fmaf(drow + dj, a, rr), g.b * a);
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < 16; ++c) out[c] = pack_half2(v[2 * c], v[2 * c + 1]);
-    if (row < g.rows && e >= 0 && e < 32)
-      g.diag_out[static_cast<int64_t>(z) * g.diag_n + row] = d;
-    put_row(0, out);
-    if (mirror) {
-      // The block's transpose: two lanes trade halves, so that each word holds two rows.
-      uint32_t* t = reinterpret_cast<uint32_t*>(stage + 128);
-      const bool odd = lane & 1;
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const uint32_t q = __shfl_xor_sync(0xffffffffu, out[c], 1);
-        const int cc = 2 * c + odd, word = lane >> 1;
-        t[stage_piece(cc, word >> 2) * 4 + (word & 3)] =
-            odd ? __byte_perm(q, out[c], 0x7632) : __byte_perm(out[c], q, 0x5410);
+      if (OP == kGram) {
+        const float2 r = __fmul2_rn(x, both(kScaleA / (kScaleX * kScaleX)));
+        out[h] = pack_half2(r.x, r.y);
+      } else if (OP == kSquare) {
+        // scaled c (R R + (D_i + D_j) R) + b R
+        const float2 t = __ffma2_rn(both(g.c * (kScaleB / kScaleA)), d,
+                                    both(fmaf(g.c, drow, g.b) * (kScaleB / kScaleA)));
+        const float2 r = __ffma2_rn(unpack_half2(in[0][h]), t,
+                                    __fmul2_rn(x, both(g.c * (kScaleB / (kScaleA * kScaleA)))));
+        out[h] = pack_half2(r.x, r.y);
+      } else {
+        const float2 r =
+            __ffma2_rn(x, both(1.f / kScaleB),
+                       __ffma2_rn(unpack_half2(in[0][h]), __fadd2_rn(d, both(g.a)),
+                                  __fmul2_rn(unpack_half2(in[kSets - 1][h]), both(g.a))));
+        if (LAST) {
+          out[h] = pack_bf162(r.x * (1.f / kScaleX), r.y * (1.f / kScaleX));
+        } else {
+          out[h] = pack_half2(r.x, r.y);
+          const float2 hi = unpack_half2(out[h]);
+          lo_out[OP == kUpdate ? 4 * q + h : 0] = pack_half2(r.x - hi.x, r.y - hi.y);
+        }
       }
     }
-  } else {
+    stage[stage_piece(lane, q)] = make_uint4(out[0], out[1], out[2], out[3]);
+    if (OP == kUpdate && !LAST)
+      stage[128 + stage_piece(lane, q)] = make_uint4(lo_out[4 * q], lo_out[4 * q + 1],
+                                                     lo_out[4 * q + 2], lo_out[4 * q + 3]);
+    if (OP != kUpdate && mirror) {
+      // The transpose: column c of the block as row c, a lane per element.
+      uint16_t* t = reinterpret_cast<uint16_t*>(stage + 128);
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-      const float2 hi = unpack_half2(in[0][c / 2]), lo = unpack_half2(in[1][c / 2]);
-      float d0 = drow, d1 = drow;
-      if (g.tall) {
-        d0 = __shfl_sync(0xffffffffu, dcol, c);
-        d1 = __shfl_sync(0xffffffffu, dcol, c + 1);
-      }
-      v[c] = fmaf(v[c], 1.f / kScaleB, fmaf(d0, hi.x, g.a * (hi.x + lo.x)));
-      v[c + 1] = fmaf(v[c + 1], 1.f / kScaleB, fmaf(d1, hi.y, g.a * (hi.y + lo.y)));
-    }
-    if (LAST) {
-#pragma unroll
-      for (int c = 0; c < 16; ++c)
-        out[c] = pack_bf162(v[2 * c] * (1.f / kScaleX), v[2 * c + 1] * (1.f / kScaleX));
-      put_row(0, out);
-      if (!g.out_vec) {
-        // Rows of the result that do not start on 16-byte boundaries: element stores, a row
-        // per instruction.
-        __syncwarp();
-        const __nv_bfloat16* el = reinterpret_cast<const __nv_bfloat16*>(stage);
-        const int64_t r0 = row - lane;
-        __nv_bfloat16* dst = g.out + (static_cast<int64_t>(z) * g.rows + r0) * g.cols + col + lane;
-        const int rows = static_cast<int>(min(static_cast<int64_t>(32), g.rows - r0));
-        if (col + lane < g.cols)
-          for (int r = 0; r < rows; ++r)
-            dst[r * g.cols] = el[stage_piece(r, lane >> 3) * 8 + (lane & 7)];
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        out[c] = pack_half2(v[2 * c], v[2 * c + 1]);
-        const float2 hi = unpack_half2(out[c]);
-        v[2 * c] -= hi.x;
-        v[2 * c + 1] -= hi.y;
-      }
-      put_row(0, out);
-#pragma unroll
-      for (int c = 0; c < 16; ++c) out[c] = pack_half2(v[2 * c], v[2 * c + 1]);
-      put_row(1, out);
+      for (int c = 0; c < 8; ++c)
+        t[stage_piece(8 * q + c, lane >> 3) * 8 + (lane & 7)] =
+            static_cast<uint16_t>(c & 1 ? out[c / 2] >> 16 : out[c / 2]);
     }
   }
-  fence_proxy_async_smem();
+  const int row0 = row - lane;
+  if (OP != kUpdate && row0 == col) {
+    // The block on the diagonal: this lane's diagonal element goes to the fp32 diagonal, a zero
+    // takes its place.  (Selected, not branched to: a branch per lane took 3 us.)
+    float x = 0.f;
+#pragma unroll
+    for (int c = 0; c < 32; ++c) x = c == lane ? v[c] : x;
+    if (row < g.rows)
+      g.diag_out[static_cast<int64_t>(z) * g.diag_n + row] =
+          OP == kGram ? x * (1.f / (kScaleX * kScaleX))
+                      : fmaf(g.c, fmaf(drow, drow, x * (1.f / (kScaleA * kScaleA))), g.b * drow);
+    reinterpret_cast<uint16_t*>(stage)[stage_piece(lane, lane >> 3) * 8 + (lane & 7)] = 0;
+  }
   __syncwarp();
-  if (lane == 0 && !(LAST && !g.out_vec)) {
-    const int r0 = static_cast<int>(row), c0 = static_cast<int>(col);
-    if (r0 < g.rows) {
-      tma_store_3d(st0, stage, c0, r0, z);
-      if (OP == kUpdate && !LAST) tma_store_3d(st1, stage + 128, c0, r0, z);
-      if (OP != kUpdate && mirror) tma_store_3d(st0, stage + 128, r0, c0, z);
-      bulk_commit();
-    }
+  const int64_t base = static_cast<int64_t>(z) * g.rows * (LAST ? g.cols : g.ld);
+  if (LAST && !g.out_vec) {
+    // Rows of the result that do not start on 16-byte boundaries: element stores, a row per
+    // instruction.
+    const uint16_t* el = reinterpret_cast<const uint16_t*>(stage);
+    uint16_t* dst = static_cast<uint16_t*>(g.out) + base + static_cast<int64_t>(row0) * g.cols + col + lane;
+    const int rows = min(32, g.rows - row0);
+    if (col + lane < g.cols)
+      for (int r = 0; r < rows; ++r)
+        dst[static_cast<int64_t>(r) * g.cols] = el[stage_piece(r, lane >> 3) * 8 + (lane & 7)];
+  } else {
+    unstage(stage, static_cast<uint16_t*>(g.out) + base, LAST ? g.cols : g.ld, row0, col, g.rows,
+            g.cols, lane);
   }
+  if (OP == kUpdate && !LAST)
+    unstage(stage + 128, g.lo + base, g.ld, row0, col, g.rows, g.cols, lane);
+  if (OP != kUpdate && mirror)
+    unstage(stage + 128, static_cast<uint16_t*>(g.out) + base, g.ld, col, row0, g.cols, g.rows, lane);
+  __syncwarp();  // the staging is free again
 }
 
 template <int BNI, int NSUB, bool TALL>
@@ -499,8 +522,9 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     }
     mbar_init(&pc->fin, 1);
     mbar_init(&pc->met, 1);
+    mbar_init(&pc->done, 4 * kOrthWG);
+    mbar_init(&pc->both, 2);
     pc->abort = 0;
-    pc->done = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -512,20 +536,32 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   tc_fence_after();
   const uint32_t tmem = pc->tmem_base;
   volatile int* abort = &pc->abort;
+  // A matrix's products need one another's results.  Where the pair works a matrix alone
+  // (ch.own), its two CTAs meet; otherwise every CTA of the launch does, all matrices at once.
   const int products = 3 * ch.steps;
+  const int sets = ch.own ? (ch.batch - pair + npairs - 1) / npairs : 1;
+  // Units u0, u0 + stride, .. below u1 of product `op` in set q.
+  auto units = [&](int op, int q, int& u0, int& u1, int& stride) {
+    const OrthGeom& g = ch.geom[op];
+    u0 = ch.own ? (pair + q * npairs) * g.units_per : pair;
+    u1 = ch.own ? u0 + g.units_per : g.num_units;
+    stride = ch.own ? 1 : npairs;
+  };
 
   if (warp == 0) {
     // TMA producer (both CTAs); both CTAs' copies complete on the leader's "full" barrier.
     uint32_t it = 0;
     bool ok = true;
-    auto product = [&](auto opc, int cur) {
+    auto product = [&](auto opc, int cur, int set) {
       constexpr int OP = decltype(opc)::value;
       constexpr bool A_MN = TALL && OP == kGram;
       constexpr bool B_MN = (TALL && OP == kGram) || (!TALL && OP == kUpdate);
       const OrthGeom& g = ch.geom[OP];
       const CUtensorMap* ma = &maps.a[OP][cur];
       const CUtensorMap* mb = &maps.b[OP][cur];
-      for (int u = pair; ok && u < g.num_units; u += npairs) {
+      int u0, u1, stride;
+      units(OP, set, u0, u1, stride);
+      for (int u = u0; ok && u < u1; u += stride) {
         int z, i, j, nsub;
         orth_unit<BNI, NSUB, OP != kUpdate>(g, u, z, i, j, nsub);
         const int mrow = i * 2 * kBM + static_cast<int>(rank) * kBM;
@@ -564,22 +600,40 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         }
       }
     };
-    for (int p = 0; ok && p < products; ++p) {
-      if (p > 0) {
-        // Every CTA has finished the product before; let this CTA's epilogue know.
-        ok = wait_met(ch.counter, p * static_cast<int>(gridDim.x), abort, ctl);
-        if (lane == 0) mbar_arrive(&pc->met);
-        __syncwarp();
-        if (!ok) break;
+    const uint32_t both_own = mapa_shared(smem_u32(&pc->both), rank);
+    const uint32_t both_peer = mapa_shared(smem_u32(&pc->both), rank ^ 1);
+    int met = 0;  // products begun, less one
+    for (int q = 0; ok && q < sets; ++q)
+      for (int p = 0; ok && p < products; ++p) {
+        if (p > 0 || q > 0) {
+          // This CTA's part of the product before is in memory; wait for the others' and let
+          // the epilogue know.
+          ok = wait_warp(&pc->done, met & 1, abort, ctl);
+          if (ok && ch.own) {
+            if (lane == 0) {
+              mbar_arrive_cluster(both_own);
+              mbar_arrive_cluster(both_peer);
+            }
+            __syncwarp();
+            ok = wait_both(&pc->both, met & 1, abort, ctl);
+          } else if (ok) {
+            if (lane == 0) red_release_add_s32(ch.counter, 1);
+            __syncwarp();
+            ok = wait_met(ch.counter, (met + 1) * static_cast<int>(gridDim.x), abort, ctl);
+          }
+          ++met;
+          if (lane == 0) mbar_arrive(&pc->met);
+          __syncwarp();
+          if (!ok) break;
+        }
+        const int cur = (p / 3) & 1;
+        if (p % 3 == 0)
+          product(std::integral_constant<int, kGram>{}, cur, q);
+        else if (p % 3 == 1)
+          product(std::integral_constant<int, kSquare>{}, 0, q);
+        else
+          product(std::integral_constant<int, kUpdate>{}, cur, q);
       }
-      const int cur = (p / 3) & 1;
-      if (p % 3 == 0)
-        product(std::integral_constant<int, kGram>{}, cur);
-      else if (p % 3 == 1)
-        product(std::integral_constant<int, kSquare>{}, 0);
-      else
-        product(std::integral_constant<int, kUpdate>{}, cur);
-    }
     if (ok) {
       // No remote release of a stage may reach this CTA after it has exited: wait for the
       // releases of the last stages.
@@ -602,7 +656,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     if (leader) {
       uint32_t it = 0, t = 0, used0 = 0, used1 = 0;
       bool ok = true;
-      auto product = [&](auto opc) {
+      auto product = [&](auto opc, int set) {
         constexpr int OP = decltype(opc)::value;
         constexpr bool A_MN = TALL && OP == kGram;
         constexpr bool B_MN = (TALL && OP == kGram) || (!TALL && OP == kUpdate);
@@ -621,7 +675,9 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
             umma_bf16_pair(tmem + b * BNI, ad, bd, kIdesc, (!first || kk != 0) ? 1u : 0u);
           }
         };
-        for (int u = pair; u < g.num_units; u += npairs, ++t) {
+        int u0, u1, stride;
+        units(OP, set, u0, u1, stride);
+        for (int u = u0; u < u1; u += stride, ++t) {
           int z, i, j, nsub;
           orth_unit<BNI, NSUB, OP != kUpdate>(g, u, z, i, j, nsub);
           const int b0 = NSUB == 2 ? 0 : static_cast<int>(t & 1u);
@@ -674,14 +730,15 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
           __syncwarp();
         }
       };
-      for (int p = 0; ok && p < products; ++p) {
-        if (p % 3 == 0)
-          product(std::integral_constant<int, kGram>{});
-        else if (p % 3 == 1)
-          product(std::integral_constant<int, kSquare>{});
-        else
-          product(std::integral_constant<int, kUpdate>{});
-      }
+      for (int q = 0; ok && q < sets; ++q)
+        for (int p = 0; ok && p < products; ++p) {
+          if (p % 3 == 0)
+            product(std::integral_constant<int, kGram>{}, q);
+          else if (p % 3 == 1)
+            product(std::integral_constant<int, kSquare>{}, q);
+          else
+            product(std::integral_constant<int, kUpdate>{}, q);
+        }
       // Every MMA must be complete (in both CTAs' TMEM) before TMEM is released.
       if (lane == 0) umma_commit_pair_mc(&pc->fin, 0x1);
       __syncwarp();
@@ -698,7 +755,8 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     const uint32_t tempty1 = mapa_shared(smem_u32(&pc->tempty[1]), 0);
     uint32_t t = 0, used0 = 0, used1 = 0;
     bool ok = true;
-    auto product = [&](auto opc, auto lastc, int step) {
+    float* dstage = pc->diag[warp - 2];
+    auto product = [&](auto opc, auto lastc, int step, int set) {
       constexpr int OP = decltype(opc)::value;
       constexpr bool LAST = decltype(lastc)::value;
       constexpr bool kSym = OP != kUpdate;
@@ -708,25 +766,29 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
                        OP == kUpdate ? ch.ldx : ch.ldk, ch.k,
                        OP == kUpdate ? ch.hi[cur] : ch.mat[0], ch.lo,
                        OP == kSquare ? ch.diag[0] : ch.diag[1],
-                       OP == kGram ? ch.diag[0] : ch.diag[1], ch.out, ch.co[step][0],
-                       ch.co[step][1], ch.co[step][2], TALL, ch.out_vec};
-      const CUtensorMap* st0 = OP == kGram ? &maps.mat[0] : OP == kSquare ? &maps.mat[1]
-                               : LAST ? &maps.out : &maps.hi[cur ^ 1];
-      for (int u = pair; ok && u < geo.num_units; u += npairs, ++t) {
+                       OP == kGram ? ch.diag[0] : ch.diag[1],
+                       OP == kGram     ? static_cast<void*>(ch.mat[0])
+                       : OP == kSquare ? static_cast<void*>(ch.mat[1])
+                       : LAST          ? static_cast<void*>(ch.out)
+                                       : static_cast<void*>(ch.hi[cur ^ 1]),
+                       ch.co[step][0],
+                       ch.co[step][1], ch.co[step][2], ch.out_vec};
+      int u0, u1, stride;
+      units(OP, set, u0, u1, stride);
+      for (int u = u0; ok && u < u1; u += stride, ++t) {
         int z, i, j, nsub;
         orth_unit<BNI, NSUB, kSym>(geo, u, z, i, j, nsub);
-        const int64_t row = static_cast<int64_t>(i) * 2 * kBM + rank * kBM + q * 32 + lane;
-        const int64_t row0 = row - lane;
+        const int row = i * 2 * kBM + static_cast<int>(rank) * kBM + q * 32 + lane;
+        const int row0 = row - lane;
         float drow = 0.f;
         if (OP == kSquare || (OP == kUpdate && !TALL))
           if (row < g.rows) drow = g.diag_in[static_cast<int64_t>(z) * g.diag_n + row];
         for (int h = 0; h < nsub; ++h) {
           const int b = NSUB == 2 ? h : static_cast<int>(t & 1u);
           uint32_t& used = b ? used1 : used0;
-          const int64_t col0 = static_cast<int64_t>(j) * C::kTileN + h * BNI + wg * kShare;
-          const bool mirror =
-              kSym && col0 - wg * kShare + BNI <= static_cast<int64_t>(i) * 2 * kBM;
-          OrthIn<OP> in;
+          const int col0 = j * C::kTileN + h * BNI + wg * kShare;
+          const bool mirror = kSym && col0 - wg * kShare + BNI <= i * 2 * kBM;
+          OrthIn<OP, TALL> in;
           in.fetch(g, z, row0, col0, lane);
           if (!wait_warp(&pc->tfull[b], used & 1u, abort, ctl)) {
             ok = false;
@@ -738,11 +800,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
           for (int c = 0; c < kChunks; ++c) {
             float v[32];
             tmem_ld32(tmem + lane_bits + b * BNI + wg * kShare + c * 32, v);
-            // The staging blocks are free once the stores of the block before have read them.
-            if (lane == 0) bulk_wait_read_all();
-            __syncwarp();
-            in.put(stage, lane);
-            const float dcol = in.dcol;
+            in.put(stage, dstage, lane);
             if (c + 1 < kChunks) in.fetch(g, z, row0, col0 + (c + 1) * 32, lane);
             tmem_ld_wait();
             if (c == kChunks - 1) {
@@ -756,41 +814,34 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
               __syncwarp();
             }
             if (col0 + c * 32 < g.cols)
-              orth_epilogue<OP, LAST>(g, st0, &maps.lo, stage, z, row, col0 + c * 32, mirror,
-                                      drow, dcol, v);
+              orth_epilogue<OP, LAST, TALL>(g, stage, dstage, z, row, col0 + c * 32, mirror,
+                                            drow, v);
           }
         }
       }
     };
-    for (int p = 0; ok && p < products; ++p) {
-      if (p > 0) ok = wait_warp(&pc->met, (p - 1) & 1u, abort, ctl);
-      if (!ok) break;
-      const int step = p / 3;
-      if (p % 3 == 0)
-        product(std::integral_constant<int, kGram>{}, std::false_type{}, step);
-      else if (p % 3 == 1)
-        product(std::integral_constant<int, kSquare>{}, std::false_type{}, step);
-      else if (step + 1 < ch.steps)
-        product(std::integral_constant<int, kUpdate>{}, std::false_type{}, step);
-      else
-        product(std::integral_constant<int, kUpdate>{}, std::true_type{}, step);
-      if (!ok) break;
-      // This warp's part of the product is in memory: bulk stores complete, plain stores fenced.
-      // The last of the CTA's warps reports (nobody blocks: after a wait that ran out, some
-      // warps may never come here).
-      if (lane == 0) {
-        bulk_wait_all();
+    int met = 0;
+    for (int q = 0; ok && q < sets; ++q)
+      for (int p = 0; ok && p < products; ++p) {
+        if (p > 0 || q > 0) ok = wait_warp(&pc->met, met++ & 1, abort, ctl);
+        if (!ok) break;
+        const int step = p / 3;
+        if (p % 3 == 0)
+          product(std::integral_constant<int, kGram>{}, std::false_type{}, step, q);
+        else if (p % 3 == 1)
+          product(std::integral_constant<int, kSquare>{}, std::false_type{}, step, q);
+        else if (step + 1 < ch.steps)
+          product(std::integral_constant<int, kUpdate>{}, std::false_type{}, step, q);
+        else
+          product(std::integral_constant<int, kUpdate>{}, std::true_type{}, step, q);
+        if (!ok) break;
+        // This warp's part of the product, stored by plain stores and loaded by bulk copies,
+        // becomes visible in order by the arrival, which the loading warp passes on at the
+        // meeting's scope.
         fence_proxy_async_global();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pc->done);
       }
-      __threadfence();
-      __syncwarp();
-      if (lane == 0 && atomicAdd(&pc->done, 1) == 4 * kOrthWG * (p + 1) - 1) {
-        __threadfence();
-        red_release_add_s32(ch.counter, 1);
-      }
-    }
-    if (lane == 0) bulk_wait_all();
-    __syncwarp();
   }
 
   // Neither CTA leaves while the other may still signal its barriers or use its TMEM.
@@ -835,9 +886,9 @@ cudaError_t launch_chain(const OrthChain& ch, const OrthMaps& maps, const DevCtl
     max_clusters[dev] = n > 0 ? n : 1;
   }
   cfg.numAttrs = 2;
-  int units = 1;
-  for (const OrthGeom& g : ch.geom) units = std::max(units, g.num_units);
-  cfg.gridDim = dim3(2 * std::min(units, max_clusters[dev]), 1, 1);
+  int pairs = 1;
+  for (const OrthGeom& g : ch.geom) pairs = std::max(pairs, ch.own ? ch.batch : g.num_units);
+  cfg.gridDim = dim3(2 * std::min(pairs, max_clusters[dev]), 1, 1);
   return cudaLaunchKernelEx(&cfg, kern, ch, maps, c);
 }
 

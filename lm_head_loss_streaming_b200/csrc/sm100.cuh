@@ -88,15 +88,6 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
       "r"(x), "r"(y), "r"(smem_u32(smem_src))
       : "memory");
 }
-// The same into a 3-D map (a stack of matrices).
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* smem_src,
-                                             int32_t x, int32_t y, int32_t z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-          reinterpret_cast<uint64_t>(map)),
-      "r"(x), "r"(y), "r"(z), "r"(smem_u32(smem_src))
-      : "memory");
-}
 __device__ __forceinline__ void bulk_commit() {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
