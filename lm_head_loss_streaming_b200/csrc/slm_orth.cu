@@ -186,8 +186,9 @@ __global__ void __launch_bounds__(kPrepThreads) orth_scale(const OrthPrep p, int
 
 // ----------------------------------------------------------------------------------------
 // The products: all of them in one cooperative launch of 2-SM GEMMs (M = 256 rows per CTA pair,
-// fp16 operands).  Warp 0 loads, warp 1 issues the MMAs, eight warps run the epilogue, each
-// warpgroup over half of the columns.  Operands are K-major or MN-major as they lie in memory,
+// fp16 operands).  Warp 0 loads, warp 1 issues the MMAs, sixteen warps run the epilogue, each
+// warpgroup over a quarter of a slot's columns (eight warps took 1.8 times as long: a block of
+// 32 x 32 is 3000 cycles of mostly dependent shared and global memory accesses).  Operands are K-major or MN-major as they lie in memory,
 // so that no transpose of X is ever stored.  Per step:
 //   kGram    R, D of A = X X^T:  a symmetric product, only blocks on and below the diagonal
 //            are computed and each is written to its mirrored place too
@@ -263,10 +264,10 @@ __device__ __forceinline__ bool wait_met(const int* counter, int target, volatil
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
-// Staging of an epilogue warp: two blocks of 32 rows x 32 fp16 columns, 64 bytes per row, with
+// Staging of an epilogue warp: a block of 32 rows x 32 fp16 columns, 64 bytes per row, with
 // 16-byte piece k of row r at k ^ (r / 2 % 4), so that neither a lane per row nor four lanes
 // per row conflict.
-constexpr int kOrthStage = 4096;
+constexpr int kOrthStage = 2048;
 __device__ __forceinline__ int stage_piece(int row, int k) {
   return row * 4 + (k ^ ((row >> 1) & 3));
 }
@@ -276,7 +277,6 @@ struct OrthCtl {
   uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], fin, met, done, both;
   uint32_t tmem_base;
   int abort;
-  alignas(16) float diag[4 * kOrthWG][32];  // the epilogue warps' entries of a block's columns
 };
 
 template <int BNI, int NSUB>
@@ -339,126 +339,118 @@ __device__ __forceinline__ uint32_t pack_bf162(float a, float b) {
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// What the epilogue reads for a warp's block of 32 rows x 32 columns: fetched a block ahead, so
-// that its latency passes behind the MMAs or the block before.  Four lanes share a row, so that
-// every load covers whole 64-byte pieces of rows.
-template <int OP, bool TALL>
-struct OrthIn {
-  static constexpr int kSets = OP == kGram ? 0 : OP == kSquare ? 1 : 2;
-  static constexpr bool kCols = OP == kSquare || (OP == kUpdate && TALL);
-  uint4 w[kSets == 0 ? 1 : kSets][4];  // kSquare: R; kUpdate: hi, lo
-  float dcol;                          // lane l: the diagonal's entry of column col + l
-  __device__ __forceinline__ void fetch(const OrthView& g, int z, int row0, int col, int lane) {
-    if (OP == kGram || col >= g.cols) return;
-    if (kCols)
-      dcol = col + lane < g.cols ? g.diag_in[static_cast<int64_t>(z) * g.diag_n + col + lane] : 0.f;
+// A warp's block, rows [row0, row0 + 32) and columns [col, col + 32) of a matrix at `src` whose
+// rows are padded to whole 16-byte pieces: four lanes per row, so that every access covers whole
+// 64-byte runs of rows, ...
+struct OrthBlock {
+  uint4 w[4];
+  __device__ __forceinline__ void load(const __half* src, int64_t ld, int row0, int col, int rows,
+                                       int cols, int lane) {
     const int c = col + (lane & 3) * 8, row = row0 + (lane >> 2);
-    const int64_t at = (static_cast<int64_t>(z) * g.rows + row) * g.ld + c;
-    const int64_t step = static_cast<int64_t>(g.ld) * 8;
+    const uint4* at = reinterpret_cast<const uint4*>(src + row * ld + c);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      w[q] = row + q * 8 < rows && c < cols ? at[q * ld] : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void store(void* dst, int64_t ld, int row0, int col, int rows,
+                                        int cols, int lane) const {
+    const int c = col + (lane & 3) * 8, row = row0 + (lane >> 2);
+    uint4* at = reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + row * ld + c);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (row + q * 8 < rows && c < cols) at[q * ld] = w[q];
+  }
+  // ... turned through the staging into a lane per row and back.
+  __device__ __forceinline__ void to_rows(uint4* stage, int lane, uint32_t (&r)[16]) const {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) stage[stage_piece(q * 8 + (lane >> 2), lane & 3)] = w[q];
+    __syncwarp();
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const bool in = row + q * 8 < g.rows && c < g.cols;  // rows are padded to whole pieces
-      const uint4 none = make_uint4(0, 0, 0, 0);
-      w[0][q] = !in ? none : *reinterpret_cast<const uint4*>(g.in + at + q * step);
-      if (OP == kUpdate)
-        w[kSets - 1][q] = !in ? none : *reinterpret_cast<const uint4*>(g.lo + at + q * step);
+      const uint4 v = stage[stage_piece(lane, q)];
+      r[4 * q] = v.x;
+      r[4 * q + 1] = v.y;
+      r[4 * q + 2] = v.z;
+      r[4 * q + 3] = v.w;
     }
+    __syncwarp();
   }
-  // Into the warp's staging blocks.
-  __device__ __forceinline__ void put(uint4* stage, float* dstage, int lane) const {
+  __device__ __forceinline__ void from_rows(uint4* stage, int lane, const uint32_t (&r)[16],
+                                            bool zero_diagonal = false) {
 #pragma unroll
-    for (int e = 0; e < kSets; ++e)
+    for (int q = 0; q < 4; ++q)
+      stage[stage_piece(lane, q)] = make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+    if (zero_diagonal)
+      reinterpret_cast<uint16_t*>(stage)[stage_piece(lane, lane >> 3) * 8 + (lane & 7)] = 0;
+    __syncwarp();
+    read(stage, lane);
+  }
+  __device__ __forceinline__ void read(const uint4* stage, int lane) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        stage[e * 128 + stage_piece(q * 8 + (lane >> 2), lane & 3)] = w[e][q];
-    if (kCols) dstage[lane] = dcol;
+    for (int q = 0; q < 4; ++q) w[q] = stage[stage_piece(q * 8 + (lane >> 2), lane & 3)];
+    __syncwarp();
   }
 };
 
-// A staged block to rows [row0, row0 + 32), columns [col, col + 32) of the matrix at `dst`, whose
-// rows are padded to whole pieces: four lanes per row.  (Bulk stores from the staging measured
-// slower: each block waited about 0.7 us for the one before to be read.)
-__device__ __forceinline__ void unstage(const uint4* block, void* dst, int64_t ld, int row0,
-                                        int col, int rows, int cols, int lane) {
-  const int c = col + (lane & 3) * 8, row = row0 + (lane >> 2);
-  uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + row * ld + c);
-  const int64_t step = ld;  // 8 rows of ld / 8 pieces
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const uint4 w = block[stage_piece(q * 8 + (lane >> 2), lane & 3)];
-    if (row + q * 8 < rows && c < cols) out[q * step] = w;
-  }
-}
-
-// One warp's block: this lane's row `row`, columns [col, col + 32) of matrix z.  The block's
-// inputs lie in the staging blocks; its outputs take their place, each lane its own row, and go
-// out from there.
+// One warp's block of product OP: v holds this lane's row `row`, columns [col, col + 32) of the
+// accumulator of matrix z.  (Bulk stores from the staging measured slower: a block waited about
+// 0.7 us for the one before to be read.)
 template <int OP, bool LAST, bool TALL>
-__device__ __forceinline__ void orth_epilogue(const OrthView& g, uint4* stage,
-                                              const float* dstage, int z, int row, int col,
-                                              bool mirror, float drow, float (&v)[32]) {
-  constexpr int kSets = OrthIn<OP, TALL>::kSets;
+__device__ __forceinline__ void orth_epilogue(const OrthView& g, uint4* stage, int z, int row,
+                                              int col, bool mirror, float drow, float (&v)[32]) {
+  constexpr bool kCols = OP == kSquare || (OP == kUpdate && TALL);  // needs D of the columns
   const int lane = threadIdx.x & 31;
-  const float4* d4 = reinterpret_cast<const float4*>(dstage);
-  uint32_t lo_out[OP == kUpdate ? 16 : 1];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {  // 8 columns at a time
-    uint32_t in[2][4];
-#pragma unroll
-    for (int e = 0; e < kSets; ++e) {
-      const uint4 w = stage[e * 128 + stage_piece(lane, q)];
-      in[e][0] = w.x;
-      in[e][1] = w.y;
-      in[e][2] = w.z;
-      in[e][3] = w.w;
-    }
-    uint32_t out[4];
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {  // a pair of columns
-      const float2 x = make_float2(v[8 * q + 2 * h], v[8 * q + 2 * h + 1]);
-      float2 d = both(drow);
-      if (OrthIn<OP, TALL>::kCols) {
-        const float4 f = d4[2 * q + h / 2];
-        d = h & 1 ? make_float2(f.z, f.w) : make_float2(f.x, f.y);
-      }
-      if (OP == kGram) {
-        const float2 r = __fmul2_rn(x, both(kScaleA / (kScaleX * kScaleX)));
-        out[h] = pack_half2(r.x, r.y);
-      } else if (OP == kSquare) {
-        // scaled c (R R + (D_i + D_j) R) + b R
-        const float2 t = __ffma2_rn(both(g.c * (kScaleB / kScaleA)), d,
-                                    both(fmaf(g.c, drow, g.b) * (kScaleB / kScaleA)));
-        const float2 r = __ffma2_rn(unpack_half2(in[0][h]), t,
-                                    __fmul2_rn(x, both(g.c * (kScaleB / (kScaleA * kScaleA)))));
-        out[h] = pack_half2(r.x, r.y);
-      } else {
-        const float2 r =
-            __ffma2_rn(x, both(1.f / kScaleB),
-                       __ffma2_rn(unpack_half2(in[0][h]), __fadd2_rn(d, both(g.a)),
-                                  __fmul2_rn(unpack_half2(in[kSets - 1][h]), both(g.a))));
-        if (LAST) {
-          out[h] = pack_bf162(r.x * (1.f / kScaleX), r.y * (1.f / kScaleX));
-        } else {
-          out[h] = pack_half2(r.x, r.y);
-          const float2 hi = unpack_half2(out[h]);
-          lo_out[OP == kUpdate ? 4 * q + h : 0] = pack_half2(r.x - hi.x, r.y - hi.y);
-        }
-      }
-    }
-    stage[stage_piece(lane, q)] = make_uint4(out[0], out[1], out[2], out[3]);
-    if (OP == kUpdate && !LAST)
-      stage[128 + stage_piece(lane, q)] = make_uint4(lo_out[4 * q], lo_out[4 * q + 1],
-                                                     lo_out[4 * q + 2], lo_out[4 * q + 3]);
-    if (OP != kUpdate && mirror) {
-      // The transpose: column c of the block as row c, a lane per element.
-      uint16_t* t = reinterpret_cast<uint16_t*>(stage + 128);
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-        t[stage_piece(8 * q + c, lane >> 3) * 8 + (lane & 7)] =
-            static_cast<uint16_t>(c & 1 ? out[c / 2] >> 16 : out[c / 2]);
+  const int row0 = row - lane;
+  const int64_t base = static_cast<int64_t>(z) * g.rows * g.ld;
+  uint32_t hi[16], lo[16];
+  OrthBlock blk;
+  if (OP != kGram) {
+    OrthBlock blk_lo;
+    blk.load(g.in + base, g.ld, row0, col, g.rows, g.cols, lane);
+    if (OP == kUpdate) blk_lo.load(g.lo + base, g.ld, row0, col, g.rows, g.cols, lane);
+    float dcol = 0.f;
+    if (kCols && col + lane < g.cols)
+      dcol = g.diag_in[static_cast<int64_t>(z) * g.diag_n + col + lane];
+    blk.to_rows(stage, lane, hi);
+    if (OP == kUpdate) blk_lo.to_rows(stage, lane, lo);
+    if (kCols) {
+      reinterpret_cast<float*>(stage)[lane] = dcol;
+      __syncwarp();
     }
   }
-  const int row0 = row - lane;
+  const float4* d4 = reinterpret_cast<const float4*>(stage);
+#pragma unroll
+  for (int h = 0; h < 16; ++h) {  // a pair of columns
+    const float2 x = make_float2(v[2 * h], v[2 * h + 1]);
+    float2 d = both(drow);
+    if (kCols) {
+      const float4 f = d4[h / 2];
+      d = h & 1 ? make_float2(f.z, f.w) : make_float2(f.x, f.y);
+    }
+    if (OP == kGram) {
+      const float2 r = __fmul2_rn(x, both(kScaleA / (kScaleX * kScaleX)));
+      hi[h] = pack_half2(r.x, r.y);
+    } else if (OP == kSquare) {
+      // scaled c (R R + (D_i + D_j) R) + b R
+      const float2 t = __ffma2_rn(both(g.c * (kScaleB / kScaleA)), d,
+                                  both(fmaf(g.c, drow, g.b) * (kScaleB / kScaleA)));
+      const float2 r = __ffma2_rn(unpack_half2(hi[h]), t,
+                                  __fmul2_rn(x, both(g.c * (kScaleB / (kScaleA * kScaleA)))));
+      hi[h] = pack_half2(r.x, r.y);
+    } else {
+      const float2 r = __ffma2_rn(x, both(1.f / kScaleB),
+                                  __ffma2_rn(unpack_half2(hi[h]), __fadd2_rn(d, both(g.a)),
+                                             __fmul2_rn(unpack_half2(lo[h]), both(g.a))));
+      if (LAST) {
+        hi[h] = pack_bf162(r.x * (1.f / kScaleX), r.y * (1.f / kScaleX));
+      } else {
+        hi[h] = pack_half2(r.x, r.y);
+        const float2 f = unpack_half2(hi[h]);
+        lo[h] = pack_half2(r.x - f.x, r.y - f.y);
+      }
+    }
+  }
+  if (kCols) __syncwarp();  // the staging is free again
   if (OP != kUpdate && row0 == col) {
     // The block on the diagonal: this lane's diagonal element goes to the fp32 diagonal, a zero
     // takes its place.  (Selected, not branched to: a branch per lane took 3 us.)
@@ -469,28 +461,43 @@ __device__ __forceinline__ void orth_epilogue(const OrthView& g, uint4* stage,
       g.diag_out[static_cast<int64_t>(z) * g.diag_n + row] =
           OP == kGram ? x * (1.f / (kScaleX * kScaleX))
                       : fmaf(g.c, fmaf(drow, drow, x * (1.f / (kScaleA * kScaleA))), g.b * drow);
-    reinterpret_cast<uint16_t*>(stage)[stage_piece(lane, lane >> 3) * 8 + (lane & 7)] = 0;
   }
-  __syncwarp();
-  const int64_t base = static_cast<int64_t>(z) * g.rows * (LAST ? g.cols : g.ld);
   if (LAST && !g.out_vec) {
     // Rows of the result that do not start on 16-byte boundaries: element stores, a row per
     // instruction.
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      stage[stage_piece(lane, q)] = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
+    __syncwarp();
     const uint16_t* el = reinterpret_cast<const uint16_t*>(stage);
-    uint16_t* dst = static_cast<uint16_t*>(g.out) + base + static_cast<int64_t>(row0) * g.cols + col + lane;
+    uint16_t* dst = static_cast<uint16_t*>(g.out) +
+                    (static_cast<int64_t>(z) * g.rows + row0) * g.cols + col + lane;
     const int rows = min(32, g.rows - row0);
     if (col + lane < g.cols)
       for (int r = 0; r < rows; ++r)
         dst[static_cast<int64_t>(r) * g.cols] = el[stage_piece(r, lane >> 3) * 8 + (lane & 7)];
-  } else {
-    unstage(stage, static_cast<uint16_t*>(g.out) + base, LAST ? g.cols : g.ld, row0, col, g.rows,
-            g.cols, lane);
+    __syncwarp();
+    return;
   }
-  if (OP == kUpdate && !LAST)
-    unstage(stage + 128, g.lo + base, g.ld, row0, col, g.rows, g.cols, lane);
-  if (OP != kUpdate && mirror)
-    unstage(stage + 128, static_cast<uint16_t*>(g.out) + base, g.ld, col, row0, g.cols, g.rows, lane);
-  __syncwarp();  // the staging is free again
+  const int64_t out_ld = LAST ? g.cols : g.ld;
+  uint16_t* out = static_cast<uint16_t*>(g.out) + static_cast<int64_t>(z) * g.rows * out_ld;
+  blk.from_rows(stage, lane, hi, OP != kUpdate && row0 == col);
+  blk.store(out, out_ld, row0, col, g.rows, g.cols, lane);
+  if (OP == kUpdate && !LAST) {
+    blk.from_rows(stage, lane, lo);
+    blk.store(g.lo + base, g.ld, row0, col, g.rows, g.cols, lane);
+  }
+  if (OP != kUpdate && mirror) {
+    // The transpose: column c of the block as row c, a lane per element.
+    uint16_t* t = reinterpret_cast<uint16_t*>(stage);
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      t[stage_piece(c, lane >> 3) * 8 + (lane & 7)] =
+          static_cast<uint16_t>(c & 1 ? hi[c / 2] >> 16 : hi[c / 2]);
+    __syncwarp();
+    blk.read(stage, lane);
+    blk.store(out, out_ld, col, row0, g.cols, g.rows, lane);
+  }
 }
 
 template <int BNI, int NSUB, bool TALL>
@@ -755,7 +762,6 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     const uint32_t tempty1 = mapa_shared(smem_u32(&pc->tempty[1]), 0);
     uint32_t t = 0, used0 = 0, used1 = 0;
     bool ok = true;
-    float* dstage = pc->diag[warp - 2];
     auto product = [&](auto opc, auto lastc, int step, int set) {
       constexpr int OP = decltype(opc)::value;
       constexpr bool LAST = decltype(lastc)::value;
@@ -779,7 +785,6 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         int z, i, j, nsub;
         orth_unit<BNI, NSUB, kSym>(geo, u, z, i, j, nsub);
         const int row = i * 2 * kBM + static_cast<int>(rank) * kBM + q * 32 + lane;
-        const int row0 = row - lane;
         float drow = 0.f;
         if (OP == kSquare || (OP == kUpdate && !TALL))
           if (row < g.rows) drow = g.diag_in[static_cast<int64_t>(z) * g.diag_n + row];
@@ -788,8 +793,6 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
           uint32_t& used = b ? used1 : used0;
           const int col0 = j * C::kTileN + h * BNI + wg * kShare;
           const bool mirror = kSym && col0 - wg * kShare + BNI <= i * 2 * kBM;
-          OrthIn<OP, TALL> in;
-          in.fetch(g, z, row0, col0, lane);
           if (!wait_warp(&pc->tfull[b], used & 1u, abort, ctl)) {
             ok = false;
             break;
@@ -800,8 +803,6 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
           for (int c = 0; c < kChunks; ++c) {
             float v[32];
             tmem_ld32(tmem + lane_bits + b * BNI + wg * kShare + c * 32, v);
-            in.put(stage, dstage, lane);
-            if (c + 1 < kChunks) in.fetch(g, z, row0, col0 + (c + 1) * 32, lane);
             tmem_ld_wait();
             if (c == kChunks - 1) {
               // The slot is drained once this load has completed.
@@ -810,12 +811,9 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
               // Test hook (fault == 1): withhold the release of the first accumulator.
               if (lane == 0 && !(ctl.fault == 1 && t == 0))
                 mbar_arrive_cluster(b ? tempty1 : tempty0);
-            } else {
-              __syncwarp();
             }
             if (col0 + c * 32 < g.cols)
-              orth_epilogue<OP, LAST, TALL>(g, stage, dstage, z, row, col0 + c * 32, mirror,
-                                            drow, v);
+              orth_epilogue<OP, LAST, TALL>(g, stage, z, row, col0 + c * 32, mirror, drow, v);
           }
         }
       }
