@@ -392,31 +392,43 @@ struct OrthBlock {
   }
 };
 
+// What a block's epilogue reads, fetched a block ahead (behind the MMAs, or the block before).
+template <int OP, bool TALL>
+struct OrthIn {
+  static constexpr bool kCols = OP == kSquare || (OP == kUpdate && TALL);  // D of the columns
+  OrthBlock hi, lo;  // kSquare: R in hi
+  float dcol;        // lane l: the diagonal's entry of column col + l
+  __device__ __forceinline__ void fetch(const OrthView& g, int z, int row0, int col, int lane) {
+    if (OP == kGram) return;
+    const int64_t base = static_cast<int64_t>(z) * g.rows * g.ld;
+    hi.load(g.in + base, g.ld, row0, col, g.rows, g.cols, lane);
+    if (OP == kUpdate) lo.load(g.lo + base, g.ld, row0, col, g.rows, g.cols, lane);
+    if (kCols)
+      dcol = col + lane < g.cols ? g.diag_in[static_cast<int64_t>(z) * g.diag_n + col + lane] : 0.f;
+  }
+};
+
 // One warp's block of product OP: v holds this lane's row `row`, columns [col, col + 32) of the
 // accumulator of matrix z.  (Bulk stores from the staging measured slower: a block waited about
 // 0.7 us for the one before to be read.)
 template <int OP, bool LAST, bool TALL>
 __device__ __forceinline__ void orth_epilogue(const OrthView& g, uint4* stage, int z, int row,
-                                              int col, bool mirror, float drow, float (&v)[32]) {
-  constexpr bool kCols = OP == kSquare || (OP == kUpdate && TALL);  // needs D of the columns
+                                              int col, int next_col, bool mirror, float drow,
+                                              OrthIn<OP, TALL>& in, float (&v)[32]) {
+  constexpr bool kCols = OrthIn<OP, TALL>::kCols;
   const int lane = threadIdx.x & 31;
   const int row0 = row - lane;
   const int64_t base = static_cast<int64_t>(z) * g.rows * g.ld;
   uint32_t hi[16], lo[16];
   OrthBlock blk;
   if (OP != kGram) {
-    OrthBlock blk_lo;
-    blk.load(g.in + base, g.ld, row0, col, g.rows, g.cols, lane);
-    if (OP == kUpdate) blk_lo.load(g.lo + base, g.ld, row0, col, g.rows, g.cols, lane);
-    float dcol = 0.f;
-    if (kCols && col + lane < g.cols)
-      dcol = g.diag_in[static_cast<int64_t>(z) * g.diag_n + col + lane];
-    blk.to_rows(stage, lane, hi);
-    if (OP == kUpdate) blk_lo.to_rows(stage, lane, lo);
+    in.hi.to_rows(stage, lane, hi);
+    if (OP == kUpdate) in.lo.to_rows(stage, lane, lo);
     if (kCols) {
-      reinterpret_cast<float*>(stage)[lane] = dcol;
+      reinterpret_cast<float*>(stage)[lane] = in.dcol;
       __syncwarp();
     }
+    if (next_col >= 0) in.fetch(g, z, row0, next_col, lane);
   }
   const float4* d4 = reinterpret_cast<const float4*>(stage);
 #pragma unroll
@@ -793,6 +805,8 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
           uint32_t& used = b ? used1 : used0;
           const int col0 = j * C::kTileN + h * BNI + wg * kShare;
           const bool mirror = kSym && col0 - wg * kShare + BNI <= i * 2 * kBM;
+          OrthIn<OP, TALL> in;
+          in.fetch(g, z, row - lane, col0, lane);
           if (!wait_warp(&pc->tfull[b], used & 1u, abort, ctl)) {
             ok = false;
             break;
@@ -813,7 +827,9 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
                 mbar_arrive_cluster(b ? tempty1 : tempty0);
             }
             if (col0 + c * 32 < g.cols)
-              orth_epilogue<OP, LAST, TALL>(g, stage, z, row, col0 + c * 32, mirror, drow, v);
+              orth_epilogue<OP, LAST, TALL>(g, stage, z, row, col0 + c * 32,
+                                            c + 1 < kChunks ? col0 + (c + 1) * 32 : -1, mirror,
+                                            drow, in, v);
           }
         }
       }
