@@ -527,8 +527,7 @@ bool make_map_stack(CUtensorMap* m, const void* base, int64_t inner, int64_t out
 // seconds, the CTAs' meeting after it included.  Per 64-wide K block a tile takes its MMAs
 // (27 TFLOP/s per pair; two thirds of that at 128 columns) or its operands' way from L2 (9.3 TB/s
 // shared by the pairs that are busy), whichever is longer; the rates as measured on the products
-// of 4096 x 4096 matrices.  A round of tiles also costs its epilogue, about 0.5 us per 128
-// columns.  `own`: one pair works all tiles of a matrix.
+// of 4096 x 4096 matrices.  A round of tiles also costs its epilogue, about 1 us per 128 columns.  `own`: one pair works all tiles of a matrix.
 double orth_tiles(OrthGeom* g, int bn, bool own, int64_t rows, int64_t cols, int64_t k,
                   int64_t batch, bool sym) {
   const int64_t pairs = std::max(1, sm_count() / 2);
@@ -545,7 +544,7 @@ double orth_tiles(OrthGeom* g, int bn, bool own, int64_t rows, int64_t cols, int
   auto round = [&](int64_t busy) {
     const double mma = 2.0 * kPairM * bn * kBK / (bn == 128 ? 18e12 : 27e12);
     const double l2 = (kPairM + bn) * kBK * 2.0 * static_cast<double>(busy) / 9.3e12;
-    return g->k_blocks * std::max(mma, l2) + 0.5e-6 * bn / 128;
+    return g->k_blocks * std::max(mma, l2) + 1e-6 * bn / 128;
   };
   if (own) {
     const int64_t busy = std::min(batch, pairs);
@@ -1270,6 +1269,9 @@ int slm_orthogonalize(int dtype, const void* grad, int64_t ld, int64_t batch_str
   const int64_t k = L.k;
   OrthChain ch{};
   const int bn = orth_plan(&ch, m, n, batch);
+  // At most one tile of the update per pair, and a second accumulator slot free for it.
+  ch.resident = bn <= 256 && steps > 1 &&
+                (ch.own ? ch.geom[2].units_per == 1 : ch.geom[2].num_units <= sm_count() / 2);
   ch.steps = steps;
   ch.batch = static_cast<int>(batch);
   ch.out_vec = n % 8 == 0 && !misaligned(out, 16);

@@ -326,6 +326,7 @@ struct OrthChain {
   int steps, batch;
   int own;      // each matrix is worked by one CTA pair alone
   int out_vec;  // the result's rows start on 16-byte boundaries
+  int resident;  // X's tiles stay in tensor memory between the steps
   int m, n, k, ldx, ldk;
   __half *hi[2], *lo, *mat[2];  // mat: R, R_B
   float* diag[2];               // D, D_B: [batch][k]

@@ -204,6 +204,9 @@ __global__ void __launch_bounds__(kPrepThreads) orth_scale(const OrthPrep p, int
 // L2 is what bounds these products (about 9.3 TB/s measured over the 74 pairs: 256-column
 // tiles reach 1.2 PFLOP/s).  The next tile's MMAs for the first slot start while the epilogue
 // still drains the second.
+// Where every pair has at most one tile of the update (NSUB = 1; up to 74 tiles of 256 x 256),
+// hi and lo of that tile stay in the second slot from step to step, two fp16 numbers per
+// 32-bit cell: only hi goes to memory, for the products to read.
 // ----------------------------------------------------------------------------------------
 enum OrthOp { kGram = 0, kSquare = 1, kUpdate = 2 };
 constexpr int kOrthWG = 2;
@@ -393,7 +396,8 @@ struct OrthBlock {
 };
 
 // What a block's epilogue reads, fetched a block ahead (behind the MMAs, or the block before).
-template <int OP, bool TALL>
+// FROM: hi and lo of the update come from tensor memory instead.
+template <int OP, bool TALL, bool FROM>
 struct OrthIn {
   static constexpr bool kCols = OP == kSquare || (OP == kUpdate && TALL);  // D of the columns
   OrthBlock hi, lo;  // kSquare: R in hi
@@ -401,8 +405,10 @@ struct OrthIn {
   __device__ __forceinline__ void fetch(const OrthView& g, int z, int row0, int col, int lane) {
     if (OP == kGram) return;
     const int64_t base = static_cast<int64_t>(z) * g.rows * g.ld;
-    hi.load(g.in + base, g.ld, row0, col, g.rows, g.cols, lane);
-    if (OP == kUpdate) lo.load(g.lo + base, g.ld, row0, col, g.rows, g.cols, lane);
+    if (OP == kSquare || !FROM) {
+      hi.load(g.in + base, g.ld, row0, col, g.rows, g.cols, lane);
+      if (OP == kUpdate) lo.load(g.lo + base, g.ld, row0, col, g.rows, g.cols, lane);
+    }
     if (kCols)
       dcol = col + lane < g.cols ? g.diag_in[static_cast<int64_t>(z) * g.diag_n + col + lane] : 0.f;
   }
@@ -411,19 +417,35 @@ struct OrthIn {
 // One warp's block of product OP: v holds this lane's row `row`, columns [col, col + 32) of the
 // accumulator of matrix z.  (Bulk stores from the staging measured slower: a block waited about
 // 0.7 us for the one before to be read.)
-template <int OP, bool LAST, bool TALL>
+// FROM, TO: hi and lo of the update's tile are read from / left in tensor memory at `master`.
+template <int OP, bool LAST, bool TALL, bool FROM, bool TO>
 __device__ __forceinline__ void orth_epilogue(const OrthView& g, uint4* stage, int z, int row,
                                               int col, int next_col, bool mirror, float drow,
-                                              OrthIn<OP, TALL>& in, float (&v)[32]) {
-  constexpr bool kCols = OrthIn<OP, TALL>::kCols;
+                                              OrthIn<OP, TALL, FROM>& in, uint32_t master,
+                                              float (&v)[32]) {
+  constexpr bool kCols = OrthIn<OP, TALL, FROM>::kCols;
   const int lane = threadIdx.x & 31;
   const int row0 = row - lane;
   const int64_t base = static_cast<int64_t>(z) * g.rows * g.ld;
   uint32_t hi[16], lo[16];
   OrthBlock blk;
   if (OP != kGram) {
-    in.hi.to_rows(stage, lane, hi);
-    if (OP == kUpdate) in.lo.to_rows(stage, lane, lo);
+    if (FROM) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t w[16];
+        tmem_ld16_raw(master + 16 * half, w);
+        tmem_ld_wait();
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+          hi[8 * half + h] = __byte_perm(w[2 * h], w[2 * h + 1], 0x5410);
+          lo[8 * half + h] = __byte_perm(w[2 * h], w[2 * h + 1], 0x7632);
+        }
+      }
+    } else {
+      in.hi.to_rows(stage, lane, hi);
+      if (OP == kUpdate) in.lo.to_rows(stage, lane, lo);
+    }
     if (kCols) {
       reinterpret_cast<float*>(stage)[lane] = in.dcol;
       __syncwarp();
@@ -496,8 +518,22 @@ __device__ __forceinline__ void orth_epilogue(const OrthView& g, uint4* stage, i
   blk.from_rows(stage, lane, hi, OP != kUpdate && row0 == col);
   blk.store(out, out_ld, row0, col, g.rows, g.cols, lane);
   if (OP == kUpdate && !LAST) {
-    blk.from_rows(stage, lane, lo);
-    blk.store(g.lo + base, g.ld, row0, col, g.rows, g.cols, lane);
+    if (TO) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t w[16];
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+          w[2 * h] = __byte_perm(hi[8 * half + h], lo[8 * half + h], 0x5410);
+          w[2 * h + 1] = __byte_perm(hi[8 * half + h], lo[8 * half + h], 0x7632);
+        }
+        tmem_st16_raw(master + 16 * half, w);
+      }
+      tmem_st_wait();
+    } else {
+      blk.from_rows(stage, lane, lo);
+      blk.store(g.lo + base, g.ld, row0, col, g.rows, g.cols, lane);
+    }
   }
   if (OP != kUpdate && mirror) {
     // The transpose: column c of the block as row c, a lane per element.
@@ -699,7 +735,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         for (int u = u0; u < u1; u += stride, ++t) {
           int z, i, j, nsub;
           orth_unit<BNI, NSUB, OP != kUpdate>(g, u, z, i, j, nsub);
-          const int b0 = NSUB == 2 ? 0 : static_cast<int>(t & 1u);
+          const int b0 = NSUB == 2 || ch.resident ? 0 : static_cast<int>(t & 1u);
           uint32_t& used = b0 ? used1 : used0;
           ok = wait_warp(&pc->tempty[b0], (used & 1u) ^ 1u, abort, ctl);
           if (!ok) return;
@@ -774,9 +810,10 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     const uint32_t tempty1 = mapa_shared(smem_u32(&pc->tempty[1]), 0);
     uint32_t t = 0, used0 = 0, used1 = 0;
     bool ok = true;
-    auto product = [&](auto opc, auto lastc, int step, int set) {
+    auto product = [&](auto opc, auto lastc, auto fromc, auto toc, int step, int set) {
       constexpr int OP = decltype(opc)::value;
       constexpr bool LAST = decltype(lastc)::value;
+      constexpr bool FROM = decltype(fromc)::value, TO = decltype(toc)::value;
       constexpr bool kSym = OP != kUpdate;
       const OrthGeom& geo = ch.geom[OP];
       const int cur = step & 1;
@@ -801,11 +838,11 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         if (OP == kSquare || (OP == kUpdate && !TALL))
           if (row < g.rows) drow = g.diag_in[static_cast<int64_t>(z) * g.diag_n + row];
         for (int h = 0; h < nsub; ++h) {
-          const int b = NSUB == 2 ? h : static_cast<int>(t & 1u);
+          const int b = NSUB == 2 ? h : ch.resident ? 0 : static_cast<int>(t & 1u);
           uint32_t& used = b ? used1 : used0;
           const int col0 = j * C::kTileN + h * BNI + wg * kShare;
           const bool mirror = kSym && col0 - wg * kShare + BNI <= i * 2 * kBM;
-          OrthIn<OP, TALL> in;
+          OrthIn<OP, TALL, FROM> in;
           in.fetch(g, z, row - lane, col0, lane);
           if (!wait_warp(&pc->tfull[b], used & 1u, abort, ctl)) {
             ok = false;
@@ -827,9 +864,10 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
                 mbar_arrive_cluster(b ? tempty1 : tempty0);
             }
             if (col0 + c * 32 < g.cols)
-              orth_epilogue<OP, LAST, TALL>(g, stage, z, row, col0 + c * 32,
+              orth_epilogue<OP, LAST, TALL, FROM, TO>(g, stage, z, row, col0 + c * 32,
                                             c + 1 < kChunks ? col0 + (c + 1) * 32 : -1, mirror,
-                                            drow, in, v);
+                                            drow, in,
+                                            tmem + lane_bits + BNI + wg * kShare + c * 32, v);
           }
         }
       }
@@ -840,14 +878,26 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         if (p > 0 || q > 0) ok = wait_warp(&pc->met, met++ & 1, abort, ctl);
         if (!ok) break;
         const int step = p / 3;
-        if (p % 3 == 0)
-          product(std::integral_constant<int, kGram>{}, std::false_type{}, step, q);
-        else if (p % 3 == 1)
-          product(std::integral_constant<int, kSquare>{}, std::false_type{}, step, q);
-        else if (step + 1 < ch.steps)
-          product(std::integral_constant<int, kUpdate>{}, std::false_type{}, step, q);
-        else
-          product(std::integral_constant<int, kUpdate>{}, std::true_type{}, step, q);
+        constexpr std::false_type no{};
+        constexpr std::true_type yes{};
+        constexpr std::integral_constant<int, kUpdate> up{};
+        const bool last = step + 1 == ch.steps;
+        if (p % 3 == 0) {
+          product(std::integral_constant<int, kGram>{}, no, no, no, step, q);
+        } else if (p % 3 == 1) {
+          product(std::integral_constant<int, kSquare>{}, no, no, no, step, q);
+        } else if (NSUB == 1 && ch.resident) {
+          if (step == 0)
+            product(up, no, no, yes, step, q);
+          else if (!last)
+            product(up, no, yes, yes, step, q);
+          else
+            product(up, yes, yes, no, step, q);
+        } else if (!last) {
+          product(up, no, no, no, step, q);
+        } else {
+          product(up, yes, no, no, step, q);
+        }
         if (!ok) break;
         // This warp's part of the product, stored by plain stores and loaded by bulk copies,
         // becomes visible in order by the arrival, which the loading warp passes on at the
@@ -902,8 +952,11 @@ cudaError_t launch_chain(const OrthChain& ch, const OrthMaps& maps, const DevCtl
   cfg.numAttrs = 2;
   int pairs = 1;
   for (const OrthGeom& g : ch.geom) pairs = std::max(pairs, ch.own ? ch.batch : g.num_units);
-  cfg.gridDim = dim3(2 * std::min(pairs, max_clusters[dev]), 1, 1);
-  return cudaLaunchKernelEx(&cfg, kern, ch, maps, c);
+  pairs = std::min(pairs, max_clusters[dev]);
+  cfg.gridDim = dim3(2 * pairs, 1, 1);
+  OrthChain co = ch;
+  co.resident = ch.resident && (ch.own || ch.geom[kUpdate].num_units <= pairs);
+  return cudaLaunchKernelEx(&cfg, kern, co, maps, c);
 }
 
 }  // namespace
