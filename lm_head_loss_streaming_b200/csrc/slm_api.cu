@@ -527,9 +527,9 @@ bool make_map_stack(CUtensorMap* m, const void* base, int64_t inner, int64_t out
 // seconds, the CTAs' meeting after it included.  Per 64-wide K block a tile takes its MMAs
 // (27 TFLOP/s per pair; two thirds of that at 128 columns) or its operands' way from L2 (9.3 TB/s
 // shared by the pairs that are busy), whichever is longer; the rates as measured on the products
-// of 4096 x 4096 matrices.  A round of tiles also costs its epilogue, about 1 us per 128 columns.  `own`: one pair works all tiles of a matrix.
-double orth_tiles(OrthGeom* g, int bn, bool own, int64_t rows, int64_t cols, int64_t k,
-                  int64_t batch, bool sym) {
+// of 4096 x 4096 matrices.  A round of tiles also costs its epilogue, about 1 us per 128 columns.
+double orth_tiles(OrthGeom* g, int bn, int64_t rows, int64_t cols, int64_t k, int64_t batch,
+                  bool sym) {
   const int64_t pairs = std::max(1, sm_count() / 2);
   const int64_t nm = ceil_div(rows, kPairM), nn = ceil_div(cols, bn);
   // Symmetric: the tiles that reach below the diagonal.
@@ -546,35 +546,31 @@ double orth_tiles(OrthGeom* g, int bn, bool own, int64_t rows, int64_t cols, int
     const double l2 = (kPairM + bn) * kBK * 2.0 * static_cast<double>(busy) / 9.3e12;
     return g->k_blocks * std::max(mma, l2) + 1e-6 * bn / 128;
   };
-  if (own) {
-    const int64_t busy = std::min(batch, pairs);
-    return static_cast<double>(ceil_div(batch, pairs)) * (per * round(busy) + 2e-6);
-  }
   return static_cast<double>(units / pairs) * round(pairs) +
          (units % pairs != 0 ? round(units % pairs) : 0.0) + 4e-6;
 }
 
-// The tile grids of a step's three products, their tiles' width, and whether a pair works each
-// matrix alone: of the six ways the one that is estimated to take least.  Wide tiles read less
-// from L2 per flop, narrow ones leave fewer pairs idle: the update of a 4096 x 4096 matrix took
-// 178 us at 128 columns and 125 at 512, the products of a 2048 x 2048 one run on half of the
-// pairs at 512.
+// The tile grids of a step's three products and their tiles' width: of 512, 256 and 128 columns
+// the one whose rounds are estimated to take least.  Wide tiles read less from L2 per flop,
+// narrow ones leave fewer pairs idle and have shorter epilogues.  Whole calls measured at 128 /
+// 256 / 512 columns: 256 x 256 101 / 123 / 152 us, 1024 x 1024 174 / 206 / 367, 2048 x 2048
+// 332 / 296 / 516; the update alone of a 4096 x 4096 matrix 178 us at 128 and 125 at 512.  (A pair
+// working each matrix of a stack by itself, without the launch's meetings, was slower but for a
+// single 64 x 64 matrix, 68 us against 72.)
 int orth_plan(OrthChain* ch, int64_t m, int64_t n, int64_t batch) {
   const int64_t k = std::min(m, n), l = std::max(m, n);
   int best = 0;
   double best_cost = 0;
-  for (int own = 0; own < 2; ++own)
-    for (int bn : {512, 256, 128}) {
-      OrthGeom g[3];
-      const double cost = orth_tiles(&g[0], bn, own, k, k, l, batch, true) +
-                          orth_tiles(&g[1], bn, own, k, k, k, batch, true) +
-                          orth_tiles(&g[2], bn, own, m, n, k, batch, false);
-      if (best != 0 && cost >= best_cost) continue;
-      best = bn;
-      best_cost = cost;
-      ch->own = own;
-      std::copy(g, g + 3, ch->geom);
-    }
+  for (int bn : {512, 256, 128}) {
+    OrthGeom g[3];
+    const double cost = orth_tiles(&g[0], bn, k, k, l, batch, true) +
+                        orth_tiles(&g[1], bn, k, k, k, batch, true) +
+                        orth_tiles(&g[2], bn, m, n, k, batch, false);
+    if (best != 0 && cost >= best_cost) continue;
+    best = bn;
+    best_cost = cost;
+    std::copy(g, g + 3, ch->geom);
+  }
   return best;
 }
 
@@ -1270,10 +1266,8 @@ int slm_orthogonalize(int dtype, const void* grad, int64_t ld, int64_t batch_str
   OrthChain ch{};
   const int bn = orth_plan(&ch, m, n, batch);
   // At most one tile of the update per pair, and a second accumulator slot free for it.
-  ch.resident = bn <= 256 && steps > 1 &&
-                (ch.own ? ch.geom[2].units_per == 1 : ch.geom[2].num_units <= sm_count() / 2);
+  ch.resident = bn <= 256 && steps > 1 && ch.geom[2].num_units <= sm_count() / 2;
   ch.steps = steps;
-  ch.batch = static_cast<int>(batch);
   ch.out_vec = n % 8 == 0 && !misaligned(out, 16);
   ch.m = static_cast<int>(m);
   ch.n = static_cast<int>(n);

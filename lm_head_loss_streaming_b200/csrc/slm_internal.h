@@ -323,9 +323,8 @@ struct OrthGeom {
 };
 struct OrthChain {
   OrthGeom geom[3];
-  int steps, batch;
-  int own;      // each matrix is worked by one CTA pair alone
-  int out_vec;  // the result's rows start on 16-byte boundaries
+  int steps;
+  int out_vec;   // the result's rows start on 16-byte boundaries
   int resident;  // X's tiles stay in tensor memory between the steps
   int m, n, k, ldx, ldk;
   __half *hi[2], *lo, *mat[2];  // mat: R, R_B

@@ -223,26 +223,6 @@ __device__ __forceinline__ void red_release_add_s32(int* p, int v) {
 __device__ __forceinline__ void fence_proxy_async_global() {
   asm volatile("fence.proxy.async.global;" ::: "memory");
 }
-// Waits (boundedly) until both CTAs of the pair have arrived; what they wrote is then visible to
-// this warp's loads and bulk copies.
-__device__ __forceinline__ bool wait_both(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                          const DevCtl& ctl) {
-  const uint32_t a = smem_u32(bar);
-  bool done = mbar_try_wait_cluster(a, parity);
-  if (!done) {
-    const long long t0 = clock64();
-    while (!(done = mbar_try_wait_cluster(a, parity))) {
-      if (*abort) break;
-      if (clock64() - t0 > ctl.timeout_cycles) {
-        *abort = 1;
-        atomicOr(ctl.status, kFlagTimeout);
-        break;
-      }
-    }
-  }
-  fence_proxy_async_global();
-  return __all_sync(0xffffffffu, done);
-}
 // Waits (boundedly; lane 0 polls) until `target` arrivals are counted; what the arriving CTAs
 // wrote is then visible to this thread's loads and bulk copies.
 __device__ __forceinline__ bool wait_met(const int* counter, int target, volatile int* abort,
@@ -277,7 +257,7 @@ __device__ __forceinline__ int stage_piece(int row, int k) {
 
 template <int STAGES>
 struct OrthCtl {
-  uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], fin, met, done, both;
+  uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], fin, met, done;
   uint32_t tmem_base;
   int abort;
 };
@@ -578,7 +558,6 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     mbar_init(&pc->fin, 1);
     mbar_init(&pc->met, 1);
     mbar_init(&pc->done, 4 * kOrthWG);
-    mbar_init(&pc->both, 2);
     pc->abort = 0;
     fence_barrier_init();
   }
@@ -591,32 +570,20 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   tc_fence_after();
   const uint32_t tmem = pc->tmem_base;
   volatile int* abort = &pc->abort;
-  // A matrix's products need one another's results.  Where the pair works a matrix alone
-  // (ch.own), its two CTAs meet; otherwise every CTA of the launch does, all matrices at once.
   const int products = 3 * ch.steps;
-  const int sets = ch.own ? (ch.batch - pair + npairs - 1) / npairs : 1;
-  // Units u0, u0 + stride, .. below u1 of product `op` in set q.
-  auto units = [&](int op, int q, int& u0, int& u1, int& stride) {
-    const OrthGeom& g = ch.geom[op];
-    u0 = ch.own ? (pair + q * npairs) * g.units_per : pair;
-    u1 = ch.own ? u0 + g.units_per : g.num_units;
-    stride = ch.own ? 1 : npairs;
-  };
 
   if (warp == 0) {
     // TMA producer (both CTAs); both CTAs' copies complete on the leader's "full" barrier.
     uint32_t it = 0;
     bool ok = true;
-    auto product = [&](auto opc, int cur, int set) {
+    auto product = [&](auto opc, int cur) {
       constexpr int OP = decltype(opc)::value;
       constexpr bool A_MN = TALL && OP == kGram;
       constexpr bool B_MN = (TALL && OP == kGram) || (!TALL && OP == kUpdate);
       const OrthGeom& g = ch.geom[OP];
       const CUtensorMap* ma = &maps.a[OP][cur];
       const CUtensorMap* mb = &maps.b[OP][cur];
-      int u0, u1, stride;
-      units(OP, set, u0, u1, stride);
-      for (int u = u0; ok && u < u1; u += stride) {
+      for (int u = pair; ok && u < g.num_units; u += npairs) {
         int z, i, j, nsub;
         orth_unit<BNI, NSUB, OP != kUpdate>(g, u, z, i, j, nsub);
         const int mrow = i * 2 * kBM + static_cast<int>(rank) * kBM;
@@ -655,40 +622,28 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         }
       }
     };
-    const uint32_t both_own = mapa_shared(smem_u32(&pc->both), rank);
-    const uint32_t both_peer = mapa_shared(smem_u32(&pc->both), rank ^ 1);
-    int met = 0;  // products begun, less one
-    for (int q = 0; ok && q < sets; ++q)
-      for (int p = 0; ok && p < products; ++p) {
-        if (p > 0 || q > 0) {
-          // This CTA's part of the product before is in memory; wait for the others' and let
-          // the epilogue know.
-          ok = wait_warp(&pc->done, met & 1, abort, ctl);
-          if (ok && ch.own) {
-            if (lane == 0) {
-              mbar_arrive_cluster(both_own);
-              mbar_arrive_cluster(both_peer);
-            }
-            __syncwarp();
-            ok = wait_both(&pc->both, met & 1, abort, ctl);
-          } else if (ok) {
-            if (lane == 0) red_release_add_s32(ch.counter, 1);
-            __syncwarp();
-            ok = wait_met(ch.counter, (met + 1) * static_cast<int>(gridDim.x), abort, ctl);
-          }
-          ++met;
-          if (lane == 0) mbar_arrive(&pc->met);
+    for (int p = 0; ok && p < products; ++p) {
+      if (p > 0) {
+        // This CTA's part of the product before is in memory; wait for the others' and let the
+        // epilogue know.
+        ok = wait_warp(&pc->done, (p - 1) & 1, abort, ctl);
+        if (ok) {
+          if (lane == 0) red_release_add_s32(ch.counter, 1);
           __syncwarp();
-          if (!ok) break;
+          ok = wait_met(ch.counter, p * static_cast<int>(gridDim.x), abort, ctl);
         }
-        const int cur = (p / 3) & 1;
-        if (p % 3 == 0)
-          product(std::integral_constant<int, kGram>{}, cur, q);
-        else if (p % 3 == 1)
-          product(std::integral_constant<int, kSquare>{}, 0, q);
-        else
-          product(std::integral_constant<int, kUpdate>{}, cur, q);
+        if (lane == 0) mbar_arrive(&pc->met);
+        __syncwarp();
+        if (!ok) break;
       }
+      const int cur = (p / 3) & 1;
+      if (p % 3 == 0)
+        product(std::integral_constant<int, kGram>{}, cur);
+      else if (p % 3 == 1)
+        product(std::integral_constant<int, kSquare>{}, 0);
+      else
+        product(std::integral_constant<int, kUpdate>{}, cur);
+    }
     if (ok) {
       // No remote release of a stage may reach this CTA after it has exited: wait for the
       // releases of the last stages.
@@ -711,7 +666,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     if (leader) {
       uint32_t it = 0, t = 0, used0 = 0, used1 = 0;
       bool ok = true;
-      auto product = [&](auto opc, int set) {
+      auto product = [&](auto opc) {
         constexpr int OP = decltype(opc)::value;
         constexpr bool A_MN = TALL && OP == kGram;
         constexpr bool B_MN = (TALL && OP == kGram) || (!TALL && OP == kUpdate);
@@ -730,9 +685,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
             umma_bf16_pair(tmem + b * BNI, ad, bd, kIdesc, (!first || kk != 0) ? 1u : 0u);
           }
         };
-        int u0, u1, stride;
-        units(OP, set, u0, u1, stride);
-        for (int u = u0; u < u1; u += stride, ++t) {
+        for (int u = pair; u < g.num_units; u += npairs, ++t) {
           int z, i, j, nsub;
           orth_unit<BNI, NSUB, OP != kUpdate>(g, u, z, i, j, nsub);
           const int b0 = NSUB == 2 || ch.resident ? 0 : static_cast<int>(t & 1u);
@@ -785,15 +738,14 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
           __syncwarp();
         }
       };
-      for (int q = 0; ok && q < sets; ++q)
-        for (int p = 0; ok && p < products; ++p) {
-          if (p % 3 == 0)
-            product(std::integral_constant<int, kGram>{}, q);
-          else if (p % 3 == 1)
-            product(std::integral_constant<int, kSquare>{}, q);
-          else
-            product(std::integral_constant<int, kUpdate>{}, q);
-        }
+      for (int p = 0; ok && p < products; ++p) {
+        if (p % 3 == 0)
+          product(std::integral_constant<int, kGram>{});
+        else if (p % 3 == 1)
+          product(std::integral_constant<int, kSquare>{});
+        else
+          product(std::integral_constant<int, kUpdate>{});
+      }
       // Every MMA must be complete (in both CTAs' TMEM) before TMEM is released.
       if (lane == 0) umma_commit_pair_mc(&pc->fin, 0x1);
       __syncwarp();
@@ -810,7 +762,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     const uint32_t tempty1 = mapa_shared(smem_u32(&pc->tempty[1]), 0);
     uint32_t t = 0, used0 = 0, used1 = 0;
     bool ok = true;
-    auto product = [&](auto opc, auto lastc, auto fromc, auto toc, int step, int set) {
+    auto product = [&](auto opc, auto lastc, auto fromc, auto toc, int step) {
       constexpr int OP = decltype(opc)::value;
       constexpr bool LAST = decltype(lastc)::value;
       constexpr bool FROM = decltype(fromc)::value, TO = decltype(toc)::value;
@@ -828,9 +780,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
                                        : static_cast<void*>(ch.hi[cur ^ 1]),
                        ch.co[step][0],
                        ch.co[step][1], ch.co[step][2], ch.out_vec};
-      int u0, u1, stride;
-      units(OP, set, u0, u1, stride);
-      for (int u = u0; ok && u < u1; u += stride, ++t) {
+      for (int u = pair; ok && u < geo.num_units; u += npairs, ++t) {
         int z, i, j, nsub;
         orth_unit<BNI, NSUB, kSym>(geo, u, z, i, j, nsub);
         const int row = i * 2 * kBM + static_cast<int>(rank) * kBM + q * 32 + lane;
@@ -872,40 +822,38 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         }
       }
     };
-    int met = 0;
-    for (int q = 0; ok && q < sets; ++q)
-      for (int p = 0; ok && p < products; ++p) {
-        if (p > 0 || q > 0) ok = wait_warp(&pc->met, met++ & 1, abort, ctl);
-        if (!ok) break;
-        const int step = p / 3;
-        constexpr std::false_type no{};
-        constexpr std::true_type yes{};
-        constexpr std::integral_constant<int, kUpdate> up{};
-        const bool last = step + 1 == ch.steps;
-        if (p % 3 == 0) {
-          product(std::integral_constant<int, kGram>{}, no, no, no, step, q);
-        } else if (p % 3 == 1) {
-          product(std::integral_constant<int, kSquare>{}, no, no, no, step, q);
-        } else if (NSUB == 1 && ch.resident) {
-          if (step == 0)
-            product(up, no, no, yes, step, q);
-          else if (!last)
-            product(up, no, yes, yes, step, q);
-          else
-            product(up, yes, yes, no, step, q);
-        } else if (!last) {
-          product(up, no, no, no, step, q);
-        } else {
-          product(up, yes, no, no, step, q);
-        }
-        if (!ok) break;
-        // This warp's part of the product, stored by plain stores and loaded by bulk copies,
-        // becomes visible in order by the arrival, which the loading warp passes on at the
-        // meeting's scope.
-        fence_proxy_async_global();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pc->done);
+    for (int p = 0; ok && p < products; ++p) {
+      if (p > 0) ok = wait_warp(&pc->met, (p - 1) & 1, abort, ctl);
+      if (!ok) break;
+      const int step = p / 3;
+      constexpr std::false_type no{};
+      constexpr std::true_type yes{};
+      constexpr std::integral_constant<int, kUpdate> up{};
+      const bool last = step + 1 == ch.steps;
+      if (p % 3 == 0) {
+        product(std::integral_constant<int, kGram>{}, no, no, no, step);
+      } else if (p % 3 == 1) {
+        product(std::integral_constant<int, kSquare>{}, no, no, no, step);
+      } else if (NSUB == 1 && ch.resident) {
+        if (step == 0)
+          product(up, no, no, yes, step);
+        else if (!last)
+          product(up, no, yes, yes, step);
+        else
+          product(up, yes, yes, no, step);
+      } else if (!last) {
+        product(up, no, no, no, step);
+      } else {
+        product(up, yes, no, no, step);
       }
+      if (!ok) break;
+      // This warp's part of the product, stored by plain stores and loaded by bulk copies,
+      // becomes visible in order by the arrival, which the loading warp passes on at the
+      // meeting's scope.
+      fence_proxy_async_global();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pc->done);
+    }
   }
 
   // Neither CTA leaves while the other may still signal its barriers or use its TMEM.
@@ -951,11 +899,11 @@ cudaError_t launch_chain(const OrthChain& ch, const OrthMaps& maps, const DevCtl
   }
   cfg.numAttrs = 2;
   int pairs = 1;
-  for (const OrthGeom& g : ch.geom) pairs = std::max(pairs, ch.own ? ch.batch : g.num_units);
+  for (const OrthGeom& g : ch.geom) pairs = std::max(pairs, g.num_units);
   pairs = std::min(pairs, max_clusters[dev]);
   cfg.gridDim = dim3(2 * pairs, 1, 1);
   OrthChain co = ch;
-  co.resident = ch.resident && (ch.own || ch.geom[kUpdate].num_units <= pairs);
+  co.resident = ch.resident && ch.geom[kUpdate].num_units <= pairs;
   return cudaLaunchKernelEx(&cfg, kern, co, maps, c);
 }
 
