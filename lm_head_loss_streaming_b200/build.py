@@ -28,7 +28,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libslm.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
-SOURCES = ["slm_api.cu", "slm_kernels.cu", "slm_noalloc.cu", "slm_norm.cu", "slm_orth.cu"]
+SOURCES = ["slm_api.cu", "slm_kernels.cu", "slm_noalloc.cu", "slm_norm.cu", "slm_norm_bf16.cu",
+           "slm_norm_f16.cu", "slm_norm_f32.cu", "slm_orth.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--use_fast_math", "-Xcompiler", "-fPIC",
          "-Xcompiler", "-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC]

@@ -415,13 +415,15 @@ NormLayout norm_layout(int64_t N, int64_t d, int64_t gate_rows) {
   NormLayout L{};
   const NormPlan q = norm_plan(std::max<int64_t>(N, 1), gate_rows > 0 ? N / gate_rows : 1,
                                gate_rows > 0);
-  const size_t part = align_up(static_cast<size_t>(q.blocks) * d * sizeof(float), kAlign);
+  // No more partials than rows and, of each group, row classes (see norm_plan).
+  const int64_t blocks = std::min<int64_t>(kNormBlocks, N + 8 * q.groups);
+  const size_t part = align_up(static_cast<size_t>(blocks) * d * sizeof(float), kAlign);
   L.status_off = 0;
   L.c1_off = kAlign;
   L.post_off = align_up(L.c1_off + static_cast<size_t>(N) * sizeof(float), kAlign);
   L.pre_off = L.post_off + part;
   L.gate_off = L.pre_off + part;
-  L.total = L.gate_off + (q.shared_gate && q.slices > 1 ? part : 0) + kAlign;
+  L.total = L.gate_off + (q.shared_gate ? part : 0) + kAlign;
   return L;
 }
 

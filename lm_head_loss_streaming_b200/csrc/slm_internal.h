@@ -238,29 +238,37 @@ cudaError_t launch_finalize(const double* blk_sum, const long long* blk_cnt, int
 cudaError_t launch_zero_f32(float* p, int64_t n, cudaStream_t s);
 
 // ---- Block norm (slm_norm.cu): element types 0 = bf16, 1 = fp16, 2 = fp32. ----
-// How the rows of a backward are divided: blocks own either one of `slices` slices of one
-// group (rows that share a gate row; everything is one group without a shared gate), or, when
-// there are at least as many groups as blocks, several whole groups.
-constexpr int kNormBlocks = 296;
+// How the rows of a backward are divided: blocks own either one part of one group (rows that
+// share a gate row; everything is one group without a shared gate), or, when there are at least
+// as many groups as blocks, several whole groups.  A group's parts are its `slices` slices
+// times `classes`: the rows n = class (mod classes) of a slice.
+constexpr int kNormBlocks = 592;
 struct NormPlan {
   int64_t rows;    // rows per group
   int64_t groups;
-  int slices;      // slices per group
+  int slices, classes;
   int blocks;
   bool shared_gate;
+  __host__ __device__ int parts() const { return slices * classes; }
 };
 struct NormRows {
   int64_t g0, g1, rows;
-  int64_t lo, hi;  // rows of each group that the block owns
-  __host__ __device__ int64_t begin(int64_t g) const { return g * rows + lo; }
+  int64_t lo, hi;  // rows of each group that the block owns, of them those of its class
+  int cls, classes;
+  __host__ __device__ int64_t begin(int64_t g) const {
+    const int64_t n = g * rows + lo;
+    return n + (cls - n % classes + classes) % classes;
+  }
   __host__ __device__ int64_t end(int64_t g) const { return g * rows + hi; }
 };
 __host__ __device__ inline NormRows norm_rows(const NormPlan& q, int b) {
   NormRows r;
   r.rows = q.rows;
-  if (q.slices > 1) {
-    const int s = b % q.slices;
-    r.g0 = b / q.slices;
+  r.classes = q.classes;
+  r.cls = b % q.classes;
+  if (q.parts() > 1) {
+    const int s = b / q.classes % q.slices;
+    r.g0 = b / q.parts();
     r.g1 = r.g0 + 1;
     r.lo = q.rows * s / q.slices;
     r.hi = q.rows * (s + 1) / q.slices;
@@ -275,7 +283,7 @@ __host__ __device__ inline NormRows norm_rows(const NormPlan& q, int b) {
 // Plan for N >= 1 rows; rows_per_gate = 1 is a gate of its own for each row (not shared).
 // (`max_blocks` row workers at most, which take `batch` rows at a time).
 NormPlan norm_plan(int64_t N, int64_t rows_per_gate, bool has_gate, int max_blocks = kNormBlocks,
-                   int batch = 1);
+                   int batch = 1, int classes = 1);
 
 struct NormFwd {
   const void *x, *y, *w_post, *w_pre, *gate;
@@ -285,6 +293,7 @@ struct NormFwd {
   float residual_scale, block_scale, eps, weight_offset;
   void *residual, *hidden;      // contiguous rows
   float *rstd_post, *rstd_pre;  // [N]; may be NULL
+  int shift0;  // elements from a 16-byte boundary to the first row
 };
 struct NormBwd {
   const void *x, *y, *w_post, *w_pre, *gate, *d_residual, *d_hidden;
@@ -298,6 +307,7 @@ struct NormBwd {
   NormPlan plan;
   float* c1;                               // [N]
   float *part_post, *part_pre, *part_gate;  // [plan.blocks][d] each
+  int shift0;  // elements from a 16-byte boundary to the first row
 };
 cudaError_t launch_norm_fwd(int dtype, const NormFwd& p, cudaStream_t s);
 cudaError_t launch_norm_bwd(int dtype, const NormBwd& p, const DevCtl& c, cudaStream_t s);

@@ -153,7 +153,8 @@ def run_case(t, dr, dh, rs=0.75, bs=1.25, eps=1e-6, o=0.0, views=None):
 # Widths: one channel, below and above a warp, odd, whole 16-byte pieces, several pieces per
 # thread, more than one block of threads per row; rows: one, few, ragged.
 SHAPES = [(1, 1), (3, 7), (2, 64), (5, 100), (130, 256), (37, 1001), (1, 4096), (70, 2048),
-          (33, 4096), (301, 520), (9, 8192), (17, 16384), (3, 16392), (2, 40000), (5, 33001)]
+          (33, 4096), (301, 520), (9, 8192), (17, 16384), (3, 16392), (2, 40000), (5, 33001), (1, 1001), (40, 5001), (21, 16387),
+          (1700, 515), (700, 2049), (9, 9999)]
 
 
 @pytest.mark.parametrize("dtype", [BF, HF, F32])
@@ -167,7 +168,7 @@ def test_all_parts(shape, dtype):
 @pytest.mark.parametrize("post", [False, True])
 @pytest.mark.parametrize("pre", [False, True])
 @pytest.mark.parametrize("gate_rows", [0, 1, 6, 30, 60])
-@pytest.mark.parametrize("d", [96, 101, 4096])
+@pytest.mark.parametrize("d", [96, 101, 1540, 4096, 4097])
 def test_parts_and_gates(post, pre, gate_rows, d):
     t, dr, dh = make(60, d, BF, F32, gate_rows, F32 if gate_rows == 6 else BF, post, pre, seed=d)
     run_case(t, dr, dh, o=1.0 if gate_rows == 6 else 0.0)
@@ -176,8 +177,34 @@ def test_parts_and_gates(post, pre, gate_rows, d):
 @pytest.mark.parametrize("N,gate_rows", [(1000, 500), (1200, 2), (900, 300), (2048, 1),
                                          (1184, 37)])
 def test_shared_gate_slices(N, gate_rows):
-    t, dr, dh = make(N, 72, HF, gate_rows=gate_rows, seed=N)
-    run_case(t, dr, dh)
+    for d in (72, 77, 2052):
+        t, dr, dh = make(N, d, HF, gate_rows=gate_rows, seed=N)
+        run_case(t, dr, dh)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 1000), (HF, 2057), (F32, 515), (BF, 6000)])
+@pytest.mark.parametrize("start", [1, 3, 8])
+def test_views_that_start_between_pieces(dtype, d, start):
+    """Every array begins `start` elements into its buffer, the rows end to end from there, with
+    neighbours that must be neither read into a row nor written."""
+    N = 23
+    t, dr, dh = make(N, d, dtype, gate_rows=1, seed=d)
+
+    def inner(v):
+        buf = torch.full((N * d + 2 * start,), float("nan"), dtype=dtype, device="cuda")
+        buf[start:start + N * d] = v.reshape(-1)
+        return buf[start:start + N * d].view(N, d)
+
+    u = dict(t, x=inner(t["x"]), y=inner(t["y"]))
+    res, hid = inner(torch.zeros_like(t["x"])), inner(torch.zeros_like(t["x"]))
+    f = block_norm_fwd(u["x"], u["y"], t["w_pre"], t["w_post"], t["gate"], 0.75, 1.25,
+                       residual=res, hidden=hid)
+    b = block_norm_bwd(f, u["x"], u["y"], t["w_pre"], t["w_post"], t["gate"], inner(dr), inner(dh))
+    val, tol = reference(t, dr, dh, 0.75, 1.25, 1e-6, 0.0)
+    check({**f.__dict__, **b.__dict__}, val, tol, ("residual",) + FWD + BWD)
+    for out in (res, hid):
+        whole = torch.as_strided(out, (N * d + 2 * start,), (1,), out.storage_offset() - start)
+        assert whole[:start].isnan().all() and whole[-start:].isnan().all()
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -249,7 +276,8 @@ def test_in_place_residual_and_given_outputs(d):
     assert torch.equal(x, ref.residual) and torch.equal(h, ref.hidden)
 
 
-@pytest.mark.parametrize("N,d,gate_rows", [(700, 1024, 1), (513, 136, 27), (64, 16384, 64)])
+@pytest.mark.parametrize("N,d,gate_rows", [(700, 1024, 1), (513, 136, 27), (64, 16384, 64),
+                                           (700, 1023, 1), (513, 131, 27), (64, 9001, 64)])
 def test_same_bits_each_time(N, d, gate_rows):
     t, dr, dh = make(N, d, BF, gate_rows=gate_rows, seed=3)
     a = run_case(t, dr, dh)

@@ -71,7 +71,7 @@ def test_workspace_sizes():
     # Partials of a bounded number of row blocks, whatever the rows and the groups.
     for gate_rows in (0, 1, 2, 4096, 65536):
         ws = _lib.slm_block_norm_workspace_bytes(65536, 4096, gate_rows)
-        assert 0 < ws <= 65536 * 4 + 3 * 296 * 4096 * 4 + 4096
+        assert 0 < ws <= 65536 * 4 + 3 * 592 * 4096 * 4 + 4096
 
 
 def test_cpu_tensors_and_missing_parts_are_refused():
