@@ -383,13 +383,47 @@ struct Edge {
     else
       row(static_cast<const T*>(p) + at, c, d, v);
   }
+  // Inside the array by two aligned loads and a shift (the same for all lanes: their columns
+  // are whole pieces apart), near its ends element by element.
   template <int K2>
   static __device__ __forceinline__ void row(const T* q, int c, int d, float2 (&v)[K2]) {
+    if (c < 2 * K2 - 1 || c + 4 * K2 > d) {
 #pragma unroll
-    for (int k = 0; k < K2; ++k) {
-      const int a = c + 2 * k;
-      v[k].x = a >= 0 && a < d ? to_f<T>(__ldg(q + a)) : 0.f;
-      v[k].y = a + 1 >= 0 && a + 1 < d ? to_f<T>(__ldg(q + a + 1)) : 0.f;
+      for (int k = 0; k < K2; ++k) {
+        const int a = c + 2 * k;
+        v[k].x = a >= 0 && a < d ? to_f<T>(__ldg(q + a)) : 0.f;
+        v[k].y = a + 1 >= 0 && a + 1 < d ? to_f<T>(__ldg(q + a + 1)) : 0.f;
+      }
+      return;
+    }
+    constexpr int kWords = 2 * K2 * static_cast<int>(sizeof(T)) / 4;  // words of the columns
+    const uintptr_t at = reinterpret_cast<uintptr_t>(q + c);
+    const uint4* from = reinterpret_cast<const uint4*>(at & ~static_cast<uintptr_t>(15));
+    const int off = static_cast<int>(at & 15);
+    uint32_t w[kWords + 4];
+#pragma unroll
+    for (int i = 0; i < kWords / 4 + 1; ++i) {
+      const uint4 u = i < kWords / 4 || off != 0 ? __ldg(from + i) : make_uint4(0, 0, 0, 0);
+      w[4 * i] = u.x;
+      w[4 * i + 1] = u.y;
+      w[4 * i + 2] = u.z;
+      w[4 * i + 3] = u.w;
+    }
+    if (off & 8)
+#pragma unroll
+      for (int i = 0; i < kWords + 2; ++i) w[i] = w[i + 2];
+    if (off & 4)
+#pragma unroll
+      for (int i = 0; i < kWords + 1; ++i) w[i] = w[i + 1];
+    if (sizeof(T) == 2 && (off & 2))
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = __byte_perm(w[i], w[i + 1], 0x5432);
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i) {
+      float2 f[K];
+      Piece<T>::unpack(make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]), f);
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[i * K + k] = f[k];
     }
   }
 };
@@ -565,7 +599,8 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_fwd_vec(const Norm
 //          columns; the copied windows reach into the neighbouring rows, whose elements are
 //          masked
 // ----------------------------------------------------------------------------------------
-constexpr int kRingThreads = 256;  // computing threads
+constexpr int kRingThreads = 256;  // computing threads (more where one row takes more)
+constexpr int kRingMost = 352;     // 11 warps and the copying one: still 168 registers a thread
 constexpr int kRingWarps = kRingThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxStages = 6;
@@ -580,17 +615,18 @@ struct RingCtl {
 
 template <class T, int TPR, int NV, int GATE>
 struct RingCfg {
-  static constexpr int kRows = kRingThreads / TPR;  // rows per batch
+  static constexpr int kThreads = TPR > kRingThreads ? TPR : kRingThreads;
+  static constexpr int kRows = kThreads / TPR;      // rows per batch
   static constexpr int kSeg = TPR * NV * 16;        // bytes of one array's row segment, at most
   static constexpr int kGateSeg = GATE == 0 ? 0 : GATE == 1 ? kSeg : 2 * kSeg;
   static constexpr int kStage = kRows * (4 * kSeg + kGateSeg);
   static constexpr int kCtl = (static_cast<int>(sizeof(RingCtl)) + 127) / 128 * 128;
-  static constexpr int kScratch = kRows > 1 ? kRingThreads * NV * Piece<T>::kElems * 4 : 0;
+  static constexpr int kScratch = kRows > 1 ? kThreads * NV * Piece<T>::kElems * 4 : 0;
   static constexpr int kFit = (232448 - 128 - kCtl - kScratch - kSeg) / kStage;
   static constexpr int kStages = kFit > kMaxStages ? kMaxStages : kFit;
   static constexpr size_t kSmem =
       128 + kCtl + kScratch + kSeg + static_cast<size_t>(kStages) * kStage;
-  static_assert(kStages >= 4, "two batches in use, two under way");
+  static_assert(kStages >= 3, "two batches in use, one under way");
 };
 
 // Three sums over the warp with six shuffles instead of fifteen: the first two steps also deal
@@ -608,11 +644,12 @@ __device__ __forceinline__ float warp_sum3(float v0, float v1, float v2, int lan
 }
 
 template <class T, int TPR, int NV, int GATE, bool CL, bool SHIFT>
-__global__ void __launch_bounds__(kRingThreads + 32, 1)
+__global__ void __launch_bounds__((TPR > kRingThreads ? TPR : kRingThreads) + 32, 1)
     norm_bwd_ring(const NormBwd p, const DevCtl ctl, const int seg) {
   using P = Piece<T>;
   using C = RingCfg<T, TPR, NV, GATE>;
   constexpr int K = P::kPairs, kRows = C::kRows, S = C::kStages;
+  constexpr int kThreads = C::kThreads, kWarps = kThreads / 32;
   static_assert(!CL || TPR == kRingThreads, "a cluster shares one row");
   extern __shared__ uint8_t ring_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ring_raw) + 127) &
@@ -638,12 +675,12 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1)
   // The status word is cleared here, without a launch for it: a wait can only run out long
   // after the first block has started.
   if (blockIdx.x == 0 && threadIdx.x == 0) *ctl.status = 0;
-  for (int i = threadIdx.x; i < C::kSeg / 16; i += kRingThreads + 32)
+  for (int i = threadIdx.x; i < C::kSeg / 16; i += kThreads + 32)
     reinterpret_cast<uint4*>(zeros)[i] = make_uint4(0, 0, 0, 0);
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&rc->full[s], 1);
-      mbar_init(&rc->empty[s], kRingWarps);
+      mbar_init(&rc->empty[s], kWarps);
     }
     for (int s = 0; s < 4; ++s) mbar_init(&rc->sums[s], 1);
     rc->abort = 0;
@@ -654,7 +691,7 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1)
   else
     __syncthreads();
 
-  if (warp == kRingWarps) {
+  if (warp == kWarps) {
     // ------------------------------ copies ------------------------------
     const int arrays = has_y + has_dr + 2 * pre;
     uint32_t it = 0;
@@ -796,7 +833,7 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1)
       for (int k = 0; k < K; ++k) w[k] = shared ? mul2(w[k], bs) : bs;
     };
     auto consumers_sync = [] {
-      asm volatile("bar.sync 1, %0;" ::"n"(kRingThreads) : "memory");
+      asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
     };
     // The column sums of the batch's row lanes, added in a fixed order into lane 0's.
     auto join = [&](float2(&acc)[NV][K]) {
@@ -805,7 +842,7 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1)
       for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int h = 0; h < K / 2; ++h)
-          scratch[(v * (K / 2) + h) * kRingThreads + threadIdx.x] = make_float4(
+          scratch[(v * (K / 2) + h) * kThreads + threadIdx.x] = make_float4(
               acc[v][2 * h].x, acc[v][2 * h].y, acc[v][2 * h + 1].x, acc[v][2 * h + 1].y);
       consumers_sync();
       if (rw == 0)
@@ -814,7 +851,7 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1)
           for (int v = 0; v < NV; ++v)
 #pragma unroll
             for (int h = 0; h < K / 2; ++h) {
-              const float4 f = scratch[(v * (K / 2) + h) * kRingThreads + threadIdx.x + o * TPR];
+              const float4 f = scratch[(v * (K / 2) + h) * kThreads + threadIdx.x + o * TPR];
               acc[v][2 * h] = add2(acc[v][2 * h], make_float2(f.x, f.y));
               acc[v][2 * h + 1] = add2(acc[v][2 * h + 1], make_float2(f.z, f.w));
             }
@@ -1161,7 +1198,7 @@ cudaError_t bwd_ring(NormBwd p, const DevCtl& c, int cs, cudaStream_t s) {
   attr[0].val.clusterDim.x = cs;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(kRingThreads + 32, 1, 1);
+  cfg.blockDim = dim3(C::kThreads + 32, 1, 1);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
   cfg.attrs = attr;
@@ -1197,6 +1234,7 @@ cudaError_t bwd_vec(const NormBwd& p, int64_t nvec, const DevCtl& c, cudaStream_
   if (nvec <= 128) return bwd_ring<T, 64, 2, GATE, false, SHIFT>(p, c, 1, s);
   if (nvec <= 256) return bwd_ring<T, 128, 2, GATE, false, SHIFT>(p, c, 1, s);
   if (nvec <= 512) return bwd_ring<T, 256, 2, GATE, false, SHIFT>(p, c, 1, s);
+  if (nvec <= 2 * kRingMost) return bwd_ring<T, kRingMost, 2, GATE, false, SHIFT>(p, c, 1, s);
   return bwd_ring<T, 256, 2, GATE, true, SHIFT>(p, c, nvec <= 1024 ? 2 : nvec <= 2048 ? 4 : 8, s);
 }
 
