@@ -442,36 +442,35 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 
-// Sum over the TPR threads of a row (a warp, or the whole block), in every one of them.
-template <int TPR>
+// Sum over a row's threads (a warp, or the whole block), in every one of them.
+template <bool WARP>
 __device__ __forceinline__ float row_sum(float v, float* part) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (TPR > 32) {
+  if (!WARP) {
     const int lane = threadIdx.x & 31;
     if (lane == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = lane < TPR / 32 ? part[lane] : 0.f;
+    v = lane < (blockDim.x >> 5) ? part[lane] : 0.f;
 #pragma unroll
-    for (int o = TPR >= 1024 ? 16 : TPR / 64; o > 0; o >>= 1)
-      v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (TPR < 1024) v = __shfl_sync(0xffffffffu, v, 0);
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   }
   return v;
 }
 
 // Forward by 16-byte pieces: each row is read once into the registers
-// of its TPR threads (NV pieces of x and of y each), and r and h are written from there.
-template <class T, int TPR, int NV, bool SHIFT>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_fwd_vec(const NormFwd p) {
+// of its threads (NV pieces of x and of y each), and r and h are written from there.  A row is a
+// block's, as many warps as it has pieces for, or, if short (WARP), one warp's of four.
+template <class T, int NV, bool WARP, bool SHIFT>
+__global__ void __launch_bounds__(WARP ? 128 : NV == 2 ? 512 : 1024) norm_fwd_vec(const NormFwd p) {
   using P = Piece<T>;
   constexpr int K = P::kPairs;
-  constexpr int kRows = TPR < 128 ? 128 / TPR : 1;  // rows per block
-  static_assert(TPR == 32 || TPR >= 128, "a row is a warp's or a block's");
   __shared__ float part[2][32];
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / TPR;
-  const int t = threadIdx.x % TPR;
-  if (kRows > 1 && n >= p.N) return;
+  const int TPR = WARP ? 32 : blockDim.x;  // threads per row
+  const int64_t n =
+      WARP ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5) : static_cast<int64_t>(blockIdx.x);
+  const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
+  if (WARP && n >= p.N) return;
   // SHIFT: the row starts `shift` elements after an aligned piece (the same in every array).
   const int d = static_cast<int>(p.d);
   const int shift = SHIFT ? static_cast<int>((p.shift0 + n * p.d) % P::kElems) : 0;
@@ -513,7 +512,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_fwd_vec(const Norm
 #pragma unroll
       for (int k = 0; k < K; ++k) s = fma2(f[k], f[k], s);
     }
-    iy = rsqrtf(fmaf(row_sum<TPR>(s.x + s.y, part[0]), inv_d, p.eps));
+    iy = rsqrtf(fmaf(row_sum<WARP>(s.x + s.y, part[0]), inv_d, p.eps));
     if (t == 0 && p.rstd_post) p.rstd_post[n] = iy;
   }
   const int64_t grow = p.gate ? n / p.rows_per_gate * p.d : 0;
@@ -563,7 +562,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_fwd_vec(const Norm
     if (i < nvec && p.residual) store(p.residual, i, r[v]);
   }
   if (!p.w_pre) return;
-  const float ir = rsqrtf(fmaf(row_sum<TPR>(s.x + s.y, part[1]), inv_d, p.eps));
+  const float ir = rsqrtf(fmaf(row_sum<WARP>(s.x + s.y, part[1]), inv_d, p.eps));
   if (t == 0 && p.rstd_pre) p.rstd_pre[n] = ir;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
@@ -1136,14 +1135,13 @@ struct RowFit {
 };
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-template <class T, int TPR, int NV>
-cudaError_t fwd_vec(const NormFwd& p, bool shift, cudaStream_t s) {
-  constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
-  const unsigned grid = static_cast<unsigned>((p.N + kRows - 1) / kRows);
+template <class T, int NV, bool WARP>
+cudaError_t fwd_vec(const NormFwd& p, int threads, bool shift, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>(WARP ? (p.N + 3) / 4 : p.N);
   if (shift)
-    norm_fwd_vec<T, TPR, NV, true><<<grid, TPR < 128 ? 128 : TPR, 0, s>>>(p);
+    norm_fwd_vec<T, NV, WARP, true><<<grid, threads, 0, s>>>(p);
   else
-    norm_fwd_vec<T, TPR, NV, false><<<grid, TPR < 128 ? 128 : TPR, 0, s>>>(p);
+    norm_fwd_vec<T, NV, WARP, false><<<grid, threads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -1163,15 +1161,15 @@ cudaError_t fwd_t(NormFwd p, cudaStream_t s) {
     return cudaGetLastError();
   }
   p.shift0 = static_cast<int>(fit.shift0);
+  // Few rows: as many threads per row as there are pieces, for latency.  Many: two pieces per
+  // thread (four where that takes more than 512 threads), whose loads are in flight together.
   const bool few = p.N <= 2 * sm_count();
-  if (nvec <= 32) return fwd_vec<T, 32, 1>(p, shift, s);
-  if (nvec <= 64 && !few) return fwd_vec<T, 32, 2>(p, shift, s);
-  if (nvec <= 128) return fwd_vec<T, 128, 1>(p, shift, s);
-  if (nvec <= 256) return few ? fwd_vec<T, 256, 1>(p, shift, s) : fwd_vec<T, 128, 2>(p, shift, s);
-  if (nvec <= 512) return few ? fwd_vec<T, 512, 1>(p, shift, s) : fwd_vec<T, 256, 2>(p, shift, s);
-  if (nvec <= 1024) return few ? fwd_vec<T, 1024, 1>(p, shift, s) : fwd_vec<T, 512, 2>(p, shift, s);
-  if (nvec <= 2048) return few ? fwd_vec<T, 1024, 2>(p, shift, s) : fwd_vec<T, 512, 4>(p, shift, s);
-  return fwd_vec<T, 1024, 4>(p, shift, s);
+  auto warps = [&](int64_t per) { return static_cast<int>((nvec + 32 * per - 1) / (32 * per) * 32); };
+  if (nvec <= 32) return fwd_vec<T, 1, true>(p, 128, shift, s);
+  if (nvec <= 64 && !few) return fwd_vec<T, 2, true>(p, 128, shift, s);
+  if (nvec <= 1024 && few) return fwd_vec<T, 1, false>(p, warps(1), shift, s);
+  if (nvec <= 1024) return fwd_vec<T, 2, false>(p, warps(2), shift, s);
+  return fwd_vec<T, 4, false>(p, warps(4), shift, s);
 }
 
 template <class T>
