@@ -608,6 +608,7 @@ constexpr int kPartStride = kMaxCluster * kRingWarps + 8;  // the three sums in 
 struct RingCtl {
   uint64_t full[kMaxStages], empty[kMaxStages], sums[4];
   int abort;
+  uint32_t issued;  // batches copied, at the end
   float2 factor[kMaxStages][kRingWarps];  // i_y, i_r of the batch's rows
   float part[4][3 * kPartStride];
 };
@@ -783,12 +784,7 @@ __global__ void __launch_bounds__((TPR > kRingThreads ? TPR : kRingThreads) + 32
         __syncwarp();
       }
     }
-    if (!ok) {
-      // Copies in flight land before the block leaves.
-      const uint32_t first = it > static_cast<uint32_t>(S) ? it - S : 0u;
-      for (uint32_t q = first; q < it; ++q)
-        wait_warp(&rc->full[q % S], (q / S) & 1u, abort, ctl, false);
-    }
+    if (lane == 0) rc->issued = it;
   } else {
     // ------------------------------ arithmetic ------------------------------
     const int rw = threadIdx.x / TPR, t = threadIdx.x % TPR;  // row of the batch, first piece
@@ -1110,6 +1106,13 @@ __global__ void __launch_bounds__((TPR > kRingThreads ? TPR : kRingThreads) + 32
         if (rw == 0 && col[v])
           store_f32(p.part_pre + static_cast<int64_t>(worker) * p.d, v, acc_p[v], false);
     }
+  }
+  __syncthreads();
+  if (*abort && warp == 0) {
+    // After a wait that ran out: copies in flight land (boundedly) before the block leaves.
+    const uint32_t last = rc->issued;
+    for (uint32_t q = last > static_cast<uint32_t>(S) ? last - S : 0u; q < last; ++q)
+      wait_warp(&rc->full[q % S], (q / S) & 1u, abort, ctl, false);
   }
   // No block leaves while another of its cluster may still write its sums into it.
   if (CL) {
