@@ -1263,6 +1263,14 @@ int slm_orthogonalize(int dtype, const void* grad, int64_t ld, int64_t batch_str
                     reinterpret_cast<__half*>(ws + L.a_off[1])};
   float* diag[2] = {reinterpret_cast<float*>(ws + L.diag_off[0]),
                     reinterpret_cast<float*>(ws + L.diag_off[1])};
+  if (m <= kOrthSmall && n <= kOrthSmall) {
+    OrthSmall p{grad, ld, batch_stride, momentum, static_cast<float>(beta),
+                static_cast<float>(1.0 - beta), eps, nesterov, static_cast<int>(m),
+                static_cast<int>(n), steps, static_cast<__nv_bfloat16*>(out), {}};
+    memcpy(p.co, coefficients, static_cast<size_t>(steps) * 3 * sizeof(float));
+    SLM_LAUNCH(kTrOrth, launch_orth_small(dtype, p, batch, make_ctl(status), s));
+    return SLM_OK;
+  }
   const bool tall = m > n;
   const int64_t k = L.k;
   OrthChain ch{};

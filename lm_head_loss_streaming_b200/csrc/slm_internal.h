@@ -357,6 +357,19 @@ struct OrthView {
   float a, b, c;
   int out_vec;
 };
+// Matrices of up to kOrthSmall x kOrthSmall, in one launch.
+constexpr int kOrthSmall = 256;
+struct OrthSmall {
+  const void* grad;
+  int64_t ldg, grad_batch;
+  float* momentum;
+  float beta, rest, eps;
+  int nesterov, m, n, steps;
+  __nv_bfloat16* out;
+  float co[kMaxOrthSteps][3];
+};
+cudaError_t launch_orth_small(int dtype, const OrthSmall& p, int64_t batch, const DevCtl& c,
+                              cudaStream_t s);
 cudaError_t launch_orth_prep(int dtype, const OrthPrep& p, int64_t batch, cudaStream_t s);
 // bn: the tiles' columns (512, 256 or 128); operand maps as their boxes need it.
 cudaError_t launch_orth_chain(int bn, bool tall, const OrthChain& ch, const OrthMaps& maps,

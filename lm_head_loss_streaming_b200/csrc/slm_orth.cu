@@ -220,6 +220,9 @@ __device__ __forceinline__ int ld_acquire_s32(const int* p) {
 __device__ __forceinline__ void red_release_add_s32(int* p, int v) {
   asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
+__device__ __forceinline__ void fence_proxy_async_all() {
+  asm volatile("fence.proxy.async;" ::: "memory");
+}
 __device__ __forceinline__ void fence_proxy_async_global() {
   asm volatile("fence.proxy.async.global;" ::: "memory");
 }
@@ -907,7 +910,394 @@ cudaError_t launch_chain(const OrthChain& ch, const OrthMaps& maps, const DevCtl
   return cudaLaunchKernelEx(&cfg, kern, co, maps, c);
 }
 
+// ----------------------------------------------------------------------------------------
+// Matrices of up to 256 x 256: everything between the gradient and the result in one CTA pair's
+// shared and tensor memory.  Y [k, l] is X, or X^T when m > n, its rows shared out between the
+// two CTAs (128 each), zero beyond the matrix.  Per CTA:
+//   rows    hi of its 128 rows, K-major: both operands of Y Y^T
+//   cols    hi of all 256 rows, its 128 columns, MN-major: its half of the update's B operand
+//   mat     its 128 rows of R, then of R_B in place, K-major: both operands of R R, and the
+//           update's A operand
+//   tensor memory  256 columns of accumulator, 256 of hi and lo, two fp16 numbers per cell
+// An epilogue writes the next product's operands where the MMAs read them (a row of `cols` goes to
+// the CTA that holds those columns), and a product starts when the sixteen epilogue warps of the
+// pair have arrived.  Products are all latency here (a 256 x 256 one is 0.5 us of MMAs): the way
+// through L2 and the launch-wide meetings of orth_chain take 6 us each, this way 2.
+// ----------------------------------------------------------------------------------------
+constexpr int kSmallWarps = 8;  // epilogue warps per CTA
+constexpr int kSmallThreads = 32 + 32 * kSmallWarps;
+constexpr int kSmallBlock = 128 * 128;  // bytes of 128 rows x 64 fp16 columns
+
+struct SmallCtl {
+  uint64_t ready[2], tfull, fin;  // ready: in turn, as an arrival may overtake an earlier one
+  uint32_t tmem_base;
+  int abort;
+  double sums[2 * kSmallWarps];
+  alignas(16) float d[256];  // D of A, all rows
+  float db[128];             // D_B, this CTA's rows
+};
+constexpr size_t kSmallSmem = 1024 + 12 * kSmallBlock + sizeof(SmallCtl);
+static_assert(kSmallSmem <= 232448, "shared memory per CTA");
+
+// Byte offset of 16-byte piece `piece` (8 columns) of row `row` in tiles of `rows` x 64 columns
+// with the 128-byte swizzle.
+__device__ __forceinline__ uint32_t small_at(int rows, int row, int piece) {
+  return static_cast<uint32_t>((piece >> 3) * rows * 128 + row * 128 +
+                               (((piece & 7) ^ (row & 7)) << 4));
+}
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                              uint32_t d) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+// wait_warp for a barrier that both CTAs of the pair arrive on after writing shared memory.
+__device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          const DevCtl& ctl) {
+  const uint32_t a = smem_u32(bar);
+  bool done = mbar_try_wait_cluster(a, parity);
+  if (!done) {
+    const long long t0 = clock64();
+    while (!(done = mbar_try_wait_cluster(a, parity))) {
+      if (*abort) break;
+      if (clock64() - t0 > ctl.timeout_cycles) {
+        *abort = 1;
+        atomicOr(ctl.status, kFlagTimeout);
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, done);
+}
+
+template <class T>
+__global__ void __launch_bounds__(kSmallThreads, 1)
+    orth_small(const __grid_constant__ OrthSmall p, const DevCtl ctl) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* rows = smem;                     // 4 tiles of 128 x 64
+  uint8_t* cols = smem + 4 * kSmallBlock;   // 2 tiles of 256 x 64
+  uint8_t* mat = smem + 8 * kSmallBlock;    // 4 tiles of 128 x 64
+  SmallCtl* sc = reinterpret_cast<SmallCtl*>(smem + 12 * kSmallBlock);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int64_t z = blockIdx.x >> 1;
+  const bool tall = p.m > p.n;
+  const int k = tall ? p.n : p.m, l = tall ? p.m : p.n;
+  volatile int* abort = &sc->abort;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&sc->ready[0], 2 * kSmallWarps);
+    mbar_init(&sc->ready[1], 2 * kSmallWarps);
+    mbar_init(&sc->tfull, 1);
+    mbar_init(&sc->fin, 1);
+    sc->abort = 0;
+    if (blockIdx.x == 0) *ctl.status = 0;  // a wait can only run out long after this
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc_pair(&sc->tmem_base, 512);
+    tmem_relinquish_pair();
+  }
+  for (int i = threadIdx.x; i < 12 * kSmallBlock / 16; i += kSmallThreads)
+    reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = threadIdx.x; i < 256; i += kSmallThreads) {
+    sc->d[i] = 0.f;
+    sc->db[i & 127] = 0.f;
+  }
+  fence_proxy_async_all();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = sc->tmem_base;
+  const int products = 3 * p.steps;
+
+  // Epilogue warps: rows q * 32 + lane of the CTA, columns [128 wg, 128 wg + 128).
+  const int q = warp & 3, wg = (warp - 1) >> 2;
+  const int row = q * 32 + lane;                     // of the CTA
+  const int grow = static_cast<int>(rank) * 128 + row;  // of Y
+  const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + wg * 128;
+  const uint32_t master = acc + 256;
+  float inv = 0.f;
+  if (warp > 0) {
+    // u into the cells, momentum updated, the sum of u^2.
+    double sum = 0.0;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      const int col = wg * 128 + c * 32;
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int cc = col + 16 * h + e;
+          float u = 0.f;
+          if (grow < k && cc < l) {
+            const int i = tall ? cc : grow, j = tall ? grow : cc;
+            float g[1];
+            ld_elems<T, 1>(static_cast<const T*>(p.grad) + z * p.grad_batch + i * p.ldg + j, g);
+            u = g[0];
+            if (p.momentum) {
+              float* at = p.momentum + (z * p.m + i) * p.n + j;
+              const float mom = p.beta * *at + p.rest * u;
+              *at = mom;
+              u = p.nesterov ? p.beta * mom + p.rest * u : mom;
+            }
+          }
+          sum = fma(static_cast<double>(u), static_cast<double>(u), sum);
+          w[e] = __float_as_uint(u);
+        }
+        tmem_st16_raw(master + c * 32 + 16 * h, w);
+      }
+    }
+    tmem_st_wait();
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane < 2) {
+      double* at = &sc->sums[rank * kSmallWarps + warp - 1];
+      const uint32_t dst = mapa_shared(smem_u32(at), lane);
+      const unsigned long long bits = __double_as_longlong(sum);
+      st_shared_cluster_u32(dst, static_cast<uint32_t>(bits));
+      st_shared_cluster_u32(dst + 4, static_cast<uint32_t>(bits >> 32));
+    }
+  }
+  tc_fence_before();
+  cluster_sync();  // the sums are there, and both CTAs' shared memory is cleared
+  tc_fence_after();
+
+  if (warp == 0) {
+    // MMA issuer (leader only).
+    if (rank == 0) {
+      constexpr uint32_t kSym = idesc_f16_f32(256, 256, false, false);
+      constexpr uint32_t kUpd = idesc_f16_f32(256, 256, false, true);
+      for (int t = 0; t < products; ++t) {
+        if (!wait_pair(&sc->ready[t & 1], (t >> 1) & 1, abort, ctl)) break;
+        fence_proxy_async_all();
+        tc_fence_after();
+        if (lane == 0) {
+          const int op = t % 3;
+          const uint32_t a = smem_u32(op == kGram ? rows : mat);
+          const uint32_t b = op == kUpdate ? smem_u32(cols) : a;
+          const int steps = ((op == kGram ? l : k) + 15) / 16;
+          for (int kk = 0; kk < steps; ++kk) {
+            const uint64_t ad = smem_desc_sw128(a + (kk >> 2) * kSmallBlock + (kk & 3) * 32, 16, 1024);
+            const uint64_t bd = op == kUpdate
+                                    ? smem_desc_sw128(b + kk * 2048, 2 * kSmallBlock, 1024)
+                                    : smem_desc_sw128(b + (kk >> 2) * kSmallBlock + (kk & 3) * 32, 16, 1024);
+            umma_bf16_pair(tmem, ad, bd, op == kUpdate ? kUpd : kSym, kk != 0 ? 1u : 0u);
+          }
+          umma_commit_pair_mc(&sc->tfull, 0x3);
+        }
+        __syncwarp();
+      }
+      if (lane == 0) umma_commit_pair_mc(&sc->fin, 0x1);
+      __syncwarp();
+      wait_warp(&sc->fin, 0u, abort, ctl, false);
+    }
+  } else {
+    double total = 0.0;
+#pragma unroll
+    for (int i = 0; i < 2 * kSmallWarps; ++i) total += sc->sums[i];
+    inv = static_cast<float>(kScaleX / (sqrt(total) + static_cast<double>(p.eps)));
+    // This warp's operands are written: both CTAs' barriers learn of it.
+    auto arrive = [&](int t, bool withhold) {
+      fence_proxy_async_all();
+      tc_fence_before();
+      __syncwarp();
+      if (lane < 2 && !withhold) mbar_arrive_cluster(mapa_shared(smem_u32(&sc->ready[t & 1]), lane));
+    };
+    // hi (8 pairs of columns from col) to `rows` and to the CTA that holds the columns.
+    const uint32_t cols_at = mapa_shared(smem_u32(cols), wg);
+    auto put_hi = [&](int col, const uint32_t(&hi)[8]) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int piece = col / 8 + e;
+        *reinterpret_cast<uint4*>(rows + small_at(128, row, piece)) =
+            make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
+        st_cluster_v4(cols_at + small_at(256, grow, piece & 15), hi[4 * e], hi[4 * e + 1],
+                      hi[4 * e + 2], hi[4 * e + 3]);
+      }
+    };
+    auto put_cells = [&](uint32_t at, const uint32_t(&hi)[8], const uint32_t(&lo)[8]) {
+      uint32_t w[16];
+#pragma unroll
+      for (int h = 0; h < 8; ++h) {
+        w[2 * h] = __byte_perm(hi[h], lo[h], 0x5410);
+        w[2 * h + 1] = __byte_perm(hi[h], lo[h], 0x7632);
+      }
+      tmem_st16_raw(at, w);
+    };
+    auto split = [](float2 r, uint32_t& hi, uint32_t& lo) {
+      hi = pack_half2(r.x, r.y);
+      const float2 f = unpack_half2(hi);
+      lo = pack_half2(r.x - f.x, r.y - f.y);
+    };
+    // X = u / (||u|| + eps).
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+      const int col = wg * 128 + c * 16;
+      if (col >= l) break;
+      uint32_t w[16], hi[8], lo[8];
+      tmem_ld16_raw(master + c * 16, w);
+      tmem_ld_wait();
+#pragma unroll
+      for (int h = 0; h < 8; ++h)
+        split(make_float2(__uint_as_float(w[2 * h]) * inv, __uint_as_float(w[2 * h + 1]) * inv),
+              hi[h], lo[h]);
+      put_cells(master + c * 16, hi, lo);
+      put_hi(col, hi);
+    }
+    tmem_st_wait();
+    arrive(0, false);
+
+    for (int t = 0; t < products; ++t) {
+      const int step = t / 3, op = t % 3;
+      const float a = p.co[step][0], b = p.co[step][1], cc = p.co[step][2];
+      const bool last = t == products - 1;
+      // What the other warps wrote for this product's epilogue (diagonals), then its MMAs.
+      if (!wait_pair(&sc->ready[t & 1], (t >> 1) & 1, abort, ctl)) break;
+      if (!wait_warp(&sc->tfull, t & 1, abort, ctl)) break;
+      tc_fence_after();
+      const float drow = op == kSquare ? sc->d[grow] : op == kUpdate ? sc->db[row] : 0.f;
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        const int col = wg * 128 + c * 16;
+        if (col >= (op == kUpdate ? l : k)) break;
+        uint32_t v[16], hi[8], lo[8];
+        tmem_ld16_raw(acc + c * 16, v);
+        if (op == kUpdate) {
+          uint32_t w[16];
+          tmem_ld16_raw(master + c * 16, w);
+          tmem_ld_wait();
+#pragma unroll
+          for (int h = 0; h < 8; ++h) {
+            const float2 x = make_float2(__uint_as_float(v[2 * h]), __uint_as_float(v[2 * h + 1]));
+            const float2 r = __ffma2_rn(
+                x, both(1.f / kScaleB),
+                __ffma2_rn(unpack_half2(__byte_perm(w[2 * h], w[2 * h + 1], 0x5410)),
+                           __fadd2_rn(both(drow), both(a)),
+                           __fmul2_rn(unpack_half2(__byte_perm(w[2 * h], w[2 * h + 1], 0x7632)),
+                                      both(a))));
+            if (last)
+              hi[h] = pack_bf162(r.x * (1.f / kScaleX), r.y * (1.f / kScaleX));
+            else
+              split(r, hi[h], lo[h]);
+          }
+          if (last) {
+            __nv_bfloat16* out = p.out + z * p.m * p.n;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (grow < k && col + e < l) {
+                const uint16_t bits = static_cast<uint16_t>(e & 1 ? hi[e / 2] >> 16 : hi[e / 2]);
+                out[tall ? static_cast<int64_t>(col + e) * p.n + grow
+                         : static_cast<int64_t>(grow) * p.n + col + e] =
+                    __ushort_as_bfloat16(bits);
+              }
+          } else {
+            put_cells(master + c * 16, hi, lo);
+            put_hi(col, hi);
+          }
+          __syncwarp();
+          continue;
+        }
+        uint8_t* at[2] = {mat + small_at(128, row, col / 8), mat + small_at(128, row, col / 8 + 1)};
+        if (op == kSquare) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint4 w = *reinterpret_cast<const uint4*>(at[e]);
+            lo[4 * e] = w.x;
+            lo[4 * e + 1] = w.y;
+            lo[4 * e + 2] = w.z;
+            lo[4 * e + 3] = w.w;
+          }
+        }
+        tmem_ld_wait();
+        float diag = 0.f;
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+          const float2 x = make_float2(__uint_as_float(v[2 * h]), __uint_as_float(v[2 * h + 1]));
+          float2 r;
+          if (op == kGram) {
+            r = __fmul2_rn(x, both(kScaleA / (kScaleX * kScaleX)));
+          } else {
+            const float2 dj = *reinterpret_cast<const float2*>(&sc->d[col + 2 * h]);
+            const float2 tt = __ffma2_rn(both(cc * (kScaleB / kScaleA)), dj,
+                                         both(fmaf(cc, drow, b) * (kScaleB / kScaleA)));
+            r = __ffma2_rn(unpack_half2(lo[h]), tt,
+                           __fmul2_rn(x, both(cc * (kScaleB / (kScaleA * kScaleA)))));
+          }
+          // The diagonal's element to fp32, a zero in its place.
+          const bool d0 = grow == col + 2 * h, d1 = grow == col + 2 * h + 1;
+          diag = d0 ? x.x : d1 ? x.y : diag;
+          hi[h] = pack_half2(d0 ? 0.f : r.x, d1 ? 0.f : r.y);
+        }
+        if (grow >= col && grow < col + 16) {
+          if (op == kGram) {
+            const uint32_t bits = __float_as_uint(diag * (1.f / (kScaleX * kScaleX)));
+            const uint32_t da = smem_u32(&sc->d[grow]);
+            st_shared_cluster_u32(mapa_shared(da, 0), bits);
+            st_shared_cluster_u32(mapa_shared(da, 1), bits);
+          } else {
+            sc->db[row] = fmaf(cc, fmaf(drow, drow, diag * (1.f / (kScaleA * kScaleA))), b * drow);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<uint4*>(at[e]) =
+              make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
+        __syncwarp();
+      }
+      if (op == kUpdate && !last) tmem_st_wait();
+      // Test hook (fault == 1): withhold one warp's first arrival.
+      if (!last) arrive(t + 1, ctl.fault == 1 && t == 0 && warp == 1);
+    }
+  }
+
+  // Neither CTA leaves while the other may still write its shared memory or use its TMEM.
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc_pair(tmem, 512);
+}
+
+template <class T>
+cudaError_t small_t(const OrthSmall& p, int64_t batch, const DevCtl& c, cudaStream_t s) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  static bool smem_set[64] = {false};  // per device, once
+  if (!smem_set[dev]) {
+    e = cudaFuncSetAttribute(orth_small<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmallSmem));
+    if (e != cudaSuccess) return e;
+    smem_set[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * batch), 1, 1);
+  cfg.blockDim = dim3(kSmallThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmallSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, orth_small<T>, p, c);
+}
+
 }  // namespace
+
+cudaError_t launch_orth_small(int dtype, const OrthSmall& p, int64_t batch, const DevCtl& c,
+                              cudaStream_t s) {
+  return dtype == 0   ? small_t<__nv_bfloat16>(p, batch, c, s)
+         : dtype == 1 ? small_t<__half>(p, batch, c, s)
+                      : small_t<float>(p, batch, c, s);
+}
 
 cudaError_t launch_orth_prep(int dtype, const OrthPrep& p, int64_t batch, cudaStream_t s) {
   auto aligned = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };

@@ -132,11 +132,12 @@ def test_traced_launches_have_their_classes():
         _lib.slm_trace_read()
         f = block_norm_fwd(t["x"], t["z"], t["w_pre"], t["w_post"])
         block_norm_bwd(f, t["x"], t["z"], t["w_pre"], t["w_post"], d_hidden=t["x"])
+        orthogonalize(t["W"])
         orthogonalize(t["proj"])
         st, classes = _lib.slm_trace_read()
     finally:
         _lib.slm_trace_enable(False)
     assert st == 0
     assert classes["norm"][1] == 2 and classes["norm"][0] > 0      # forward, backward
-    assert classes["orth"][1] == 2 and classes["orth"][0] > 0      # preparation, products
-    assert sum(n for _, n in classes.values()) == 4
+    assert classes["orth"][1] == 3 and classes["orth"][0] > 0      # preparation, products; small
+    assert sum(n for _, n in classes.values()) == 5

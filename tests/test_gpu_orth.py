@@ -26,7 +26,8 @@ def check(got, u, rows=ROWS, eps=1e-7):
 # One element, rows and columns, below / at / above the 64-wide K block, the 128- and 256-wide
 # tiles, odd sizes, several tiles with ragged ends, very wide and very tall.
 SHAPES = [(1, 1), (1, 9), (9, 1), (5, 3), (16, 16), (33, 64), (64, 33), (65, 127), (128, 128),
-          (129, 257), (255, 256), (256, 256), (257, 255), (384, 500), (700, 300), (520, 777),
+          (129, 257), (128, 256), (256, 128), (200, 129), (130, 250), (255, 256), (256, 256),
+          (257, 255), (384, 500), (700, 300), (520, 777),
           (1024, 1024), (1100, 900), (40, 5000), (5000, 40)]
 
 
@@ -51,7 +52,7 @@ def test_diagonal_and_repeated_rows():
     check(orthogonalize(g), g)
 
 
-@pytest.mark.parametrize("batch,m,n", [(1, 64, 64), (3, 100, 257), (5, 257, 100), (2, 600, 600),
+@pytest.mark.parametrize("batch,m,n", [(1, 64, 64), (200, 256, 130), (7, 30, 250), (3, 100, 257), (5, 257, 100), (2, 600, 600),
                                        (80, 40, 30)])
 def test_stacks(batch, m, n):
     g = torch.stack([(10.0 ** (i % 5 - 2)) * spectrum(m, n, "noise", i) for i in range(batch)])
@@ -125,6 +126,10 @@ def test_zeros_nan_and_neighbours():
     g[2, 3, 4] = float("nan")
     got = orthogonalize(g)
     assert not got[1].any() and got[2].isnan().all()
+    wide = torch.stack([spectrum(60, 270, "noise", i) for i in range(3)]).to(F32)
+    wide[1, 5, 260] = float("nan")
+    many = orthogonalize(wide)
+    assert many[1].isnan().all() and torch.equal(many[2], orthogonalize(wide[2]))
     assert torch.equal(got[0], alone[0]) and torch.equal(got[3], alone[3])
     g[2, 3, 4] = float("inf")
     assert orthogonalize(g)[2].isnan().all()
@@ -192,7 +197,7 @@ def test_same_bits_each_time(shape):
         assert torch.equal(orthogonalize(g), want)
 
 
-@pytest.mark.parametrize("shape", [(300, 200), (600, 1300)])
+@pytest.mark.parametrize("shape", [(200, 150), (300, 200), (600, 1300)])
 def test_wait_runs_out_reports_timeout_and_the_next_call_is_right(shape):
     from lm_head_loss_streaming_b200 import _lib
     g = spectrum(*shape, "noise", 11).to(BF)
