@@ -920,13 +920,22 @@ cudaError_t launch_chain(const OrthChain& ch, const OrthMaps& maps, const DevCtl
 //           update's A operand
 //   tensor memory  256 columns of accumulator, 256 of hi and lo, two fp16 numbers per cell
 // An epilogue writes the next product's operands where the MMAs read them (a row of `cols` goes to
-// the CTA that holds those columns), and a product starts when the sixteen epilogue warps of the
-// pair have arrived.  Products are all latency here (a 256 x 256 one is 0.5 us of MMAs): the way
-// through L2 and the launch-wide meetings of orth_chain take 6 us each, this way 2.
+// the CTA that holds those columns), and a product starts when the epilogue warps of the pair have
+// arrived.  A step of 256 x 256 takes 15.5 us: 4.6 of MMAs and their start, 7 of epilogue
+// arithmetic (all four schedulers of an SM issue throughout: 128 x 256 numbers each of a Gram
+// 1.2 us, a square 1.8, an update 3.6) and 4 of arrivals.  Sixteen warps with every fourth run of
+// 16 columns each, so that a narrow matrix uses them all, and global memory by way of shared memory
+// 32 B at a time: eight warps of 128 columns, whose lanes read and wrote a row each, took 53 us for
+// 64 x 64 and 131 for 256 x 256.  Graph replay, this kernel and orth_chain with its two launches
+// before: 64 x 64 43 and 66 us, 16 x 200 60 and 62, 256 x 256 92 and 99, a hundred of 128 x 128 119
+// and 145, a hundred of 256 x 256 186 and 225.
 // ----------------------------------------------------------------------------------------
-constexpr int kSmallWarps = 8;  // epilogue warps per CTA
+constexpr int kSmallWarps = 16;  // epilogue warps per CTA
 constexpr int kSmallThreads = 32 + 32 * kSmallWarps;
+constexpr int kSmallStride = kSmallWarps / 4 * 16;  // columns from one run of a warp's to the next
 constexpr int kSmallBlock = 128 * 128;  // bytes of 128 rows x 64 fp16 columns
+constexpr int kSmallStage = 32 * 64 * 4;  // bytes of a warp's fp32 elements, 32 rows x 64
+static_assert(kSmallWarps * kSmallStage == 8 * kSmallBlock, "rows and cols, cleared as stages");
 
 struct SmallCtl {
   uint64_t ready[2], tfull, fin;  // ready: in turn, as an arrival may overtake an earlier one
@@ -1000,8 +1009,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     tmem_alloc_pair(&sc->tmem_base, 512);
     tmem_relinquish_pair();
   }
-  for (int i = threadIdx.x; i < 12 * kSmallBlock / 16; i += kSmallThreads)
-    reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = threadIdx.x; i < 4 * kSmallBlock / 16; i += kSmallThreads)
+    reinterpret_cast<uint4*>(mat)[i] = make_uint4(0, 0, 0, 0);
   for (int i = threadIdx.x; i < 256; i += kSmallThreads) {
     sc->d[i] = 0.f;
     sc->db[i & 127] = 0.f;
@@ -1013,45 +1022,76 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   const uint32_t tmem = sc->tmem_base;
   const int products = 3 * p.steps;
 
-  // Epilogue warps: rows q * 32 + lane of the CTA, columns [128 wg, 128 wg + 128).
-  const int q = warp & 3, wg = (warp - 1) >> 2;
-  const int row = q * 32 + lane;                     // of the CTA
+  // Epilogue warps: rows q * 32 + lane of the CTA, 16 columns of every kSmallStride.
+  const int q = warp & 3;
+  const int col0 = ((warp - 1) >> 2) * 16;
+  const int row = q * 32 + lane;                        // of the CTA
   const int grow = static_cast<int>(rank) * 128 + row;  // of Y
-  const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + wg * 128;
+  const bool live = grow - lane < k;                    // some row of this warp is Y's
+  const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16);
   const uint32_t master = acc + 256;
+  float* const stage = reinterpret_cast<float*>(smem + max(warp - 1, 0) * kSmallStage);
   float inv = 0.f;
   if (warp > 0) {
-    // u into the cells, momentum updated, the sum of u^2.
-    double sum = 0.0;
+    // u into the cells, momentum updated, the sum of u^2.  Two runs of 16 elements per load, by way
+    // of shared memory, element c of row r at c ^ r.  When m > n a lane's row of Y is a column of
+    // the matrix, and the same runs are lanes' rows.
+    double sums[2] = {0.0, 0.0};
+    const int run = lane & 15, half = lane & 16;
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-      const int col = wg * 128 + c * 32;
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        uint32_t w[16];
+    for (int c = 0; c < 4 && live; ++c) {
+      const int col = col0 + c * kSmallStride;
+      if (col >= l) break;
+      // Element e of this lane's run: at (i, j), then a row down each, `lim` of them in the matrix.
+      const int i = tall ? col : grow - lane + half;
+      const int j = tall ? grow - lane + (run + half) : col + run;
+      const int lim = j < static_cast<int>(p.n) ? static_cast<int>(p.m) - i : 0;
+      // Every load is issued before one is used; those beyond the matrix read its first element.
+      const T* const from = static_cast<const T*>(p.grad) + z * p.grad_batch;
+      float* const mom = p.momentum ? p.momentum + z * p.m * p.n : nullptr;
+      const int jn = i * static_cast<int>(p.n) + j;
+      T raw[16];
+      float u[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) raw[e] = from[e < lim ? (i + e) * p.ldg + j : 0];
+      if (mom) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) u[e] = mom[e < lim ? jn + e * static_cast<int>(p.n) : 0];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const int cc = col + 16 * h + e;
-          float u = 0.f;
-          if (grow < k && cc < l) {
-            const int i = tall ? cc : grow, j = tall ? grow : cc;
-            float g[1];
-            ld_elems<T, 1>(static_cast<const T*>(p.grad) + z * p.grad_batch + i * p.ldg + j, g);
-            u = g[0];
-            if (p.momentum) {
-              float* at = p.momentum + (z * p.m + i) * p.n + j;
-              const float mom = p.beta * *at + p.rest * u;
-              *at = mom;
-              u = p.nesterov ? p.beta * mom + p.rest * u : mom;
-            }
-          }
-          sum = fma(static_cast<double>(u), static_cast<double>(u), sum);
-          w[e] = __float_as_uint(u);
+          const float g = static_cast<float>(raw[e]);
+          const float now = p.beta * u[e] + p.rest * g;
+          if (e < lim) mom[jn + e * static_cast<int>(p.n)] = now;
+          u[e] = p.nesterov ? p.beta * now + p.rest * g : now;
         }
-        tmem_st16_raw(master + c * 32 + 16 * h, w);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) u[e] = static_cast<float>(raw[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float in = e < lim ? u[e] : 0.f;
+        sums[e & 1] = fma(static_cast<double>(in), static_cast<double>(in), sums[e & 1]);
+        const int r = tall ? run + half : e + half, cc = c * 16 + (tall ? e : run);
+        stage[r * 64 + (cc ^ r)] = in;
       }
     }
+    __syncwarp();
+#pragma unroll 1
+    for (int c = 0; c < 4 && live; ++c) {
+      if (col0 + c * kSmallStride >= l) break;
+      uint32_t w[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(stage[lane * 64 + ((c * 16 + e) ^ lane)]);
+      tmem_st16_raw(master + col0 + c * kSmallStride, w);
+    }
     tmem_st_wait();
+    __syncwarp();
+#pragma unroll 4
+    for (int i = lane; i < kSmallStage / 16; i += 32)
+      reinterpret_cast<uint4*>(stage)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_all();
+    double sum = sums[0] + sums[1];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane < 2) {
@@ -1108,15 +1148,19 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
       if (lane < 2 && !withhold) mbar_arrive_cluster(mapa_shared(smem_u32(&sc->ready[t & 1]), lane));
     };
     // hi (8 pairs of columns from col) to `rows` and to the CTA that holds the columns.
-    const uint32_t cols_at = mapa_shared(smem_u32(cols), wg);
+    const uint32_t cols_far = mapa_shared(smem_u32(cols), rank ^ 1);
     auto put_hi = [&](int col, const uint32_t(&hi)[8]) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int piece = col / 8 + e;
         *reinterpret_cast<uint4*>(rows + small_at(128, row, piece)) =
             make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
-        st_cluster_v4(cols_at + small_at(256, grow, piece & 15), hi[4 * e], hi[4 * e + 1],
-                      hi[4 * e + 2], hi[4 * e + 3]);
+        const uint32_t at = small_at(256, grow, piece & 15);
+        if ((col < 128) == (rank == 0))
+          *reinterpret_cast<uint4*>(cols + at) =
+              make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
+        else
+          st_cluster_v4(cols_far + at, hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
       }
     };
     auto put_cells = [&](uint32_t at, const uint32_t(&hi)[8], const uint32_t(&lo)[8]) {
@@ -1135,17 +1179,15 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     };
     // X = u / (||u|| + eps).
 #pragma unroll 1
-    for (int c = 0; c < 8; ++c) {
-      const int col = wg * 128 + c * 16;
-      if (col >= l) break;
+    for (int col = col0; col < l && live; col += kSmallStride) {
       uint32_t w[16], hi[8], lo[8];
-      tmem_ld16_raw(master + c * 16, w);
+      tmem_ld16_raw(master + col, w);
       tmem_ld_wait();
 #pragma unroll
       for (int h = 0; h < 8; ++h)
         split(make_float2(__uint_as_float(w[2 * h]) * inv, __uint_as_float(w[2 * h + 1]) * inv),
               hi[h], lo[h]);
-      put_cells(master + c * 16, hi, lo);
+      put_cells(master + col, hi, lo);
       put_hi(col, hi);
     }
     tmem_st_wait();
@@ -1160,15 +1202,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
       if (!wait_warp(&sc->tfull, t & 1, abort, ctl)) break;
       tc_fence_after();
       const float drow = op == kSquare ? sc->d[grow] : op == kUpdate ? sc->db[row] : 0.f;
+      const int end = !live ? 0 : op == kUpdate ? l : k;
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
-        const int col = wg * 128 + c * 16;
-        if (col >= (op == kUpdate ? l : k)) break;
+      for (int col = col0; col < end; col += kSmallStride) {
         uint32_t v[16], hi[8], lo[8];
-        tmem_ld16_raw(acc + c * 16, v);
+        tmem_ld16_raw(acc + col, v);
         if (op == kUpdate) {
           uint32_t w[16];
-          tmem_ld16_raw(master + c * 16, w);
+          tmem_ld16_raw(master + col, w);
           tmem_ld_wait();
 #pragma unroll
           for (int h = 0; h < 8; ++h) {
@@ -1185,17 +1226,26 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
               split(r, hi[h], lo[h]);
           }
           if (last) {
-            __nv_bfloat16* out = p.out + z * p.m * p.n;
+            // The operands have been read: this warp's part of them takes what it has to turn.
+            __nv_bfloat16* const out = p.out + z * p.m * p.n;
+            uint32_t* const turn = reinterpret_cast<uint32_t*>(stage);
+            if (!tall) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (grow < k && col + e < l) {
-                const uint16_t bits = static_cast<uint16_t>(e & 1 ? hi[e / 2] >> 16 : hi[e / 2]);
-                out[tall ? static_cast<int64_t>(col + e) * p.n + grow
-                         : static_cast<int64_t>(grow) * p.n + col + e] =
-                    __ushort_as_bfloat16(bits);
-              }
+              for (int h = 0; h < 8; ++h) turn[lane * 8 + (h ^ (lane >> 2))] = hi[h];
+              __syncwarp();
+            }
+            const int run = lane & 15, half = lane & 16;
+            const int i = tall ? col : grow - lane + half, j = tall ? grow : col + run;
+            const int lim = j < static_cast<int>(p.n) ? static_cast<int>(p.m) - i : 0;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int r = e + half;
+              const uint32_t two = tall ? hi[e / 2] : turn[r * 8 + ((run >> 1) ^ (r >> 2))];
+              const uint16_t bits = static_cast<uint16_t>((tall ? e : run) & 1 ? two >> 16 : two);
+              if (e < lim) out[(i + e) * static_cast<int>(p.n) + j] = __ushort_as_bfloat16(bits);
+            }
           } else {
-            put_cells(master + c * 16, hi, lo);
+            put_cells(master + col, hi, lo);
             put_hi(col, hi);
           }
           __syncwarp();
@@ -1213,34 +1263,46 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
           }
         }
         tmem_ld_wait();
-        float diag = 0.f;
+        if (op == kGram) {
 #pragma unroll
-        for (int h = 0; h < 8; ++h) {
-          const float2 x = make_float2(__uint_as_float(v[2 * h]), __uint_as_float(v[2 * h + 1]));
-          float2 r;
-          if (op == kGram) {
-            r = __fmul2_rn(x, both(kScaleA / (kScaleX * kScaleX)));
-          } else {
+          for (int h = 0; h < 8; ++h) {
+            const float2 x = make_float2(__uint_as_float(v[2 * h]), __uint_as_float(v[2 * h + 1]));
+            const float2 r = __fmul2_rn(x, both(kScaleA / (kScaleX * kScaleX)));
+            hi[h] = pack_half2(r.x, r.y);
+          }
+        } else {
+          const float2 slope = both(cc * (kScaleB / kScaleA));
+          const float2 base = both(fmaf(cc, drow, b) * (kScaleB / kScaleA));
+#pragma unroll
+          for (int h = 0; h < 8; ++h) {
+            const float2 x = make_float2(__uint_as_float(v[2 * h]), __uint_as_float(v[2 * h + 1]));
             const float2 dj = *reinterpret_cast<const float2*>(&sc->d[col + 2 * h]);
-            const float2 tt = __ffma2_rn(both(cc * (kScaleB / kScaleA)), dj,
-                                         both(fmaf(cc, drow, b) * (kScaleB / kScaleA)));
-            r = __ffma2_rn(unpack_half2(lo[h]), tt,
-                           __fmul2_rn(x, both(cc * (kScaleB / (kScaleA * kScaleA)))));
+            const float2 r = __ffma2_rn(unpack_half2(lo[h]), __ffma2_rn(slope, dj, base),
+                                        __fmul2_rn(x, both(cc * (kScaleB / (kScaleA * kScaleA)))));
+            hi[h] = pack_half2(r.x, r.y);
           }
-          // The diagonal's element to fp32, a zero in its place.
-          const bool d0 = grow == col + 2 * h, d1 = grow == col + 2 * h + 1;
-          diag = d0 ? x.x : d1 ? x.y : diag;
-          hi[h] = pack_half2(d0 ? 0.f : r.x, d1 ? 0.f : r.y);
         }
-        if (grow >= col && grow < col + 16) {
-          if (op == kGram) {
-            const uint32_t bits = __float_as_uint(diag * (1.f / (kScaleX * kScaleX)));
-            const uint32_t da = smem_u32(&sc->d[grow]);
-            st_shared_cluster_u32(mapa_shared(da, 0), bits);
-            st_shared_cluster_u32(mapa_shared(da, 1), bits);
-          } else {
-            sc->db[row] = fmaf(cc, fmaf(drow, drow, diag * (1.f / (kScaleA * kScaleA))), b * drow);
+        if (col + 16 > grow - lane && col < grow - lane + 32) {
+          // The diagonal's elements to fp32, zeros in their place.
+          float diag = 0.f;
+#pragma unroll
+          for (int h = 0; h < 8; ++h) {
+            const bool d0 = grow == col + 2 * h, d1 = grow == col + 2 * h + 1;
+            diag = d0 ? __uint_as_float(v[2 * h]) : d1 ? __uint_as_float(v[2 * h + 1]) : diag;
+            hi[h] = d0 ? hi[h] & 0xffff0000u : d1 ? hi[h] & 0xffffu : hi[h];
           }
+          if (grow >= col && grow < col + 16) {
+            if (op == kGram) {
+              const uint32_t bits = __float_as_uint(diag * (1.f / (kScaleX * kScaleX)));
+              const uint32_t da = smem_u32(&sc->d[grow]);
+              st_shared_cluster_u32(mapa_shared(da, 0), bits);
+              st_shared_cluster_u32(mapa_shared(da, 1), bits);
+            } else {
+              sc->db[row] =
+                  fmaf(cc, fmaf(drow, drow, diag * (1.f / (kScaleA * kScaleA))), b * drow);
+            }
+          }
+          __syncwarp();
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e)
