@@ -451,9 +451,11 @@ int norm_checks(int dtype, const void* x, int64_t ldx, const void* y, int64_t ld
 
 // Orthogonalised update.
 struct OrthLayout {
-  size_t status_off, sums_off, diag_off[2], a_off[2], hi_off[2], lo_off, total;
+  size_t status_off, sums_off, diag_off[2], a_off[2], hi_off[2], lo_off, parts_off, total;
   int64_t k, ldx, ldk;
 };
+
+int orth_plan(OrthChain* ch, int64_t m, int64_t n, int64_t batch);
 
 OrthLayout orth_layout(int64_t batch, int64_t m, int64_t n) {
   OrthLayout L{};
@@ -477,7 +479,14 @@ OrthLayout orth_layout(int64_t batch, int64_t m, int64_t n) {
     off = align_up(off + b * m * L.ldx * 2, kAlign);
   }
   L.lo_off = off;
-  L.total = align_up(off + b * m * L.ldx * 2, kAlign);
+  off = align_up(off + b * m * L.ldx * 2, kAlign);
+  L.parts_off = off;
+  OrthChain ch{};
+  const int bn = orth_plan(&ch, m, n, batch);
+  if (ch.geom[0].split > 1)
+    off = align_up(off + static_cast<size_t>(ch.geom[0].num_units) * kPairM * bn * sizeof(float),
+                   kAlign);
+  L.total = off;
   return L;
 }
 
@@ -530,9 +539,11 @@ bool make_map_stack(CUtensorMap* m, const void* base, int64_t inner, int64_t out
 // (27 TFLOP/s per pair; two thirds of that at 128 columns) or its operands' way from L2 (9.3 TB/s
 // shared by the pairs that are busy), whichever is longer; the rates as measured on the products
 // of 4096 x 4096 matrices.  A round of tiles also costs its epilogue, about 1 us per 128 columns.
+// split_k: the K blocks of a tile may be shared out in parts over pairs that are idle otherwise,
+// at the cost of another meeting (4 us with the parts' way through memory) and of adding them.
 double orth_tiles(OrthGeom* g, int bn, int64_t rows, int64_t cols, int64_t k, int64_t batch,
-                  bool sym) {
-  const int64_t pairs = std::max(1, sm_count() / 2);
+                  bool sym, bool split_k) {
+  const int64_t pairs = kOrthPairs;
   const int64_t nm = ceil_div(rows, kPairM), nn = ceil_div(cols, bn);
   // Symmetric: the tiles that reach below the diagonal.
   const int64_t per = !sym ? nm * nn : bn == 512 ? (nm + 1) * (nm + 1) / 4
@@ -543,31 +554,45 @@ double orth_tiles(OrthGeom* g, int bn, int64_t rows, int64_t cols, int64_t k, in
   g->units_per = static_cast<int>(per);
   g->num_units = static_cast<int>(units);
   g->k_blocks = static_cast<int>(ceil_div(k, kBK));
-  auto round = [&](int64_t busy) {
+  g->split = 1;
+  g->part_blocks = g->k_blocks;
+  auto round = [&](int64_t busy, int blocks) {
     const double mma = 2.0 * kPairM * bn * kBK / (bn == 128 ? 18e12 : 27e12);
     const double l2 = (kPairM + bn) * kBK * 2.0 * static_cast<double>(busy) / 9.3e12;
-    return g->k_blocks * std::max(mma, l2) + 1e-6 * bn / 128;
+    return blocks * std::max(mma, l2) + 1e-6 * bn / 128;
   };
-  return static_cast<double>(units / pairs) * round(pairs) +
-         (units % pairs != 0 ? round(units % pairs) : 0.0) + 4e-6;
+  double best = static_cast<double>(units / pairs) * round(pairs, g->k_blocks) +
+                (units % pairs != 0 ? round(units % pairs, g->k_blocks) : 0.0) + 4e-6;
+  if (!split_k || bn > 256 || units == 0) return best;
+  for (int64_t s = 2; s * units <= pairs && s <= g->k_blocks; ++s) {
+    const int64_t part = ceil_div(g->k_blocks, s);
+    if (ceil_div(g->k_blocks, part) != s) continue;
+    const double joins = static_cast<double>(ceil_div(units * bn / 4, 2 * 8 * pairs));
+    const double cost = round(s * units, static_cast<int>(part)) + 4e-6 + 4e-6 +
+                        joins * (1e-6 + 0.1e-6 * static_cast<double>(s));
+    if (cost >= best) continue;
+    best = cost;
+    g->split = static_cast<int>(s);
+    g->part_blocks = static_cast<int>(part);
+    g->num_units = static_cast<int>(s * units);
+  }
+  return best;
 }
 
 // The tile grids of a step's three products and their tiles' width: of 512, 256 and 128 columns
 // the one whose rounds are estimated to take least.  Wide tiles read less from L2 per flop,
 // narrow ones leave fewer pairs idle and have shorter epilogues.  Whole calls measured at 128 /
-// 256 / 512 columns: 256 x 256 101 / 123 / 152 us, 1024 x 1024 174 / 206 / 367, 2048 x 2048
-// 332 / 296 / 516; the update alone of a 4096 x 4096 matrix 178 us at 128 and 125 at 512.  (A pair
-// working each matrix of a stack by itself, without the launch's meetings, was slower but for a
-// single 64 x 64 matrix, 68 us against 72.)
+// 256 / 512 columns: 1024 x 1024 174 / 206 / 367 us, 2048 x 2048 332 / 296 / 516; the update alone
+// of a 4096 x 4096 matrix 178 us at 128 and 125 at 512.
 int orth_plan(OrthChain* ch, int64_t m, int64_t n, int64_t batch) {
   const int64_t k = std::min(m, n), l = std::max(m, n);
   int best = 0;
   double best_cost = 0;
   for (int bn : {512, 256, 128}) {
     OrthGeom g[3];
-    const double cost = orth_tiles(&g[0], bn, k, k, l, batch, true) +
-                        orth_tiles(&g[1], bn, k, k, k, batch, true) +
-                        orth_tiles(&g[2], bn, m, n, k, batch, false);
+    const double cost = orth_tiles(&g[0], bn, k, k, l, batch, true, true) +
+                        orth_tiles(&g[1], bn, k, k, k, batch, true, false) +
+                        orth_tiles(&g[2], bn, m, n, k, batch, false, false);
     if (best != 0 && cost >= best_cost) continue;
     best = bn;
     best_cost = cost;
@@ -1276,7 +1301,7 @@ int slm_orthogonalize(int dtype, const void* grad, int64_t ld, int64_t batch_str
   OrthChain ch{};
   const int bn = orth_plan(&ch, m, n, batch);
   // At most one tile of the update per pair, and a second accumulator slot free for it.
-  ch.resident = bn <= 256 && steps > 1 && ch.geom[2].num_units <= sm_count() / 2;
+  ch.resident = bn <= 256 && steps > 1 && ch.geom[2].num_units <= kOrthPairs;
   ch.steps = steps;
   ch.out_vec = n % 8 == 0 && !misaligned(out, 16);
   ch.m = static_cast<int>(m);
@@ -1285,6 +1310,7 @@ int slm_orthogonalize(int dtype, const void* grad, int64_t ld, int64_t batch_str
   ch.ldx = static_cast<int>(L.ldx);
   ch.ldk = static_cast<int>(L.ldk);
   ch.lo = lo;
+  ch.parts = reinterpret_cast<float*>(ws + L.parts_off);
   ch.out = static_cast<__nv_bfloat16*>(out);
   ch.counter = status + 1;
   for (int i = 0; i < 2; ++i) {

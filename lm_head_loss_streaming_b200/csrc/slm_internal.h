@@ -327,9 +327,11 @@ struct OrthPrep {
 // The products' tile grids and data.  Products 0 (R and D of A), 1 (R_B and D_B) and 2 (the
 // update of X) of each step; [i] of hi and of the maps is the buffer that step i & 1 reads.
 constexpr int kMaxOrthSteps = 64;
+constexpr int kOrthPairs = 74;  // pairs of SMs that the tile grids are laid out for
 constexpr int kOrthGroup = 8;  // row tiles per raster group of the update
 struct OrthGeom {
   int num_m, num_n, units_per, num_units, k_blocks;
+  int split, part_blocks;  // K blocks shared out in `split` parts, a unit each; all units counted
 };
 struct OrthChain {
   OrthGeom geom[3];
@@ -340,6 +342,7 @@ struct OrthChain {
   __half *hi[2], *lo, *mat[2];  // mat: R, R_B
   float* diag[2];               // D, D_B: [batch][k]
   __nv_bfloat16* out;
+  float* parts;  // partial sums of a split Gram product: 256 x tile width per unit
   int* counter;  // arrivals at the meetings between products; zero at launch
   float co[kMaxOrthSteps][3];
 };

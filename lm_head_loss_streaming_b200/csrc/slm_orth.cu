@@ -186,18 +186,22 @@ __global__ void __launch_bounds__(kPrepThreads) orth_scale(const OrthPrep p, int
 
 // ----------------------------------------------------------------------------------------
 // The products: all of them in one cooperative launch of 2-SM GEMMs (M = 256 rows per CTA pair,
-// fp16 operands).  Warp 0 loads, warp 1 issues the MMAs, sixteen warps run the epilogue, each
-// warpgroup over a quarter of a slot's columns (eight warps took 1.8 times as long: a block of
-// 32 x 32 is 3000 cycles of mostly dependent shared and global memory accesses).  Operands are K-major or MN-major as they lie in memory,
-// so that no transpose of X is ever stored.  Per step:
+// fp16 operands).  Warp 0 loads, warp 1 issues the MMAs, eight warps run the epilogue, each
+// warpgroup over half of a slot's columns (sixteen, with 96 registers a thread, made 2048 x 2048
+// 10% slower and 1024 x 1024 6%).  Operands are K-major or MN-major as they lie in memory, so that
+// no transpose of X is ever stored.  Per step:
 //   kGram    R, D of A = X X^T:  a symmetric product, only blocks on and below the diagonal
 //            are computed and each is written to its mirrored place too
 //   kSquare  R_B, D_B of B = b A + c A^2, symmetric in the same way
 //   kUpdate  hi, lo of a X + B X; in the last step the result in bf16
 // A product reads what the one before wrote anywhere, so the CTAs meet between products (a
 // counter in the workspace, bounded waits; the cooperative launch makes them all resident).
-// A meeting costs about 2 us, a launch of its own with its set-up and drain 7 us: 256 x 256
-// matrices, which are all latency, took 116 us of GPU time in 15 launches.
+// A meeting costs about 2 us, a launch of its own with its set-up and drain 7 us.
+// Where the Gram product has few tiles over a long K (SPLIT), a tile's K blocks are shared out
+// over several pairs, whose fp32 sums go to memory; after another meeting every epilogue warp of
+// the launch adds blocks' parts in order and finishes them.  Five steps with and without:
+// 300 x 8192 174 and 333 us, 100 x 8192 126 and 286, 1024 x 8192 309 and 474, eight of 100 x 4000
+// 188 and 251, 64 x 2048 98 and 120.
 // The tensor memory holds two accumulator slots of BNI columns.  NSUB = 1: tiles take the slots
 // in turn, so that a tile's epilogue overlaps the next tile's MMAs.  NSUB = 2: a tile of 512
 // columns takes both; the operands then cross from L2 at 170 instead of 128 flops per byte, and
@@ -208,7 +212,7 @@ __global__ void __launch_bounds__(kPrepThreads) orth_scale(const OrthPrep p, int
 // hi and lo of that tile stay in the second slot from step to step, two fp16 numbers per
 // 32-bit cell: only hi goes to memory, for the products to read.
 // ----------------------------------------------------------------------------------------
-enum OrthOp { kGram = 0, kSquare = 1, kUpdate = 2 };
+enum OrthOp { kGram = 0, kSquare = 1, kUpdate = 2, kJoin = 3 };
 constexpr int kOrthWG = 2;
 constexpr int kOrthThreads = 64 + 128 * kOrthWG;
 // Meeting of the CTAs between products.
@@ -309,6 +313,18 @@ __device__ __forceinline__ void orth_unit(const OrthGeom& g, int u, int& z, int&
     j = r / gm;
     i = grp * kOrthGroup + (r - j * gm);
   }
+}
+
+// Part of a product's K blocks that unit u covers: its first block and their number; u becomes the
+// tile's number.
+template <bool SPLIT>
+__device__ __forceinline__ int orth_part(const OrthGeom& g, int& u, int& kb0) {
+  kb0 = 0;
+  if (!SPLIT) return g.k_blocks;
+  const int tiles = g.num_units / g.split, part = u / tiles;
+  u -= part * tiles;
+  kb0 = part * g.part_blocks;
+  return min(g.part_blocks, g.k_blocks - kb0);
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
@@ -531,7 +547,8 @@ __device__ __forceinline__ void orth_epilogue(const OrthView& g, uint4* stage, i
   }
 }
 
-template <int BNI, int NSUB, bool TALL>
+// SPLIT: the Gram product's K is split (ch.geom[kGram].split > 1).
+template <int BNI, int NSUB, bool TALL, bool SPLIT>
 __global__ void __launch_bounds__(kOrthThreads, 1)
     orth_chain(const __grid_constant__ OrthChain ch, const __grid_constant__ OrthMaps maps,
                const DevCtl ctl) {
@@ -573,7 +590,13 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   tc_fence_after();
   const uint32_t tmem = pc->tmem_base;
   volatile int* abort = &pc->abort;
-  const int products = 3 * ch.steps;
+  // Phases of a step: the products, and a join after a Gram product whose K is split.
+  constexpr int per_step = SPLIT ? 4 : 3;
+  const int phases = per_step * ch.steps;
+  auto phase_op = [&](int p) {
+    const int r = p % per_step;
+    return !SPLIT || r == 0 ? r : r == 1 ? static_cast<int>(kJoin) : r - 1;
+  };
 
   if (warp == 0) {
     // TMA producer (both CTAs); both CTAs' copies complete on the leader's "full" barrier.
@@ -587,10 +610,11 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
       const CUtensorMap* ma = &maps.a[OP][cur];
       const CUtensorMap* mb = &maps.b[OP][cur];
       for (int u = pair; ok && u < g.num_units; u += npairs) {
-        int z, i, j, nsub;
-        orth_unit<BNI, NSUB, OP != kUpdate>(g, u, z, i, j, nsub);
+        int z, i, j, nsub, tile = u, kb0;
+        const int blocks = orth_part<SPLIT && OP == kGram>(g, tile, kb0);
+        orth_unit<BNI, NSUB, OP != kUpdate>(g, tile, z, i, j, nsub);
         const int mrow = i * 2 * kBM + static_cast<int>(rank) * kBM;
-        for (int kb = 0; kb < g.k_blocks; ++kb, ++it) {
+        for (int kb = kb0; kb < kb0 + blocks; ++kb, ++it) {
           const int s = it % STAGES;
           if (!wait_warp(&pc->empty[s], ((it / STAGES) & 1u) ^ 1u, abort, ctl)) {
             ok = false;
@@ -625,7 +649,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         }
       }
     };
-    for (int p = 0; ok && p < products; ++p) {
+    for (int p = 0; ok && p < phases; ++p) {
       if (p > 0) {
         // This CTA's part of the product before is in memory; wait for the others' and let the
         // epilogue know.
@@ -639,13 +663,13 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         __syncwarp();
         if (!ok) break;
       }
-      const int cur = (p / 3) & 1;
-      if (p % 3 == 0)
-        product(std::integral_constant<int, kGram>{}, cur);
-      else if (p % 3 == 1)
+      const int step = p / per_step, op = phase_op(p);
+      if (op == kGram)
+        product(std::integral_constant<int, kGram>{}, step & 1);
+      else if (op == kSquare)
         product(std::integral_constant<int, kSquare>{}, 0);
-      else
-        product(std::integral_constant<int, kUpdate>{}, cur);
+      else if (op == kUpdate)
+        product(std::integral_constant<int, kUpdate>{}, step & 1);
     }
     if (ok) {
       // No remote release of a stage may reach this CTA after it has exited: wait for the
@@ -689,8 +713,9 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
           }
         };
         for (int u = pair; u < g.num_units; u += npairs, ++t) {
-          int z, i, j, nsub;
-          orth_unit<BNI, NSUB, OP != kUpdate>(g, u, z, i, j, nsub);
+          int z, i, j, nsub, tile = u, kb0;
+          const int blocks = orth_part<SPLIT && OP == kGram>(g, tile, kb0);
+          orth_unit<BNI, NSUB, OP != kUpdate>(g, tile, z, i, j, nsub);
           const int b0 = NSUB == 2 || ch.resident ? 0 : static_cast<int>(t & 1u);
           uint32_t& used = b0 ? used1 : used0;
           ok = wait_warp(&pc->tempty[b0], (used & 1u) ^ 1u, abort, ctl);
@@ -701,7 +726,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
           if (NSUB == 2 && nsub == 2) {
             // The first slot over the stages that are there already, then, once the second
             // slot is free, its MMAs for them, with the stages' releases.
-            const int pre = min(STAGES, g.k_blocks);
+            const int pre = min(STAGES, blocks);
             for (; kb < pre; ++kb) {
               const uint32_t q = it + kb;
               ok = wait_warp(&pc->full[q % STAGES], (q / STAGES) & 1u, abort, ctl);
@@ -722,7 +747,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
               __syncwarp();
             }
           }
-          for (; kb < g.k_blocks; ++kb, ++it) {
+          for (; kb < blocks; ++kb, ++it) {
             const int s = it % STAGES;
             ok = wait_warp(&pc->full[s], (it / STAGES) & 1u, abort, ctl);
             if (!ok) return;
@@ -741,12 +766,13 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
           __syncwarp();
         }
       };
-      for (int p = 0; ok && p < products; ++p) {
-        if (p % 3 == 0)
+      for (int p = 0; ok && p < phases; ++p) {
+        const int op = phase_op(p);
+        if (op == kGram)
           product(std::integral_constant<int, kGram>{});
-        else if (p % 3 == 1)
+        else if (op == kSquare)
           product(std::integral_constant<int, kSquare>{});
-        else
+        else if (op == kUpdate)
           product(std::integral_constant<int, kUpdate>{});
       }
       // Every MMA must be complete (in both CTAs' TMEM) before TMEM is released.
@@ -765,6 +791,11 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     const uint32_t tempty1 = mapa_shared(smem_u32(&pc->tempty[1]), 0);
     uint32_t t = 0, used0 = 0, used1 = 0;
     bool ok = true;
+    // Where block (rows, cols) of 32 x 32 of unit u's partial sums lies.
+    auto part_block = [&](int u, int rows, int cols) {
+      return reinterpret_cast<float4*>(ch.parts) +
+             ((static_cast<int64_t>(u) * 8 + rows) * (BNI / 32) + cols) * 256;
+    };
     auto product = [&](auto opc, auto lastc, auto fromc, auto toc, int step) {
       constexpr int OP = decltype(opc)::value;
       constexpr bool LAST = decltype(lastc)::value;
@@ -784,8 +815,9 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
                        ch.co[step][0],
                        ch.co[step][1], ch.co[step][2], ch.out_vec};
       for (int u = pair; ok && u < geo.num_units; u += npairs, ++t) {
-        int z, i, j, nsub;
-        orth_unit<BNI, NSUB, kSym>(geo, u, z, i, j, nsub);
+        int z, i, j, nsub, tile = u, kb0;
+        orth_part<SPLIT && OP == kGram>(geo, tile, kb0);
+        orth_unit<BNI, NSUB, kSym>(geo, tile, z, i, j, nsub);
         const int row = i * 2 * kBM + static_cast<int>(rank) * kBM + q * 32 + lane;
         float drow = 0.f;
         if (OP == kSquare || (OP == kUpdate && !TALL))
@@ -816,7 +848,14 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
               if (lane == 0 && !(ctl.fault == 1 && t == 0))
                 mbar_arrive_cluster(b ? tempty1 : tempty0);
             }
-            if (col0 + c * 32 < g.cols)
+            if (SPLIT && OP == kGram) {
+              // A part of the sum, for the join: a block's piece e of row r at e * 32 + r.
+              float4* const at = part_block(u, static_cast<int>(rank) * 4 + q,
+                                            wg * kChunks + c) + lane;
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                at[e * 32] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            } else if (col0 + c * 32 < g.cols)
               orth_epilogue<OP, LAST, TALL, FROM, TO>(g, stage, z, row, col0 + c * 32,
                                             c + 1 < kChunks ? col0 + (c + 1) * 32 : -1, mirror,
                                             drow, in,
@@ -825,17 +864,50 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         }
       }
     };
-    for (int p = 0; ok && p < products; ++p) {
+    // The parts of a split Gram product, added in order; every warp of the launch takes blocks.
+    auto join = [&]() {
+      const OrthGeom& geo = ch.geom[kGram];
+      const OrthView g{ch.k, ch.k, ch.ldk, ch.k, nullptr, nullptr, nullptr, ch.diag[0],
+                       ch.mat[0], 0.f, 0.f, 0.f, 0};
+      const int tiles = geo.num_units / geo.split, warps = 4 * kOrthWG;
+      for (int blk = (warp - 2) * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+           blk < tiles * (8 * BNI / 32); blk += warps * static_cast<int>(gridDim.x)) {
+        const int tile = blk / (8 * BNI / 32), r = blk / (BNI / 32) % 8, c = blk % (BNI / 32);
+        int z, i, j, nsub;
+        orth_unit<BNI, NSUB, true>(geo, tile, z, i, j, nsub);
+        const int row = i * 2 * kBM + r * 32 + lane, col = j * BNI + c * 32;
+        if (row - lane >= g.rows || col >= g.cols) continue;
+        float v[32] = {};
+#pragma unroll 4
+        for (int s = 0; s < geo.split; ++s) {
+          const float4* const at = part_block(s * tiles + tile, r, c) + lane;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 f = at[e * 32];
+            v[4 * e] += f.x;
+            v[4 * e + 1] += f.y;
+            v[4 * e + 2] += f.z;
+            v[4 * e + 3] += f.w;
+          }
+        }
+        OrthIn<kGram, TALL, false> in;
+        orth_epilogue<kGram, false, TALL, false, false>(
+            g, stage, z, row, col, -1, j * BNI + BNI <= i * 2 * kBM, 0.f, in, 0u, v);
+      }
+    };
+    for (int p = 0; ok && p < phases; ++p) {
       if (p > 0) ok = wait_warp(&pc->met, (p - 1) & 1, abort, ctl);
       if (!ok) break;
-      const int step = p / 3;
+      const int step = p / per_step, op = phase_op(p);
       constexpr std::false_type no{};
       constexpr std::true_type yes{};
       constexpr std::integral_constant<int, kUpdate> up{};
       const bool last = step + 1 == ch.steps;
-      if (p % 3 == 0) {
+      if (op == kGram) {
         product(std::integral_constant<int, kGram>{}, no, no, no, step);
-      } else if (p % 3 == 1) {
+      } else if (op == kJoin) {
+        if constexpr (SPLIT) join();
+      } else if (op == kSquare) {
         product(std::integral_constant<int, kSquare>{}, no, no, no, step);
       } else if (NSUB == 1 && ch.resident) {
         if (step == 0)
@@ -866,11 +938,11 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
-template <int BNI, int NSUB, bool TALL>
+template <int BNI, int NSUB, bool TALL, bool SPLIT>
 cudaError_t launch_chain(const OrthChain& ch, const OrthMaps& maps, const DevCtl& c,
                          cudaStream_t s) {
   using C = OrthCfg<BNI, NSUB>;
-  auto kern = orth_chain<BNI, NSUB, TALL>;
+  auto kern = orth_chain<BNI, NSUB, TALL, SPLIT>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -1390,14 +1462,18 @@ cudaError_t launch_orth_prep(int dtype, const OrthPrep& p, int64_t batch, cudaSt
 
 cudaError_t launch_orth_chain(int bn, bool tall, const OrthChain& ch, const OrthMaps& maps,
                               const DevCtl& c, cudaStream_t s) {
+  auto run = [&](auto tallc, auto splitc) {
+    constexpr bool T = decltype(tallc)::value, S = decltype(splitc)::value;
+    return bn == 256 ? launch_chain<256, 1, T, S>(ch, maps, c, s)
+                     : launch_chain<128, 1, T, S>(ch, maps, c, s);
+  };
+  constexpr std::false_type no{};
+  constexpr std::true_type yes{};
   if (bn == 512)
-    return tall ? launch_chain<256, 2, true>(ch, maps, c, s)
-                : launch_chain<256, 2, false>(ch, maps, c, s);
-  if (bn == 256)
-    return tall ? launch_chain<256, 1, true>(ch, maps, c, s)
-                : launch_chain<256, 1, false>(ch, maps, c, s);
-  return tall ? launch_chain<128, 1, true>(ch, maps, c, s)
-              : launch_chain<128, 1, false>(ch, maps, c, s);
+    return tall ? launch_chain<256, 2, true, false>(ch, maps, c, s)
+                : launch_chain<256, 2, false, false>(ch, maps, c, s);
+  if (ch.geom[kGram].split > 1) return tall ? run(yes, yes) : run(no, yes);
+  return tall ? run(yes, no) : run(no, no);
 }
 
 }  // namespace slm

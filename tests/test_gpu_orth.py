@@ -229,3 +229,21 @@ def test_many_calls_on_several_streams():
     torch.cuda.synchronize()
     for i in range(4):
         assert all(torch.equal(g, want[i]) for g in got[i])
+
+
+# Few tiles over a long side: the Gram product's long axis is shared out.  Parts that end inside a
+# 64-wide K block, one or several tiles, one or several matrices, with and without room for X's
+# tiles in tensor memory.
+@pytest.mark.parametrize("batch,m,n", [(1, 64, 2048), (1, 2049, 64), (1, 300, 8192), (1, 8191, 300),
+                                       (2, 130, 4100), (3, 4097, 257), (8, 100, 4000),
+                                       (1, 520, 5001), (1, 5003, 1000), (1, 3, 20000)])
+def test_long_axis_in_parts(batch, m, n):
+    g = torch.stack([spectrum(m, n, "noise", 7 + i) for i in range(batch)]).to(BF)
+    got = orthogonalize(g)
+    for i in range(batch):
+        check(got[i], g[i])
+    assert torch.equal(got, orthogonalize(g))
+
+
+def test_long_axis_in_parts_wait_runs_out():
+    test_wait_runs_out_reports_timeout_and_the_next_call_is_right((300, 6000))
