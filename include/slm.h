@@ -434,8 +434,8 @@ SLM_API int slm_block_norm_bwd(int dtype, const void* x, int64_t ldx, const void
  *   workspace at least slm_orthogonalize_workspace_bytes(batch, m, n) bytes, 256-byte aligned;
  *             its first word is the status word that slm_device_status reads.
  * The products' operands are fp16 with fp32 accumulators; X is kept to 22 bits and the
- * diagonals of A and B in fp32, so that the result is within about 2e-3 (Frobenius, relative)
- * of the exact iteration on grad, the bf16 rounding of out (1.7e-3) included.  A matrix of
+ * diagonals of A and B in fp32, so that the result is within about 2.2e-3 (Frobenius,
+ * relative) of the exact iteration on grad, the bf16 rounding of out (1.7e-3) included.  A matrix of
  * zeros gives zeros; one with a NaN or an infinity gives NaN throughout, and no other matrix of
  * the stack is touched by it.  Matrices with ||u||_F far below eps lose relative precision
  * (their X is below 2^-28).  batch, m or n = 0: nothing is done.

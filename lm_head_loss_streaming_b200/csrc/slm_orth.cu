@@ -18,7 +18,8 @@
 //     multiply-add in the epilogues:  with A = D + R,
 //         A^2 = R R + (D_i + D_j) R + D^2,    B X = R_B hi + D_B hi.
 //     (D_B multiplies hi, not hi + lo: B must act on one and the same X in all its terms, or
-//     the difference's noise reaches directions that B alone would not touch.)
+//     the difference's noise reaches directions that B alone would not touch.  orth_small has
+//     room for B (hi + lo) where k <= 128.)
 //   - hi, lo and the matrices are stored times a power of two (kScaleX, kScaleA, kScaleB), so
 //     that fp16's exponent range covers them: |X|, |A| < 4 and |B| < 16 fit, which the host
 //     checks of the coefficients, and entries down to 2^-28 are normal numbers.
@@ -991,6 +992,9 @@ cudaError_t launch_chain(const OrthChain& ch, const OrthMaps& maps, const DevCtl
 //   mat     its 128 rows of R, then of R_B in place, K-major: both operands of R R, and the
 //           update's A operand
 //   tensor memory  256 columns of accumulator, 256 of hi and lo, two fp16 numbers per cell
+// With k <= 128 the second half of cols' rows holds lo, and B acts on hi + lo: small matrices have
+// few roundings to average over, and this halves their error (16 x 23 noise, mean over 20: 1.7e-3
+// to 1.0e-3 before the rounding to bf16).
 // An epilogue writes the next product's operands where the MMAs read them (a row of `cols` goes to
 // the CTA that holds those columns), and a product starts when the epilogue warps of the pair have
 // arrived.  A step of 256 x 256 takes 15.5 us: 4.6 of MMAs and their start, 7 of epilogue
@@ -999,8 +1003,8 @@ cudaError_t launch_chain(const OrthChain& ch, const OrthMaps& maps, const DevCtl
 // 16 columns each, so that a narrow matrix uses them all, and global memory by way of shared memory
 // 32 B at a time: eight warps of 128 columns, whose lanes read and wrote a row each, took 53 us for
 // 64 x 64 and 131 for 256 x 256.  Graph replay, this kernel and orth_chain with its two launches
-// before: 64 x 64 43 and 66 us, 16 x 200 60 and 62, 256 x 256 92 and 99, a hundred of 128 x 128 119
-// and 145, a hundred of 256 x 256 186 and 225.
+// before: 64 x 64 45 and 66 us, 16 x 200 64 and 62, 256 x 256 90 and 99, a hundred of 128 x 128 127
+// and 145, a hundred of 256 x 256 182 and 225.
 // ----------------------------------------------------------------------------------------
 constexpr int kSmallWarps = 16;  // epilogue warps per CTA
 constexpr int kSmallThreads = 32 + 32 * kSmallWarps;
@@ -1051,7 +1055,8 @@ __device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, done);
 }
 
-template <class T>
+// BOTH: k <= 128, and the update multiplies lo too, by the rows of cols behind hi's.
+template <class T, bool BOTH>
 __global__ void __launch_bounds__(kSmallThreads, 1)
     orth_small(const __grid_constant__ OrthSmall p, const DevCtl ctl) {
   extern __shared__ uint8_t smem_raw[];
@@ -1198,6 +1203,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
                                     ? smem_desc_sw128(b + kk * 2048, 2 * kSmallBlock, 1024)
                                     : smem_desc_sw128(b + (kk >> 2) * kSmallBlock + (kk & 3) * 32, 16, 1024);
             umma_bf16_pair(tmem, ad, bd, op == kUpdate ? kUpd : kSym, kk != 0 ? 1u : 0u);
+            if (op == kUpdate && BOTH)
+              umma_bf16_pair(tmem, ad, smem_desc_sw128(b + (kk + 8) * 2048, 2 * kSmallBlock, 1024),
+                             kUpd, 1u);
           }
           umma_commit_pair_mc(&sc->tfull, 0x3);
         }
@@ -1219,21 +1227,27 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
       __syncwarp();
       if (lane < 2 && !withhold) mbar_arrive_cluster(mapa_shared(smem_u32(&sc->ready[t & 1]), lane));
     };
-    // hi (8 pairs of columns from col) to `rows` and to the CTA that holds the columns.
+    // 8 pairs of columns from col to the CTA that holds the columns, as its row r, ...
     const uint32_t cols_far = mapa_shared(smem_u32(cols), rank ^ 1);
-    auto put_hi = [&](int col, const uint32_t(&hi)[8]) {
+    auto put_cols = [&](int r, int col, const uint32_t(&w)[8]) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int piece = col / 8 + e;
-        *reinterpret_cast<uint4*>(rows + small_at(128, row, piece)) =
-            make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
-        const uint32_t at = small_at(256, grow, piece & 15);
+        const uint32_t at = small_at(256, r, (col / 8 + e) & 15);
         if ((col < 128) == (rank == 0))
           *reinterpret_cast<uint4*>(cols + at) =
-              make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
+              make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
         else
-          st_cluster_v4(cols_far + at, hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
+          st_cluster_v4(cols_far + at, w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
       }
+    };
+    // ... and the products' operands: hi, and lo where it takes part.
+    auto put = [&](int col, const uint32_t(&hi)[8], const uint32_t(&lo)[8]) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        *reinterpret_cast<uint4*>(rows + small_at(128, row, col / 8 + e)) =
+            make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
+      put_cols(grow, col, hi);
+      if (BOTH) put_cols(128 + grow, col, lo);
     };
     auto put_cells = [&](uint32_t at, const uint32_t(&hi)[8], const uint32_t(&lo)[8]) {
       uint32_t w[16];
@@ -1260,7 +1274,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
         split(make_float2(__uint_as_float(w[2 * h]) * inv, __uint_as_float(w[2 * h + 1]) * inv),
               hi[h], lo[h]);
       put_cells(master + col, hi, lo);
-      put_hi(col, hi);
+      put(col, hi, lo);
     }
     tmem_st_wait();
     arrive(0, false);
@@ -1274,6 +1288,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
       if (!wait_warp(&sc->tfull, t & 1, abort, ctl)) break;
       tc_fence_after();
       const float drow = op == kSquare ? sc->d[grow] : op == kUpdate ? sc->db[row] : 0.f;
+      const float on_hi = drow + a, on_lo = BOTH ? on_hi : a;
       const int end = !live ? 0 : op == kUpdate ? l : k;
 #pragma unroll 1
       for (int col = col0; col < end; col += kSmallStride) {
@@ -1289,9 +1304,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
             const float2 r = __ffma2_rn(
                 x, both(1.f / kScaleB),
                 __ffma2_rn(unpack_half2(__byte_perm(w[2 * h], w[2 * h + 1], 0x5410)),
-                           __fadd2_rn(both(drow), both(a)),
+                           both(on_hi),
                            __fmul2_rn(unpack_half2(__byte_perm(w[2 * h], w[2 * h + 1], 0x7632)),
-                                      both(a))));
+                                      both(on_lo))));
             if (last)
               hi[h] = pack_bf162(r.x * (1.f / kScaleX), r.y * (1.f / kScaleX));
             else
@@ -1318,7 +1333,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
             }
           } else {
             put_cells(master + col, hi, lo);
-            put_hi(col, hi);
+            put(col, hi, lo);
           }
           __syncwarp();
           continue;
@@ -1396,7 +1411,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   if (warp == 0) tmem_dealloc_pair(tmem, 512);
 }
 
-template <class T>
+template <class T, bool BOTH>
 cudaError_t small_t(const OrthSmall& p, int64_t batch, const DevCtl& c, cudaStream_t s) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1404,7 +1419,7 @@ cudaError_t small_t(const OrthSmall& p, int64_t batch, const DevCtl& c, cudaStre
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   static bool smem_set[64] = {false};  // per device, once
   if (!smem_set[dev]) {
-    e = cudaFuncSetAttribute(orth_small<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(orth_small<T, BOTH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmallSmem));
     if (e != cudaSuccess) return e;
     smem_set[dev] = true;
@@ -1421,16 +1436,21 @@ cudaError_t small_t(const OrthSmall& p, int64_t batch, const DevCtl& c, cudaStre
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, orth_small<T>, p, c);
+  return cudaLaunchKernelEx(&cfg, orth_small<T, BOTH>, p, c);
 }
 
 }  // namespace
 
 cudaError_t launch_orth_small(int dtype, const OrthSmall& p, int64_t batch, const DevCtl& c,
                               cudaStream_t s) {
-  return dtype == 0   ? small_t<__nv_bfloat16>(p, batch, c, s)
-         : dtype == 1 ? small_t<__half>(p, batch, c, s)
-                      : small_t<float>(p, batch, c, s);
+  auto run = [&](auto t) {
+    using T = decltype(t);
+    return std::min(p.m, p.n) <= 128 ? small_t<T, true>(p, batch, c, s)
+                                     : small_t<T, false>(p, batch, c, s);
+  };
+  if (dtype == 0) return run(__nv_bfloat16{});
+  if (dtype == 1) return run(__half{});
+  return run(float{});
 }
 
 cudaError_t launch_orth_prep(int dtype, const OrthPrep& p, int64_t batch, cudaStream_t s) {

@@ -5,7 +5,8 @@ each at its power-of-two scale) are part of what ``slm_orthogonalize`` documents
 the same places, with every sum and product in 64 bits, shows how far these formats alone take
 a result from the exact iteration on the same input.  A kernel that follows them differs from
 that emulation by fp32 sums only (relative 2^-24 per addition, against the operands' 2^-11), so
-its error is another sample of the same size.
+its error is another sample of the same size.  Matrices of up to 256 x 256 with a side of at
+most 128 multiply both fp16 numbers of X in the update, others the first.
 """
 
 import torch
@@ -24,6 +25,7 @@ def iterate(u, rows, eps, formats=False):
     tall = x.shape[0] > x.shape[1]
     if tall:
         x = x.T
+    both = x.shape[0] <= 128 and x.shape[1] <= 256
     for i, (a, b, c) in enumerate(rows):
         if not formats:
             A = x @ x.T
@@ -37,7 +39,8 @@ def iterate(u, rows, eps, formats=False):
         B = b * (R + D.diag()) + c * (R @ R + (D[:, None] + D[None, :]) * R + (D * D).diag())
         DB = B.diagonal().clone()
         RB = _f16(B - DB.diag(), 2.0 ** 12)
-        x = a * x + DB[:, None] * hi + RB @ hi
+        y = x if both else hi
+        x = a * x + DB[:, None] * y + RB @ y
     return x.T if tall else x
 
 
