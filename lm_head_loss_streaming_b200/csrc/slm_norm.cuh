@@ -91,7 +91,9 @@ __device__ __forceinline__ void block_sum(float (&v)[K]) {
 
 // ----------------------------------------------------------------------------------------
 // The kernels for every width, stride and alignment: one row per block, element loads, the
-// row read again (from L1 / L2) for each of its sweeps.
+// row read again (from L1 / L2) for each of its sweeps.  For arrays whose rows do not start equally
+// far from 16-byte boundaries, and rows wider than the kernels below take; bound by its element
+// accesses.  16384 x 4096 bf16: forward 364 us and backward 1778, by pieces 85 and 155.
 // ----------------------------------------------------------------------------------------
 constexpr int kAnyThreads = 256;
 
@@ -460,7 +462,9 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
 
 // Forward by 16-byte pieces: each row is read once into the registers
 // of its threads (NV pieces of x and of y each), and r and h are written from there.  A row is a
-// block's, as many warps as it has pieces for, or, if short (WARP), one warp's of four.
+// block's, as many warps as it has pieces for, or, if short (WARP), one warp's of four.  Bound by
+// memory: x and y in, r and h out.  16384 x 4096 bf16 85 us, 6.3 TB/s; rows that are not 16-byte aligned take
+// masks per element too, which bound 16-bit ones (16384 x 1001 fp32 67 us, 16384 x 4097 bf16 221).  One row of 4096 takes 2.9 us.
 template <class T, int NV, bool WARP, bool SHIFT>
 __global__ void __launch_bounds__(WARP ? 128 : NV == 2 ? 512 : 1024) norm_fwd_vec(const NormFwd p) {
   using P = Piece<T>;
@@ -588,6 +592,10 @@ __global__ void __launch_bounds__(WARP ? 128 : NV == 2 ? 512 : 1024) norm_fwd_ve
 // Sweep 1 over a batch forms the rows' three sums, sweep 2 the outputs, both from the ring.
 // Sweep 1 runs one batch ahead, so that the sums are exchanged behind sweep 2 of the batch
 // before: at most one block barrier per batch, and a cluster's exchange is off the critical path.
+// Bound by memory for fp32 (8192 x 4096 134 us, 6.0 TB/s), by instructions for 16-bit rows
+// (16384 x 4096 bf16 155 us, 5.2 TB/s: twice the conversions and arithmetic per byte, between
+// dependent reads of shared memory).  The general kernels, which read global memory twice, take
+// 1778 us there; sweeps in step, without the batch between them, took 207.
 // Only two parameters per column are needed in the loop: a = bs gate wq (bs wq with a gate per
 // token) and wp.  The group's sum S = sum yh g serves two gradients, which are taken when the
 // group ends:  dgate = bs wq S,  dw_post += bs gate S.
@@ -1164,14 +1172,18 @@ cudaError_t fwd_t(NormFwd p, cudaStream_t s) {
     return cudaGetLastError();
   }
   p.shift0 = static_cast<int>(fit.shift0);
-  // Few rows: as many threads per row as there are pieces, for latency.  Many: two pieces per
-  // thread (four where that takes more than 512 threads), whose loads are in flight together.
+  // Few rows: as many threads per row as there are pieces, for latency (130 x 2048 bf16 2.7 us
+  // against 3.3 with two pieces a thread; 296 x 4096 4.0 and 4.5, but 600 x 4096 7.0 and 6.0).
+  // Many: two pieces per thread, whose loads are in flight together, or four (16384 rows of 16 bits:
+  // width 4608 98 us with two and 100 with four, 5000 114 and 110, 8192 174 and 167; unaligned 4096 x
+  // 5001 64 and 52; fp32 rows of 4096 160 and 165).  Short rows: a warp each (65536 x 256 bf16 26 us, by
+  // blocks 37; 32768 x 512 21 and 24).
   const bool few = p.N <= 2 * sm_count();
   auto warps = [&](int64_t per) { return static_cast<int>((nvec + 32 * per - 1) / (32 * per) * 32); };
   if (nvec <= 32) return fwd_vec<T, 1, true>(p, 128, shift, s);
   if (nvec <= 64 && !few) return fwd_vec<T, 2, true>(p, 128, shift, s);
   if (nvec <= 1024 && few) return fwd_vec<T, 1, false>(p, warps(1), shift, s);
-  if (nvec <= 1024) return fwd_vec<T, 2, false>(p, warps(2), shift, s);
+  if (nvec <= (E == 8 ? 608 : 1024)) return fwd_vec<T, 2, false>(p, warps(2), shift, s);
   return fwd_vec<T, 4, false>(p, warps(4), shift, s);
 }
 
@@ -1228,6 +1240,11 @@ cudaError_t bwd_ring(NormBwd p, const DevCtl& c, int cs, cudaStream_t s) {
   return bwd_sums<T>(p, s);
 }
 
+// Threads per row: as few as keep two pieces each, so that a batch has many rows and few threads
+// share a sum (256 threads for every row: 65536 x 256 bf16 379 us instead of 70, 16384 x 2048 114
+// instead of 85).  One block for a row as long as its registers and ring do (4096 x 5120 62 us, in
+// clusters of two 94; 16384 x 4096 155 and 290), then as few blocks as that leaves (8192 x 16384 409
+// us in clusters of four, 689 of eight).
 template <class T, int GATE, bool SHIFT>
 cudaError_t bwd_vec(const NormBwd& p, int64_t nvec, const DevCtl& c, cudaStream_t s) {
   if (nvec <= 32) return bwd_ring<T, 32, 1, GATE, false, SHIFT>(p, c, 1, s);
