@@ -12,6 +12,7 @@ import functools
 from dataclasses import dataclass
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from .loss import _ptr
@@ -170,6 +171,7 @@ def block_norm_fwd(x, y=None, w_pre=None, w_post=None, gate=None, residual_scale
         raise ValueError("hidden is made by the norm before the next block: there is no w_pre")
     if not eps > 0:
         raise ValueError("eps must be positive")
+    given = []
     if residual is not None or hidden is not None:
         given = [(n, t) for n, t in (("residual", residual), ("hidden", hidden)) if t is not None]
         for name, t in given:
@@ -190,6 +192,8 @@ def block_norm_fwd(x, y=None, w_pre=None, w_post=None, gate=None, residual_scale
                                  stream)
     if st:
         raise _lib.SLMError(st, "slm_block_norm_fwd")
+    for _, t in given:   # written in place: autograd is to know
+        torch.autograd.graph.increment_version(t)
     return BlockNormResult(x if y is None else residual, hidden, stats, residual_scale,
                            block_scale, weight_offset)
 
@@ -214,7 +218,8 @@ def block_norm_bwd(fwd: BlockNormResult, x, y=None, w_pre=None, w_post=None, gat
     if d_hidden is not None:
         ld_dh = _check_rows("d_hidden", d_hidden, N, d, x.dtype, dev)
     stats = fwd.stats
-    if stats.shape != (2, N) or stats.get_device() != dev:
+    if (stats.shape != (2, N) or stats.get_device() != dev or stats.dtype is not torch.float32
+            or not stats.is_contiguous()):
         raise ValueError("fwd does not come from a forward over these inputs")
     device = x.device
     need = _workspace_bytes(N, d, rows if N > 0 else 0)
@@ -253,6 +258,7 @@ class BlockNorm(torch.autograd.Function):
         return None if y is None else fwd.residual, fwd.hidden
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_residual, d_hidden):
         x, y, w_pre, w_post, gate, stats = ctx.saved_tensors
         if d_residual is None and d_hidden is None:

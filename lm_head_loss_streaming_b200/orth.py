@@ -84,10 +84,13 @@ def orthogonalize(grad, momentum=None, beta=0.95, nesterov=True, steps=5,
     elif (workspace.dtype != torch.uint8 or workspace.device != dev
           or not workspace.is_contiguous() or workspace.numel() < need):
         raise ValueError(f"workspace must be a contiguous uint8 tensor of {need} bytes on {dev}")
+    written = [t for t in (momentum, out) if t is not None]
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
     st = _lib.slm_orthogonalize(_DTYPE[grad.dtype], _ptr(grad), ld, stack, batch, m, n,
                                 _ptr(momentum), beta, nesterov, rows, eps, _ptr(out),
                                 _ptr(workspace), workspace.numel(), _stream())
     _lib.check(st, "slm_orthogonalize")
+    for t in written:   # in place: autograd is to know
+        torch.autograd.graph.increment_version(t)
     return out

@@ -360,3 +360,29 @@ def test_other_stream_and_captured_graph():
         for k, v in p.__dict__.items():
             if isinstance(v, torch.Tensor):
                 assert torch.equal(v, getattr(q, k)), k
+
+
+def test_given_outputs_and_second_derivatives_are_known_to_autograd():
+    x, y = (torch.randn(40, 64, device="cuda") for _ in range(2))
+    w = torch.rand(64, device="cuda").requires_grad_()
+    hidden = torch.empty_like(x)
+    block_norm_fwd(x, y, w_pre=w.detach(), hidden=hidden)
+    loss = (hidden * w).sum()                       # keeps hidden for w's gradient
+    block_norm_fwd(y, x, w_pre=w.detach(), hidden=hidden)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    x.requires_grad_()
+    dx, = torch.autograd.grad(block_norm(x, y, w_pre=w)[1].square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        dx.sum().backward()
+
+
+def test_statistics_of_another_type_or_layout_are_refused():
+    x = torch.randn(40, 64, device="cuda")
+    w = torch.rand(64, device="cuda")
+    fwd = block_norm_fwd(x, w_pre=w)
+    from lm_head_loss_streaming_b200.norms import BlockNormResult
+    for stats in (fwd.stats.double(), fwd.stats.repeat(1, 2)[:, ::2]):
+        bad = BlockNormResult(None, None, stats, 1.0, 1.0, 0.0)
+        with pytest.raises(ValueError, match="forward"):
+            block_norm_bwd(bad, x, w_pre=w, d_hidden=x)

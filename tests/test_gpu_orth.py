@@ -247,3 +247,11 @@ def test_long_axis_in_parts(batch, m, n):
 
 def test_long_axis_in_parts_wait_runs_out():
     test_wait_runs_out_reports_timeout_and_the_next_call_is_right((300, 6000))
+
+
+def test_writes_in_place_are_known_to_autograd():
+    g = spectrum(30, 40, "noise", 1).to(F32)
+    mom, out = torch.zeros_like(g), torch.empty(30, 40, dtype=BF, device="cuda")
+    before = mom._version, out._version
+    orthogonalize(g, momentum=mom, out=out)
+    assert mom._version > before[0] and out._version > before[1]
