@@ -377,7 +377,7 @@ typedef enum slm_dtype { SLM_BF16 = 0, SLM_F16 = 1, SLM_F32 = 2 } slm_dtype;
  * All arithmetic is fp32, rounded once per output.  Every alignment and width is accepted;
  * rows that start on 16-byte boundaries and widths of whole 16-byte pieces run fastest.
  * Returns SLM_ERR_KIND for an unknown type, SLM_ERR_SHAPE for bad sizes, strides, gate_rows, a
- * scale that is not finite or eps <= 0, SLM_ERR_NULL for a missing or unusable pointer and
+ * scale that is not finite or eps < 2^-126, SLM_ERR_NULL for a missing or unusable pointer and
  * SLM_ERR_ALIGN for a pointer that is not aligned to its element type. */
 SLM_API int slm_block_norm_fwd(int dtype, const void* x, int64_t ldx, const void* y, int64_t ldy,
                                const void* w_post, const void* w_pre, int w_dtype,
@@ -438,9 +438,10 @@ SLM_API int slm_block_norm_bwd(int dtype, const void* x, int64_t ldx, const void
  * relative) of the exact iteration on grad, the bf16 rounding of out (1.7e-3) included.  A matrix of
  * zeros gives zeros; one with a NaN or an infinity gives NaN throughout, and no other matrix of
  * the stack is touched by it.  Matrices with ||u||_F far below eps lose relative precision
- * (their X is below 2^-28).  batch, m or n = 0: nothing is done.
+ * (their X is below 2^-28), and elements below 2^-126 count as zeros.  batch, m or n = 0:
+ * nothing is done.
  * Returns SLM_ERR_SHAPE for bad sizes (m, n >= 2^30; batch > 65535; 2^30 tiles of 256 x 128 or more),
- * strides, steps, beta outside [0, 1] or eps <= 0; the rest as everywhere. */
+ * strides, steps, beta outside [0, 1] or eps < 2^-126; the rest as everywhere. */
 SLM_API size_t slm_orthogonalize_workspace_bytes(int64_t batch, int64_t m, int64_t n);
 SLM_API int slm_orthogonalize(int dtype, const void* grad, int64_t ld, int64_t batch_stride,
                               int64_t batch, int64_t m, int64_t n, float* momentum, double beta,

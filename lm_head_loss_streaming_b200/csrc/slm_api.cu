@@ -14,6 +14,7 @@
 //   backward  for each token chunk: GEMM recompute of the chunk's logits with the
 //             logits-gradient epilogue (bf16 chunk buffer) -> dH = dZ W -> dW (+)= dZ^T H.
 
+#include <cfloat>
 #include <stdint.h>
 #include <stdio.h>
 #include <string.h>
@@ -1189,7 +1190,7 @@ int slm_block_norm_fwd(int dtype, const void* x, int64_t ldx, const void* y, int
   int st = norm_checks(dtype, x, ldx, y, ldy, w_post, w_pre, w_dtype, gate, gate_dtype, gate_rows,
                        N, d, residual_scale, block_scale, weight_offset);
   if (st != SLM_OK) return st;
-  if (!finite(eps) || eps <= 0.f) return SLM_ERR_SHAPE;
+  if (!finite(eps) || eps < FLT_MIN) return SLM_ERR_SHAPE;
   if (N == 0) return SLM_OK;
   if ((w_pre && !hidden) || (!w_pre && !residual)) return SLM_ERR_NULL;
   const size_t e = elem_bytes(dtype);
@@ -1265,7 +1266,7 @@ int slm_orthogonalize(int dtype, const void* grad, int64_t ld, int64_t batch_str
                       void* workspace, size_t ws_bytes, void* stream) {
   if (!valid_dtype(dtype)) return SLM_ERR_KIND;
   if (!orth_sizes_ok(batch, m, n) || steps < 1 || steps > kMaxOrthSteps || !finite(eps) ||
-      eps <= 0.f || !(beta >= 0.0 && beta <= 1.0))
+      eps < FLT_MIN || !(beta >= 0.0 && beta <= 1.0))
     return SLM_ERR_SHAPE;
   if (!coefficients) return SLM_ERR_NULL;
   if (!orth_coefficients_ok(coefficients, steps)) return SLM_ERR_KIND;

@@ -141,10 +141,18 @@ __global__ void __launch_bounds__(kPrepThreads) orth_moment(const OrthPrep p) {
   }
 }
 
+// The scale kScaleX / (||u|| + eps) as two factors to multiply by in turn, the first a power of
+// two: the scale itself may leave fp32's range where u nearly does.
+__device__ __forceinline__ float2 orth_factors(double sum, float eps) {
+  const double s = kScaleX / (sqrt(sum) + static_cast<double>(eps));
+  const float pre = s > 1e30 ? 0x1p64f : s < 1e-30 ? 0x1p-64f : 1.f;
+  return make_float2(pre, static_cast<float>(s / pre));
+}
+
 // X = u / (||u|| + eps) as hi + lo; the norm from the partial sums, added in a fixed order.
 template <class T, int V>
 __global__ void __launch_bounds__(kPrepThreads) orth_scale(const OrthPrep p, int nsums) {
-  __shared__ float inv_sh;
+  __shared__ float2 inv_sh;
   const int64_t b = blockIdx.y;
   if (threadIdx.x < 32) {
     double t = 0.0;
@@ -152,10 +160,10 @@ __global__ void __launch_bounds__(kPrepThreads) orth_scale(const OrthPrep p, int
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     if (threadIdx.x == 0)
-      inv_sh = static_cast<float>(kScaleX / (sqrt(t) + static_cast<double>(p.eps)));
+      inv_sh = orth_factors(t, p.eps);
   }
   __syncthreads();
-  const float inv = inv_sh;
+  const float2 inv = inv_sh;
   const int64_t groups = p.m * (p.n / V);
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPrepThreads + threadIdx.x; i < groups;
        i += static_cast<int64_t>(gridDim.x) * kPrepThreads) {
@@ -171,7 +179,7 @@ __global__ void __launch_bounds__(kPrepThreads) orth_scale(const OrthPrep p, int
     alignas(16) __half hi[V], lo[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const float x = u[e] * inv;
+      const float x = u[e] * inv.x * inv.y;
       hi[e] = __float2half_rn(x);
       lo[e] = __float2half_rn(x - __half2float(hi[e]));
     }
@@ -1108,7 +1116,6 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16);
   const uint32_t master = acc + 256;
   float* const stage = reinterpret_cast<float*>(smem + max(warp - 1, 0) * kSmallStage);
-  float inv = 0.f;
   if (warp > 0) {
     // u into the cells, momentum updated, the sum of u^2.  Two runs of 16 elements per load, by way
     // of shared memory, element c of row r at c ^ r.  When m > n a lane's row of Y is a column of
@@ -1219,7 +1226,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     double total = 0.0;
 #pragma unroll
     for (int i = 0; i < 2 * kSmallWarps; ++i) total += sc->sums[i];
-    inv = static_cast<float>(kScaleX / (sqrt(total) + static_cast<double>(p.eps)));
+    const float2 inv = orth_factors(total, p.eps);
     // This warp's operands are written: both CTAs' barriers learn of it.
     auto arrive = [&](int t, bool withhold) {
       fence_proxy_async_all();
@@ -1271,7 +1278,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
       tmem_ld_wait();
 #pragma unroll
       for (int h = 0; h < 8; ++h)
-        split(make_float2(__uint_as_float(w[2 * h]) * inv, __uint_as_float(w[2 * h + 1]) * inv),
+        split(make_float2(__uint_as_float(w[2 * h]) * inv.x * inv.y,
+                          __uint_as_float(w[2 * h + 1]) * inv.x * inv.y),
               hi[h], lo[h]);
       put_cells(master + col, hi, lo);
       put(col, hi, lo);

@@ -169,8 +169,8 @@ def block_norm_fwd(x, y=None, w_pre=None, w_post=None, gate=None, residual_scale
             raise ValueError("residual is an output of the block's add: there is none without y")
     if w_pre is None and hidden is not None:
         raise ValueError("hidden is made by the norm before the next block: there is no w_pre")
-    if not eps > 0:
-        raise ValueError("eps must be positive")
+    if not eps >= 2.0 ** -126:
+        raise ValueError("eps must be positive, and normal in float32")
     given = []
     if residual is not None or hidden is not None:
         given = [(n, t) for n, t in (("residual", residual), ("hidden", hidden)) if t is not None]

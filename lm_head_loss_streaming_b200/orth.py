@@ -64,8 +64,8 @@ def orthogonalize(grad, momentum=None, beta=0.95, nesterov=True, steps=5,
     rows = _steps(coefficients, steps)
     if not 0.0 <= beta <= 1.0:
         raise ValueError("beta must be within [0, 1]")
-    if not eps > 0:
-        raise ValueError("eps must be positive")
+    if not eps >= 2.0 ** -126:
+        raise ValueError("eps must be positive, and normal in float32")
     for name, t, dtype in (("momentum", momentum, torch.float32), ("out", out, torch.bfloat16)):
         if t is None:
             continue

@@ -255,3 +255,14 @@ def test_writes_in_place_are_known_to_autograd():
     before = mom._version, out._version
     orthogonalize(g, momentum=mom, out=out)
     assert mom._version > before[0] and out._version > before[1]
+
+
+@pytest.mark.parametrize("m,n", [(40, 64), (40, 300)])
+@pytest.mark.parametrize("size", [1e-37, 2e38])
+def test_scales_beyond_fp32(m, n, size):
+    """||u|| whose reciprocal, or its product with the kernels' scale, leaves fp32."""
+    g = spectrum(m, n, "noise", 3)
+    g = (g / g.abs().max() * size).to(F32)
+    u = g.where(g.abs() >= 2.0 ** -126, 0)     # subnormal elements count as zeros
+    check(orthogonalize(g, eps=2e-38), u, eps=2e-38)
+    assert not orthogonalize(torch.zeros_like(g), eps=2e-38).any()

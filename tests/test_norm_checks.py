@@ -121,3 +121,8 @@ def test_wrapper_refusals():
             block_norm_bwd(f, **{**ok, **kw})
     with pytest.raises(ValueError):
         block_norm_bwd(BlockNormResult(x, x, torch.empty(2, 5, device="cuda"), 1.0, 1.0, 0.0), **ok, **g)
+
+
+def test_subnormal_eps_is_refused():
+    """The kernel would take it for zero."""
+    assert _fwd(eps=1e-42) == 2

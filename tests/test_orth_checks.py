@@ -96,3 +96,8 @@ def test_wrapper_refusals():
         orthogonalize(bf, out=bf)
     with pytest.raises(_lib.SLMError):
         orthogonalize(g, coefficients=(3.0, 0.0, 0.0))
+
+
+def test_subnormal_eps_is_refused():
+    """The kernels would take it for zero."""
+    assert _call(eps=1e-42) == 2
