@@ -24,6 +24,7 @@
 #include <type_traits>
 
 #include "slm_internal.h"
+#include "slm_norm_rows.h"
 #include "slm_wait.cuh"
 #include "sm100.cuh"
 
@@ -92,7 +93,8 @@ __device__ __forceinline__ void block_sum(float (&v)[K]) {
 // ----------------------------------------------------------------------------------------
 // The kernels for every width, stride and alignment: one row per block, element loads, the
 // row read again (from L1 / L2) for each of its sweeps.  For arrays whose rows do not start equally
-// far from 16-byte boundaries, and rows wider than the kernels below take; bound by its element
+// far from 16-byte boundaries, rows wider than the kernels below take, and in the backward rows
+// narrower than a piece; bound by its element
 // accesses.  16384 x 4096 bf16: forward 364 us and backward 1778, by pieces 85 and 155.
 // ----------------------------------------------------------------------------------------
 constexpr int kAnyThreads = 256;
@@ -604,7 +606,7 @@ __global__ void __launch_bounds__(WARP ? 128 : NV == 2 ? 512 : 1024) norm_fwd_ve
 //   SHIFT  rows do not all start on 16-byte boundaries: a worker takes rows n = class (mod
 //          `classes`) only, which start equally far from one, so that its threads keep their
 //          columns; the copied windows reach into the neighbouring rows, whose elements are
-//          masked
+//          masked (rows narrower than a piece go to the general kernels: slm_norm_rows.h)
 // ----------------------------------------------------------------------------------------
 constexpr int kRingThreads = 256;  // computing threads (more where one row takes more)
 constexpr int kRingMost = 352;     // 11 warps and the copying one: still 168 registers a thread
@@ -731,14 +733,12 @@ __global__ void __launch_bounds__((TPR > kRingThreads ? TPR : kRingThreads) + 32
                 : arr == 3 ? (pre ? p.d_hidden : nullptr) : GATE ? p.gate : nullptr;
           ld = arr == 0 ? p.ldx : arr == 1 ? p.ldy : arr == 2 ? p.ld_dr : arr == 3 ? p.ld_dh : p.d;
         };
-        // Pieces [lo, hi) of row `row` that this block copies whole.  Of the arrays' first row
-        // and last row, a piece that reaches outside the array is not.
+        // Pieces [lo, hi) of row `row` that this block copies whole.
         auto whole = [&](int64_t row, int& lo, int& hi) {
-          lo = piece0;
-          hi = piece0 + mine;
-          if (SHIFT && row == 0 && shift > 0) lo = max(lo, 1);
-          if (SHIFT && row == p.N - 1) hi = min(hi, static_cast<int>((p.d + shift) / P::kElems));
-          hi = max(lo, hi);
+          const NormWindow w = SHIFT ? norm_window(row, p.N, p.d, shift, P::kElems, piece0, mine)
+                                     : NormWindow{piece0, piece0 + mine};
+          lo = w.lo;
+          hi = w.hi;
         };
         uint32_t bytes = 0;
         for (int rw = 0; rw < valid; ++rw) {
@@ -1279,7 +1279,7 @@ cudaError_t bwd_t(NormBwd p, const DevCtl& c, cudaStream_t s) {
   // A shared gate with more groups than can be split by row class is left to the general path.
   if (shift && p.plan.shared_gate) fit.ok = fit.ok && p.plan.groups * E <= kNormBlocks;
   const int64_t nvec = shift ? (p.d + 2 * E - 2) / E : p.d / E;  // the most that a row has
-  if (fit.ok && nvec <= 2 * kRingThreads * kMaxCluster) {
+  if (fit.ok && norm_ring_takes(p.d, E) && nvec <= 2 * kRingThreads * kMaxCluster) {
     p.shift0 = static_cast<int>(fit.shift0);
     if (!token)
       return shift ? bwd_vec<T, 0, true>(p, nvec, c, s) : bwd_vec<T, 0, false>(p, nvec, c, s);
