@@ -607,6 +607,8 @@ __global__ void __launch_bounds__(WARP ? 128 : NV == 2 ? 512 : 1024) norm_fwd_ve
 //          `classes`) only, which start equally far from one, so that its threads keep their
 //          columns; the copied windows reach into the neighbouring rows, whose elements are
 //          masked (rows narrower than a piece go to the general kernels: slm_norm_rows.h)
+//   PRE    there is the second norm.  Without it nothing depends on r, which must not be formed: an
+//          infinite y would make it infinite, and its zero factors would make NaN of that
 // ----------------------------------------------------------------------------------------
 constexpr int kRingThreads = 256;  // computing threads (more where one row takes more)
 constexpr int kRingMost = 352;     // 11 warps and the copying one: still 168 registers a thread
@@ -653,7 +655,7 @@ __device__ __forceinline__ float warp_sum3(float v0, float v1, float v2, int lan
   return k;
 }
 
-template <class T, int TPR, int NV, int GATE, bool CL, bool SHIFT>
+template <class T, int TPR, int NV, int GATE, bool CL, bool SHIFT, bool PRE>
 __global__ void __launch_bounds__((TPR > kRingThreads ? TPR : kRingThreads) + 32, 1)
     norm_bwd_ring(const NormBwd p, const DevCtl ctl, const int seg) {
   using P = Piece<T>;
@@ -679,7 +681,9 @@ __global__ void __launch_bounds__((TPR > kRingThreads ? TPR : kRingThreads) + 32
   const int nvec = static_cast<int>((p.d + shift + P::kElems - 1) / P::kElems);
   const int piece0 = rank * seg;
   const int mine = max(0, min(seg, nvec - piece0));
-  const bool has_y = p.y != nullptr, has_dr = p.d_residual != nullptr, pre = p.w_pre != nullptr;
+  const bool has_y = p.y != nullptr, has_dr = p.d_residual != nullptr;
+  // Always PRE; as a constant in that variant it changed ptxas's schedule (16384 x 4096 168 us, not 156).
+  const bool pre = PRE && p.w_pre != nullptr;
   volatile int* abort = &rc->abort;
 
   // The status word is cleared here, without a launch for it: a wait can only run out long
@@ -950,7 +954,7 @@ __global__ void __launch_bounds__((TPR > kRingThreads ? TPR : kRingThreads) + 32
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         ay[k] = mul2(GATE ? mul2(a[v][k], gate[k]) : a[v][k], iy);
-        r[k] = fma2(rs, r[k], mul2(ay[k], y[k]));
+        r[k] = PRE ? fma2(rs, r[k], mul2(ay[k], y[k])) : zero;
       }
     };
     // Sweep 1: sum u r, sum a yh (dr + i_r u), sum a yh r over the rows of the batch, handed on
@@ -1197,10 +1201,10 @@ cudaError_t bwd_sums(const NormBwd& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <class T, int TPR, int NV, int GATE, bool CL, bool SHIFT>
-cudaError_t bwd_ring(NormBwd p, const DevCtl& c, int cs, cudaStream_t s) {
+template <class T, int TPR, int NV, int GATE, bool CL, bool SHIFT, bool PRE>
+cudaError_t bwd_ring_t(NormBwd p, const DevCtl& c, int cs, cudaStream_t s) {
   using C = RingCfg<T, TPR, NV, GATE>;
-  auto kern = norm_bwd_ring<T, TPR, NV, GATE, CL, SHIFT>;
+  auto kern = norm_bwd_ring<T, TPR, NV, GATE, CL, SHIFT, PRE>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -1238,6 +1242,12 @@ cudaError_t bwd_ring(NormBwd p, const DevCtl& c, int cs, cudaStream_t s) {
   cfg.gridDim = dim3(static_cast<unsigned>(p.plan.blocks * cs), 1, 1);
   if ((e = cudaLaunchKernelEx(&cfg, kern, p, c, (nvec + cs - 1) / cs)) != cudaSuccess) return e;
   return bwd_sums<T>(p, s);
+}
+
+template <class T, int TPR, int NV, int GATE, bool CL, bool SHIFT>
+cudaError_t bwd_ring(const NormBwd& p, const DevCtl& c, int cs, cudaStream_t s) {
+  return p.w_pre ? bwd_ring_t<T, TPR, NV, GATE, CL, SHIFT, true>(p, c, cs, s)
+                 : bwd_ring_t<T, TPR, NV, GATE, CL, SHIFT, false>(p, c, cs, s);
 }
 
 // Threads per row: as few as keep two pieces each, so that a batch has many rows and few threads
