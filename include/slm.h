@@ -37,7 +37,8 @@
  *     H_q, H_p [N, d]; W [V, d]; dH_q [N, d].  Every tensor base must be 16-byte aligned
  *     and d must be a multiple of 8 (16-byte rows for the tensor-memory-access engine).
  *   - `stream` is a cudaStream_t (NULL = legacy default stream).  All work is enqueued
- *     asynchronously on it; no entry point synchronises, except slm_device_status.
+ *     asynchronously on it; no entry point synchronises, except slm_device_status and
+ *     slm_operator_status.
  *   - Errors found on the host (null pointer, bad shape or alignment, small workspace,
  *     wrong kind, unsupported GPU, CUDA launch error) are returned immediately and nothing
  *     is enqueued.  Errors found on the device (a label outside [0, V) that is not
@@ -447,6 +448,13 @@ SLM_API int slm_orthogonalize(int dtype, const void* grad, int64_t ld, int64_t b
                               int64_t batch, int64_t m, int64_t n, float* momentum, double beta,
                               int nesterov, const float* coefficients, int steps, float eps,
                               void* out, void* workspace, size_t ws_bytes, void* stream);
+
+/* Whether a wait of slm_block_norm_bwd or slm_orthogonalize ran out (SLM_ERR_TIMEOUT) on the
+ * current device since this was last asked: in any call, whichever workspace it had and whether
+ * or not that is still there, as far as the call has finished.  The outputs of such a call are
+ * undefined, a momentum among them: it may have been advanced, and a caller who wants to repeat
+ * the call needs the old one.  Synchronises `stream`, and clears what it reports. */
+SLM_API int slm_operator_status(void* stream);
 
 /* Test hook for the device-side failure path (not for production use).  fault_mode 1 makes
  * every following launch withhold one internal pipeline release, so that a bounded wait in

@@ -15,7 +15,7 @@ def __getattr__(name):
     # The binding and the autograd wrapper load the native library lazily, so the
     # input generators stay importable on machines without the built extension.
     if name in ("streaming_lm_head_loss", "StreamingLMHeadLoss", "lm_head_loss_fwd",
-                "lm_head_loss_bwd"):
+                "lm_head_loss_bwd", "device_status"):
         from . import loss as _loss
         return getattr(_loss, name)
     if name in ("block_norm", "block_norm_fwd", "block_norm_bwd"):

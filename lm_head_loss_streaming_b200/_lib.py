@@ -54,6 +54,7 @@ SIGNATURES = {
                                     _P, _INT]),
     "slm_chunk_for_budget": (_I64, [_INT, _I64, _I64, _I64, _SZ, _INT]),
     "slm_device_status": (_INT, [_P, _P]),
+    "slm_operator_status": (_INT, [_P]),
     "slm_debug_set": (_INT, [_INT, ctypes.c_longlong]),
     "slm_fused_workspace_bytes": (_SZ, [_INT, _I64, _I64, _I64, _I64]),
     "slm_loss_fwd_bwd": (_INT, [_INT, _P, _P, _P, _P, _I32, _I64, _I64, _I64, _P, _P,
@@ -177,6 +178,10 @@ def slm_chunk_for_budget(kind, N, d, V, budget_bytes, fused=False):
 
 def slm_device_status(workspace, stream):
     return load().slm_device_status(workspace, stream)
+
+
+def slm_operator_status(stream):
+    return load().slm_operator_status(stream)
 
 
 def slm_debug_set(fault_mode, timeout_cycles=0):

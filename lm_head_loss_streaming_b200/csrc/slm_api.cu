@@ -403,7 +403,7 @@ FusedLayout fused_layout(int kind, int64_t N, int64_t V, int64_t chunk_tokens) {
   return L;
 }
 
-// Block norms.
+// Block norms and the orthogonalised update.
 bool valid_dtype(int t) { return t >= SLM_BF16 && t <= SLM_F32; }
 size_t elem_bytes(int t) { return t == SLM_F32 ? 4 : 2; }
 bool finite(float v) { return v == v && v <= 3.4e38f && v >= -3.4e38f; }
@@ -615,6 +615,11 @@ int orth_plan(OrthChain* ch, int64_t m, int64_t n, int64_t batch) {
   } while (0)
 
 }  // namespace
+}  // namespace slm
+
+namespace slm {
+cudaError_t norm_ran_out(int* flags);  // slm_norm.cu
+cudaError_t orth_ran_out(int* flags);  // slm_orth.cu
 }  // namespace slm
 
 using namespace slm;
@@ -1429,6 +1434,16 @@ int slm_device_status(const void* workspace, void* stream) {
   if (flags & kFlagTimeout) return SLM_ERR_TIMEOUT;
   if (flags & kFlagLabelRange) return SLM_ERR_LABEL_RANGE;
   return SLM_OK;
+}
+
+int slm_operator_status(void* stream) {
+  int st = check_device();
+  if (st != SLM_OK) return st;
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return SLM_ERR_CUDA;
+  int flags = 0;
+  if (norm_ran_out(&flags) != cudaSuccess || orth_ran_out(&flags) != cudaSuccess)
+    return SLM_ERR_CUDA;
+  return flags & kFlagTimeout ? SLM_ERR_TIMEOUT : SLM_OK;
 }
 
 }  // extern "C"

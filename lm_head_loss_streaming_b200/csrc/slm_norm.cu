@@ -11,6 +11,9 @@ cudaError_t norm_fwd_f32(const NormFwd& p, cudaStream_t s);
 cudaError_t norm_bwd_bf16(const NormBwd& p, const DevCtl& c, cudaStream_t s);
 cudaError_t norm_bwd_f16(const NormBwd& p, const DevCtl& c, cudaStream_t s);
 cudaError_t norm_bwd_f32(const NormBwd& p, const DevCtl& c, cudaStream_t s);
+cudaError_t norm_ran_out_bf16(int* flags);
+cudaError_t norm_ran_out_f16(int* flags);
+cudaError_t norm_ran_out_f32(int* flags);
 
 NormPlan norm_plan(int64_t N, int64_t rows_per_gate, bool has_gate, int max_blocks, int batch,
                    int classes) {
@@ -37,6 +40,12 @@ cudaError_t launch_norm_bwd(int dtype, const NormBwd& p, const DevCtl& c, cudaSt
   return dtype == 0   ? norm_bwd_bf16(p, c, s)
          : dtype == 1 ? norm_bwd_f16(p, c, s)
                       : norm_bwd_f32(p, c, s);
+}
+
+cudaError_t norm_ran_out(int* flags) {
+  cudaError_t e = norm_ran_out_bf16(flags);
+  if (e == cudaSuccess) e = norm_ran_out_f16(flags);
+  return e == cudaSuccess ? norm_ran_out_f32(flags) : e;
 }
 
 }  // namespace slm

@@ -25,6 +25,7 @@
 
 #include "slm_internal.h"
 #include "slm_norm_rows.h"
+#include "slm_ran_out.cuh"
 #include "slm_wait.cuh"
 #include "sm100.cuh"
 
@@ -1127,6 +1128,7 @@ __global__ void __launch_bounds__((TPR > kRingThreads ? TPR : kRingThreads) + 32
   }
   __syncthreads();
   if (*abort && warp == 0) {
+    if (lane == 0) record_ran_out();
     // After a wait that ran out: copies in flight land (boundedly) before the block leaves.
     const uint32_t last = rc->issued;
     for (uint32_t q = last > static_cast<uint32_t>(S) ? last - S : 0u; q < last; ++q)

@@ -7,4 +7,5 @@ cudaError_t norm_fwd_bf16(const NormFwd& p, cudaStream_t s) { return fwd_t<__nv_
 cudaError_t norm_bwd_bf16(const NormBwd& p, const DevCtl& c, cudaStream_t s) {
   return bwd_t<__nv_bfloat16>(p, c, s);
 }
+cudaError_t norm_ran_out_bf16(int* flags) { return take_ran_out(flags); }
 }  // namespace slm

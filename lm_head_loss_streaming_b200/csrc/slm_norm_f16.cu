@@ -7,4 +7,5 @@ cudaError_t norm_fwd_f16(const NormFwd& p, cudaStream_t s) { return fwd_t<__half
 cudaError_t norm_bwd_f16(const NormBwd& p, const DevCtl& c, cudaStream_t s) {
   return bwd_t<__half>(p, c, s);
 }
+cudaError_t norm_ran_out_f16(int* flags) { return take_ran_out(flags); }
 }  // namespace slm

@@ -7,4 +7,5 @@ cudaError_t norm_fwd_f32(const NormFwd& p, cudaStream_t s) { return fwd_t<float>
 cudaError_t norm_bwd_f32(const NormBwd& p, const DevCtl& c, cudaStream_t s) {
   return bwd_t<float>(p, c, s);
 }
+cudaError_t norm_ran_out_f32(int* flags) { return take_ran_out(flags); }
 }  // namespace slm

@@ -31,6 +31,7 @@
 #include <type_traits>
 
 #include "slm_internal.h"
+#include "slm_ran_out.cuh"
 #include "slm_wait.cuh"
 #include "sm100.cuh"
 
@@ -945,6 +946,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   cluster_sync();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
+  if (threadIdx.x == 0 && *abort) record_ran_out();
 }
 
 template <int BNI, int NSUB, bool TALL, bool SPLIT>
@@ -1417,6 +1419,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   cluster_sync();
   tc_fence_after();
   if (warp == 0) tmem_dealloc_pair(tmem, 512);
+  if (threadIdx.x == 0 && *abort) record_ran_out();
 }
 
 template <class T, bool BOTH>
@@ -1460,6 +1463,8 @@ cudaError_t launch_orth_small(int dtype, const OrthSmall& p, int64_t batch, cons
   if (dtype == 1) return run(__half{});
   return run(float{});
 }
+
+cudaError_t orth_ran_out(int* flags) { return take_ran_out(flags); }
 
 cudaError_t launch_orth_prep(int dtype, const OrthPrep& p, int64_t batch, cudaStream_t s) {
   auto aligned = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };

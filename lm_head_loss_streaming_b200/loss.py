@@ -378,8 +378,15 @@ def target_flatness(target_hidden, weight):
     return out
 
 
-def device_status(fwd: FwdResult):
-    """Synchronise and return the device status of the last call on this workspace."""
+def device_status(fwd: FwdResult | None = None):
+    """Synchronise and return the device status of the last call on this workspace.
+
+    Without ``fwd``: that of all ``block_norm`` backwards and ``orthogonalize`` calls on the current
+    device since this was last asked (``slm_operator_status``), which do not hand out a workspace.
+    7 (SLM_ERR_TIMEOUT) says that a wait inside one of them ran out; its results are then undefined,
+    a momentum among them, which may have been advanced."""
+    if fwd is None:
+        return _lib.slm_operator_status(_stream())
     return _lib.slm_device_status(_ptr(fwd.workspace), _stream())
 
 

@@ -206,7 +206,7 @@ def block_norm_bwd(fwd: BlockNormResult, x, y=None, w_pre=None, w_post=None, gat
     be None: zero).  ``dx`` and ``dy`` have the inputs' type, ``dgate`` the gate's shape and
     type (summed over the rows that share a gate row), the weights' gradients are float32.
     The sums run in a fixed order.  ``workspace`` may hold a uint8 tensor of
-    ``slm_block_norm_workspace_bytes``."""
+    ``slm_block_norm_workspace_bytes``.  ``device_status()`` tells of waits that ran out."""
     dev, stream = _current(x)
     N, d, dt, ldx, ldy, wt, gt, rows = _check_block(x, y, w_pre, w_post, gate, dev)
     if (w_pre is None) != (d_hidden is None) or (d_hidden is None and d_residual is None):

@@ -45,7 +45,8 @@ def orthogonalize(grad, momentum=None, beta=0.95, nesterov=True, steps=5,
     ``coefficients`` is one (a, b, c), or a sequence of one per step, within the range that
     ``slm_orthogonalize`` documents.  Returns X as a contiguous bf16 tensor of grad's shape
     (``out`` if given).  ``workspace`` may be a uint8 tensor of
-    ``orthogonalize_workspace_bytes``."""
+    ``orthogonalize_workspace_bytes``.  ``device_status()`` tells of waits that ran out: what the
+    call returned is then undefined, and ``momentum`` may have been advanced."""
     if not isinstance(grad, torch.Tensor) or not grad.is_cuda or grad.dim() not in (2, 3):
         raise ValueError("grad must be a 2-D or 3-D CUDA tensor")
     if grad.dtype not in _DTYPE:

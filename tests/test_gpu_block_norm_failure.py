@@ -47,3 +47,33 @@ def test_wait_runs_out_reports_timeout_and_the_next_call_is_right(N, d, dtype, g
     for k, v in want.__dict__.items():
         if isinstance(v, torch.Tensor):
             assert torch.equal(getattr(got, k), v), k
+
+
+@pytest.mark.parametrize("what", ["norm", "norm clusters", "update", "small update"])
+def test_wait_that_ran_out_is_known_without_a_workspace(what):
+    """The default calls and autograd drop their workspace; the device remembers."""
+    from lm_head_loss_streaming_b200 import block_norm, device_status, orthogonalize
+    n, d = (700, 16384) if what == "norm clusters" else (2000, 4096)
+    x, y = (torch.randn(n, d, device="cuda").to(BF).requires_grad_() for _ in range(2))
+    w = torch.ones(d, device="cuda", dtype=BF)
+    side = 200 if what == "small update" else 500
+    g = torch.randn(side, side, device="cuda")
+
+    def call():
+        if "update" in what:
+            orthogonalize(g)
+        else:
+            block_norm(x, y, w_pre=w)[1].sum().backward()
+
+    device_status()                                  # what earlier tests left
+    call()
+    assert device_status() == 0
+    assert _lib.slm_debug_set(1, 100_000_000) == 0   # ~0.05-0.1 s per wait
+    try:
+        call()
+        torch.cuda.synchronize()
+    finally:
+        assert _lib.slm_debug_set(0, 0) == 0
+    call()                                           # a good call after it clears nothing
+    assert device_status() == 7
+    assert device_status() == 0
