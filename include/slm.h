@@ -424,7 +424,8 @@ SLM_API int slm_block_norm_bwd(int dtype, const void* x, int64_t ldx, const void
  *   dtype     slm_dtype of grad.
  *   grad      [batch, m, n]: ld elements from row to row (>= n), batch_stride from matrix to
  *             matrix (>= (m - 1) ld + n when batch > 1).  Not written.
- *   momentum  float [batch, m, n] contiguous, updated in place, or NULL.
+ *   momentum  float [batch, m, n] contiguous, updated in place, or NULL.  A call that is refused
+ *             has not touched it.
  *   beta      a double, so that 1 - beta is not the complement of a rounded beta.
  *   coefficients  HOST float [steps][3].  Every value must be finite, and the iteration must
  *             stay within the kernels' fp16 scaling for every X with singular values in [0, 1]:
@@ -462,6 +463,8 @@ SLM_API int slm_operator_status(void* stream);
  * lets its own copies and MMAs finish, frees its tensor memory and returns; results of that
  * call are undefined.  fault_mode 2 makes the GEMMs' CTA pairs give up their loose
  * lockstep at the first wait (it only shapes performance: results must not change).
+ * fault_mode 4 makes slm_orthogonalize's launch whose blocks must all be resident be refused, as
+ * by a device without room for them: the call returns SLM_ERR_CUDA, with nothing enqueued.
  * fault_mode 0 restores normal operation.  timeout_cycles bounds every
  * pipeline wait in SM clock cycles (0 = the default of 4e9, about 2 s).  Process-wide;
  * takes effect at the next launch.  Returns SLM_ERR_SHAPE for an invalid mode or bound. */

@@ -620,6 +620,8 @@ int orth_plan(OrthChain* ch, int64_t m, int64_t n, int64_t batch) {
 namespace slm {
 cudaError_t norm_ran_out(int* flags);  // slm_norm.cu
 cudaError_t orth_ran_out(int* flags);  // slm_orth.cu
+// Whether the device takes launch_orth_chain's launch.
+cudaError_t ready_orth_chain(int bn, bool tall, const OrthChain& ch, const DevCtl& c);
 }  // namespace slm
 
 using namespace slm;
@@ -1350,6 +1352,8 @@ int slm_orthogonalize(int dtype, const void* grad, int64_t ld, int64_t batch_str
   const OrthPrep prep{grad, m, n, ld, batch_stride, L.ldx, momentum, static_cast<float>(beta),
                       static_cast<float>(1.0 - beta), eps, nesterov,
                       reinterpret_cast<double*>(ws + L.sums_off), hi[0], lo, status, ch.counter};
+  // The preparation advances the momentum: the launch after it must not be refused.
+  if (ready_orth_chain(bn, tall, ch, make_ctl(status)) != cudaSuccess) return SLM_ERR_CUDA;
   SLM_LAUNCH(kTrOrth, launch_orth_prep(dtype, prep, batch, s));
   SLM_LAUNCH(kTrOrth, launch_orth_chain(bn, tall, ch, maps, make_ctl(status), s));
   return SLM_OK;
@@ -1416,7 +1420,8 @@ int slm_debug_exp2(const float* x, float* y_fma, float* y_mufu, int64_t n, void*
 }
 
 int slm_debug_set(int fault_mode, long long timeout_cycles) {
-  if (fault_mode < 0 || fault_mode > 2 || timeout_cycles < 0) return SLM_ERR_SHAPE;
+  if (fault_mode < 0 || (fault_mode > 2 && fault_mode != 4) || timeout_cycles < 0)
+    return SLM_ERR_SHAPE;
   g_fault.store(fault_mode);
   g_timeout.store(timeout_cycles > 0 ? timeout_cycles : kTimeoutCycles);
   return SLM_OK;

@@ -949,8 +949,9 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   if (threadIdx.x == 0 && *abort) record_ran_out();
 }
 
+// maps = NULL: only whether the launch would be taken, so that nothing before it is enqueued in vain.
 template <int BNI, int NSUB, bool TALL, bool SPLIT>
-cudaError_t launch_chain(const OrthChain& ch, const OrthMaps& maps, const DevCtl& c,
+cudaError_t launch_chain(const OrthChain& ch, const OrthMaps* maps, const DevCtl& c,
                          cudaStream_t s) {
   using C = OrthCfg<BNI, NSUB>;
   auto kern = orth_chain<BNI, NSUB, TALL, SPLIT>;
@@ -958,6 +959,7 @@ cudaError_t launch_chain(const OrthChain& ch, const OrthMaps& maps, const DevCtl
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (c.fault == 4) return cudaErrorCooperativeLaunchTooLarge;  // test hook
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -981,8 +983,10 @@ cudaError_t launch_chain(const OrthChain& ch, const OrthMaps& maps, const DevCtl
     int n = 0;
     cfg.gridDim = dim3(2 * 512, 1, 1);
     if ((e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg)) != cudaSuccess) return e;
-    max_clusters[dev] = n > 0 ? n : 1;
+    if (n < 1) return cudaErrorCooperativeLaunchTooLarge;
+    max_clusters[dev] = n;
   }
+  if (!maps) return cudaSuccess;
   cfg.numAttrs = 2;
   int pairs = 1;
   for (const OrthGeom& g : ch.geom) pairs = std::max(pairs, g.num_units);
@@ -990,7 +994,7 @@ cudaError_t launch_chain(const OrthChain& ch, const OrthMaps& maps, const DevCtl
   cfg.gridDim = dim3(2 * pairs, 1, 1);
   OrthChain co = ch;
   co.resident = ch.resident && ch.geom[kUpdate].num_units <= pairs;
-  return cudaLaunchKernelEx(&cfg, kern, co, maps, c);
+  return cudaLaunchKernelEx(&cfg, kern, co, *maps, c);
 }
 
 // ----------------------------------------------------------------------------------------
@@ -1493,8 +1497,8 @@ cudaError_t launch_orth_prep(int dtype, const OrthPrep& p, int64_t batch, cudaSt
   return run(float{});
 }
 
-cudaError_t launch_orth_chain(int bn, bool tall, const OrthChain& ch, const OrthMaps& maps,
-                              const DevCtl& c, cudaStream_t s) {
+static cudaError_t orth_chain_call(int bn, bool tall, const OrthChain& ch, const OrthMaps* maps,
+                                   const DevCtl& c, cudaStream_t s) {
   auto run = [&](auto tallc, auto splitc) {
     constexpr bool T = decltype(tallc)::value, S = decltype(splitc)::value;
     return bn == 256 ? launch_chain<256, 1, T, S>(ch, maps, c, s)
@@ -1507,6 +1511,15 @@ cudaError_t launch_orth_chain(int bn, bool tall, const OrthChain& ch, const Orth
                 : launch_chain<256, 2, false, false>(ch, maps, c, s);
   if (ch.geom[kGram].split > 1) return tall ? run(yes, yes) : run(no, yes);
   return tall ? run(yes, no) : run(no, no);
+}
+
+cudaError_t launch_orth_chain(int bn, bool tall, const OrthChain& ch, const OrthMaps& maps,
+                              const DevCtl& c, cudaStream_t s) {
+  return orth_chain_call(bn, tall, ch, &maps, c, s);
+}
+
+cudaError_t ready_orth_chain(int bn, bool tall, const OrthChain& ch, const DevCtl& c) {
+  return orth_chain_call(bn, tall, ch, nullptr, c, nullptr);
 }
 
 }  // namespace slm
