@@ -436,9 +436,17 @@ SLM_API int slm_block_norm_bwd(int dtype, const void* x, int64_t ldx, const void
  *   workspace at least slm_orthogonalize_workspace_bytes(batch, m, n) bytes, 256-byte aligned;
  *             its first word is the status word that slm_device_status reads.
  * The products' operands are fp16 with fp32 accumulators; X is kept to 22 bits and the
- * diagonals of A and B in fp32, so that the result is within about 2.2e-3 (Frobenius,
- * relative) of the exact iteration on grad, the bf16 rounding of out (1.7e-3) included.  A matrix of
- * zeros gives zeros; one with a NaN or an infinity gives NaN throughout, and no other matrix of
+ * diagonals of A and B in fp32.  Off the exact iteration on grad (Frobenius, relative), the bf16
+ * rounding of out (1.7e-3) included, with the coefficients above:
+ *     five steps      2.5e-3   (4e-3 where a side is below 32)
+ *     ten steps       5e-3
+ *     sixteen steps   3e-2
+ * The last two are for gradients of full rank with both sides 32 or more.  Directions that a
+ * gradient does not hold are filled by rounding, about 1e-7 of the others, and every step
+ * multiplies them by its a until they count as directions: ten of these steps (3.4^10 = 2.4e5)
+ * bring them to 3e-2, twelve to 2e-1, sixteen to singular values of 1.  The iteration in fp32 does
+ * the same (5e-3, 6e-2 and 1), as does any; so does a side below 32.  Nothing is refused for it.
+ * A matrix of zeros gives zeros; one with a NaN or an infinity gives NaN throughout, and no other matrix of
  * the stack is touched by it.  Matrices with ||u||_F far below eps lose relative precision
  * (their X is below 2^-28), and elements below 2^-126 count as zeros.  batch, m or n = 0:
  * nothing is done.

@@ -9,7 +9,9 @@
 // Number formats.  The products run on the tensor cores with fp16 operands (11-bit
 // significands; bf16's 8 bits lose 1e-2 to 3e-1 of the result here, because the steps
 // multiply small singular directions, and with them the rounding noise, by up to a^steps) and
-// fp32 accumulators.  Three choices keep the result within about 1e-3 of the exact iteration:
+// fp32 accumulators.  Three choices keep the result of five steps within about 1.4e-3 of the exact
+// iteration (a later step adds 2e-4 to 3e-4; directions that the gradient lacks hold rounding noise,
+// which the product of the steps' a multiplies, as in fp32):
 //   - X is held as hi + lo, two fp16 numbers (22 bits).  Products use hi; the term a X, which
 //     carries the small singular directions through, uses both.
 //   - A and B are held as a diagonal in fp32 and fp16 off-diagonal entries (zero diagonal).
