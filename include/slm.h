@@ -429,8 +429,9 @@ SLM_API int slm_block_norm_bwd(int dtype, const void* x, int64_t ldx, const void
  *   beta      a double, so that 1 - beta is not the complement of a rounded beta.
  *   coefficients  HOST float [steps][3].  Every value must be finite, and the iteration must
  *             stay within the kernels' fp16 scaling for every X with singular values in [0, 1]:
- *             all iterates' singular values at most 1.9 and |b s^2 + c s^4| at most 15, else
- *             SLM_ERR_KIND.  (3.4445, -4.7750, 2.0315), five times, stays below 1.21 and 2.81.
+ *             all iterates' singular values at most 1.995 and |b s^2 + c s^4| at most 15, else
+ *             SLM_ERR_KIND.  (3.4445, -4.7750, 2.0315), five times, stays below 1.21 and 2.81;
+ *             schedules of a polynomial per step whose iterates reach 1.99 are taken.
  *   steps     1 to 64.
  *   out       bf16 [batch, m, n] contiguous; overlaps neither grad nor momentum.
  *   workspace at least slm_orthogonalize_workspace_bytes(batch, m, n) bytes, 256-byte aligned;

@@ -498,22 +498,36 @@ bool orth_sizes_ok(int64_t batch, int64_t m, int64_t n) {
 }
 
 // Whether the iteration keeps every X with singular values in [0, 1] within the kernels' fp16
-// scaling (see slm_orth.cu); the polynomials are sampled, with 1% to spare between samples.
+// scaling (see slm_orth.cu).  The largest |s (a + b s^2 + c s^4)| over [0, most] is at the end or
+// where a + 3 b t + 5 c t^2 = 0, t = s^2; the largest |b t + c t^2| at the end or t = -b / 2c.
 bool orth_coefficients_ok(const float* co, int steps) {
   double most = 1.0;
   for (int i = 0; i < steps; ++i) {
     const double a = co[3 * i], b = co[3 * i + 1], c = co[3 * i + 2];
     if (!finite(co[3 * i]) || !finite(co[3 * i + 1]) || !finite(co[3 * i + 2])) return false;
+    const double end = most * most;
     double next = 0.0, bmax = 0.0;
-    constexpr int kSamples = 1024;
-    for (int q = 0; q <= kSamples; ++q) {
-      const double s = most * q / kSamples, l = s * s;
-      const double pb = b * l + c * l * l;
+    auto see = [&](double t) {
+      if (!(t > 0.0 && t <= end)) return;
+      const double pb = b * t + c * t * t;
       bmax = std::max(bmax, std::abs(pb));
-      next = std::max(next, std::abs(s * (a + pb)));
+      next = std::max(next, std::abs(std::sqrt(t) * (a + pb)));
+    };
+    see(end);
+    if (c != 0.0) see(-b / (2.0 * c));
+    if (c != 0.0) {
+      const double disc = 9.0 * b * b - 20.0 * a * c;
+      if (disc >= 0.0) {
+        // Both roots without cancellation: q / (5 c) and a / q.
+        const double q = -0.5 * (3.0 * b + std::copysign(std::sqrt(disc), b));
+        see(q / (5.0 * c));
+        if (q != 0.0) see(a / q);
+      }
+    } else if (b != 0.0) {
+      see(-a / (3.0 * b));
     }
-    most = 1.01 * next;
-    if (!(most <= 1.9) || !(bmax <= 15.0)) return false;
+    most = next;
+    if (!(most <= 1.995) || !(bmax <= 15.0)) return false;
   }
   return true;
 }
