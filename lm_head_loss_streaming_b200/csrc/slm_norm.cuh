@@ -1160,6 +1160,12 @@ struct RowFit {
   }
   bool shifted() const { return shift0 != 0 || d % elems != 0; }
 };
+// Row classes: after this many rows the distance to the 16-byte boundary comes round again.
+inline int row_classes(int64_t N, int64_t d, int elems, bool shift) {
+  int classes = 1;
+  while (shift && N > 1 && classes * d % elems != 0) classes *= 2;
+  return classes;
+}
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 template <class T, int NV, bool WARP>
@@ -1244,10 +1250,8 @@ cudaError_t bwd_ring_t(NormBwd p, const DevCtl& c, int cs, cudaStream_t s) {
     if ((e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg)) != cudaSuccess) return e;
     most = n > 0 ? n : 1;
   }
-  // Row classes: after `classes` rows the distance to the 16-byte boundary comes round again.
   constexpr int E = Piece<T>::kElems;
-  int classes = 1;
-  while (SHIFT && p.N > 1 && classes * p.d % E != 0) classes *= 2;
+  const int classes = row_classes(p.N, p.d, E, SHIFT);
   p.plan = norm_plan(p.N, p.rows_per_gate, p.gate != nullptr, std::min(most, kNormBlocks), C::kRows,
                      classes);
   const int nvec = static_cast<int>(SHIFT ? (p.d + 2 * E - 2) / E : p.d / E);
@@ -1298,8 +1302,10 @@ cudaError_t bwd_t(NormBwd p, const DevCtl& c, cudaStream_t s) {
                      !aligned16(p.gate) || !aligned16(p.dgate);
   // Pieces of 8 fp32 gates start on 16-byte boundaries where those of the rows do.
   if (wide) fit.ok = fit.ok && fit.shift0 == 0 && aligned16(p.gate) && aligned16(p.dgate);
-  // A shared gate with more groups than can be split by row class is left to the general path.
-  if (shift && p.plan.shared_gate) fit.ok = fit.ok && p.plan.groups * E <= kNormBlocks;
+  // A shared gate with more groups than can be split by row class (each class of each group has a
+  // worker of its own) is left to the general path.
+  const int classes = row_classes(p.N, p.d, E, shift);
+  if (classes > 1 && p.plan.shared_gate) fit.ok = fit.ok && p.plan.groups * classes <= kNormBlocks;
   const int64_t nvec = shift ? (p.d + 2 * E - 2) / E : p.d / E;  // the most that a row has
   if (fit.ok && norm_ring_takes(p.d, E) && nvec <= 2 * kRingThreads * kMaxCluster) {
     p.shift0 = static_cast<int>(fit.shift0);
