@@ -1128,12 +1128,14 @@ __global__ void __launch_bounds__((TPR > kRingThreads ? TPR : kRingThreads) + 32
   }
   __syncthreads();
   if (*abort && warp == 0) {
-    if (lane == 0) record_ran_out();
     // After a wait that ran out: copies in flight land (boundedly) before the block leaves.
     const uint32_t last = rc->issued;
     for (uint32_t q = last > static_cast<uint32_t>(S) ? last - S : 0u; q < last; ++q)
       wait_warp(&rc->full[q % S], (q / S) & 1u, abort, ctl, false);
   }
+  // By the copying warp: in warp 0's branch above it changed ptxas's schedule of the loop (16384 x 4096
+  // bf16 167 us, not 155).
+  if (*abort && threadIdx.x == kThreads) record_ran_out();
   // No block leaves while another of its cluster may still write its sums into it: one whose waits
   // all ended has received every sum; to one that gave up, those sent before the barrier may still
   // be on their way, which takes microseconds.
