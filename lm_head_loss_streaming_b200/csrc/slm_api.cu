@@ -458,8 +458,17 @@ struct OrthLayout {
 
 int orth_plan(OrthChain* ch, int64_t m, int64_t n, int64_t batch);
 
+// Matrices that a CTA pair works in shared and tensor memory: of the workspace they use the status
+// word only.
+bool orth_is_small(int64_t m, int64_t n) { return m <= kOrthSmall && n <= kOrthSmall; }
+constexpr size_t kOrthSmallWorkspace = 4096;
+
 OrthLayout orth_layout(int64_t batch, int64_t m, int64_t n) {
   OrthLayout L{};
+  if (orth_is_small(m, n)) {
+    L.total = kOrthSmallWorkspace;
+    return L;
+  }
   L.k = std::min(m, n);
   L.ldx = static_cast<int64_t>(align_up(static_cast<size_t>(n), 8));
   L.ldk = static_cast<int64_t>(align_up(static_cast<size_t>(L.k), 8));
@@ -1303,14 +1312,7 @@ int slm_orthogonalize(int dtype, const void* grad, int64_t ld, int64_t batch_str
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   int* status = reinterpret_cast<int*>(ws + L.status_off);
-  __half* hi[2] = {reinterpret_cast<__half*>(ws + L.hi_off[0]),
-                   reinterpret_cast<__half*>(ws + L.hi_off[1])};
-  __half* lo = reinterpret_cast<__half*>(ws + L.lo_off);
-  __half* mat[2] = {reinterpret_cast<__half*>(ws + L.a_off[0]),
-                    reinterpret_cast<__half*>(ws + L.a_off[1])};
-  float* diag[2] = {reinterpret_cast<float*>(ws + L.diag_off[0]),
-                    reinterpret_cast<float*>(ws + L.diag_off[1])};
-  if (m <= kOrthSmall && n <= kOrthSmall) {
+  if (orth_is_small(m, n)) {
     OrthSmall p{grad, ld, batch_stride, momentum, static_cast<float>(beta),
                 static_cast<float>(1.0 - beta), eps, nesterov, static_cast<int>(m),
                 static_cast<int>(n), steps, static_cast<__nv_bfloat16*>(out), {}};
@@ -1318,6 +1320,13 @@ int slm_orthogonalize(int dtype, const void* grad, int64_t ld, int64_t batch_str
     SLM_LAUNCH(kTrOrth, launch_orth_small(dtype, p, batch, make_ctl(status), s));
     return SLM_OK;
   }
+  __half* hi[2] = {reinterpret_cast<__half*>(ws + L.hi_off[0]),
+                   reinterpret_cast<__half*>(ws + L.hi_off[1])};
+  __half* lo = reinterpret_cast<__half*>(ws + L.lo_off);
+  __half* mat[2] = {reinterpret_cast<__half*>(ws + L.a_off[0]),
+                    reinterpret_cast<__half*>(ws + L.a_off[1])};
+  float* diag[2] = {reinterpret_cast<float*>(ws + L.diag_off[0]),
+                    reinterpret_cast<float*>(ws + L.diag_off[1])};
   const bool tall = m > n;
   const int64_t k = L.k;
   OrthChain ch{};
