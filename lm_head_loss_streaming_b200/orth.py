@@ -21,12 +21,16 @@ def orthogonalize_workspace_bytes(batch, m, n):
 def _steps(coefficients, steps):
     """One (a, b, c) per step, from one triple for all steps or one each."""
     try:
+        n = int(steps)
+    except (TypeError, ValueError):
+        n = 0
+    if n < 1 or n > 64 or n != steps:
+        raise ValueError(f"steps must be a whole number from 1 to 64, not {steps}")
+    try:
         rows = [tuple(float(v) for v in c) for c in coefficients]
     except TypeError:
-        rows = [tuple(float(v) for v in coefficients)] * int(steps)
-    if int(steps) < 1 or int(steps) > 64:
-        raise ValueError(f"steps must be 1 to 64, not {steps}")
-    if len(rows) != int(steps) or any(len(r) != 3 for r in rows):
+        rows = [tuple(float(v) for v in coefficients)] * n
+    if len(rows) != n or any(len(r) != 3 for r in rows):
         raise ValueError("coefficients must be one (a, b, c) or one for each step")
     return rows
 
