@@ -466,8 +466,10 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
 // Forward by 16-byte pieces: each row is read once into the registers
 // of its threads (NV pieces of x and of y each), and r and h are written from there.  A row is a
 // block's, as many warps as it has pieces for, or, if short (WARP), one warp's of four.  Bound by
-// memory: x and y in, r and h out.  16384 x 4096 bf16 85 us, 6.3 TB/s; rows that are not 16-byte aligned take
-// masks per element too, which bound 16-bit ones (16384 x 1001 fp32 67 us, 16384 x 4097 bf16 221).  One row of 4096 takes 2.9 us.
+// memory: x and y in, r and h out.  16384 x 4096 bf16 85 us, 6.3 TB/s.  Rows that are not 16-byte
+// aligned also align the parameters of every piece of every row and mask its elements, which bounds
+// 16-bit ones (16384 x 4097 bf16 222 us, 2.4 TB/s; 16384 x 1001 fp32 with a gate per token, five
+// arrays, 67 us, 4.9 TB/s).  One row of 4096 takes 2.9 us.
 template <class T, int NV, bool WARP, bool SHIFT>
 __global__ void __launch_bounds__(WARP ? 128 : NV == 2 ? 512 : 1024) norm_fwd_vec(const NormFwd p) {
   using P = Piece<T>;
@@ -595,7 +597,7 @@ __global__ void __launch_bounds__(WARP ? 128 : NV == 2 ? 512 : 1024) norm_fwd_ve
 // Sweep 1 over a batch forms the rows' three sums, sweep 2 the outputs, both from the ring.
 // Sweep 1 runs one batch ahead, so that the sums are exchanged behind sweep 2 of the batch
 // before: at most one block barrier per batch, and a cluster's exchange is off the critical path.
-// Bound by memory for fp32 (8192 x 4096 134 us, 6.0 TB/s), by instructions for 16-bit rows
+// Bound by memory for fp32 (8192 x 4096 136 us, 5.9 TB/s), by instructions for 16-bit rows
 // (16384 x 4096 bf16 155 us, 5.2 TB/s: twice the conversions and arithmetic per byte, between
 // dependent reads of shared memory).  The general kernels, which read global memory twice, take
 // 1778 us there; sweeps in step, without the batch between them, took 207.
@@ -1271,7 +1273,7 @@ cudaError_t bwd_ring(const NormBwd& p, const DevCtl& c, int cs, cudaStream_t s) 
 // Threads per row: as few as keep two pieces each, so that a batch has many rows and few threads
 // share a sum (256 threads for every row: 65536 x 256 bf16 379 us instead of 70, 16384 x 2048 114
 // instead of 85).  One block for a row as long as its registers and ring do (4096 x 5120 62 us, in
-// clusters of two 94; 16384 x 4096 155 and 290), then as few blocks as that leaves (8192 x 16384 409
+// clusters of two 94; 16384 x 4096 155 and 290), then as few blocks as that leaves (8192 x 16384 396
 // us in clusters of four, 689 of eight).
 template <class T, int GATE, bool SHIFT>
 cudaError_t bwd_vec(const NormBwd& p, int64_t nvec, const DevCtl& c, cudaStream_t s) {

@@ -1,4 +1,4 @@
-// slm_wait.cuh - the bounded pipeline wait shared by the GEMM kernels.
+// slm_wait.cuh - the bounded pipeline wait shared by the GEMM kernels and the block norm's ring.
 #pragma once
 
 #include "slm_internal.h"
